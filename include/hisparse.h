@@ -14,6 +14,12 @@
  *   hs_sparse_mla_decode  attention over only those rows               [P2 footnote 1]
  *   hs_offload_pages      copy completed pages of all layers to host   [P1 "How it works"]
  *
+ * and what a prefill or a dense decode of the same cache needs, one layer at a time:
+ *
+ *   hs_append_quantized   quantise a layer's new KV rows and index keys into the cache
+ *   hs_read_rows          read cached rows and index keys back as values
+ *   hs_chunk_attention    attention of new tokens over every cached row below their limit
+ *
  * Conventions
  * - Every call returns an hs_status. No C++ exception crosses the ABI.
  * - Every call opens an NVTX range named after it (inert unless a profiler is
@@ -299,6 +305,96 @@ hs_status hs_sparse_mla_decode(hs_pool* pool, int32_t layer, int32_t n_tokens,
  *  d_pool_pages [n] int32, d_host_pages [n] int64. */
 hs_status hs_offload_pages(hs_pool* pool, int32_t n, const int32_t* d_pool_pages,
                            const int64_t* d_host_pages, hs_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Prefill and dense decode (graph-capturable). These calls wait for the previous
+ * kernel of the stream before they read anything, and let no later kernel start
+ * before they end, so their inputs may come from, and their outputs go to, any call.
+ * The pool's device must be current (HS_ERR_INVALID otherwise). They use none of the
+ * pool's scratch and are not bounded by max_tokens or max_q_per_req.
+ * ------------------------------------------------------------------------- */
+
+/* Element types of the values these calls read and write. */
+#define HS_BF16 0
+#define HS_FP16 1
+#define HS_FP32 2
+
+/* Quantise the new rows of one layer as they are written: n_tokens KV rows of `layer`
+ * and index keys of its indexer group (layer / layers_per_indexer).
+ *  d_req, d_pos  [n] request slot and position of each token. req -1 skips the token
+ *                (padding). A position given twice in adjacent tokens is written once, from
+ *                the later one; otherwise a position may occur once per call.
+ *  dtype         element type of the three inputs: HS_BF16, HS_FP16 or HS_FP32.
+ *  d_latent, d_rope  [n, 512] and [n, 64], both or neither (NULL). Per 128 latent values:
+ *                scale = amax / 448 (1 when all are zero), code = the e4m3 value nearest to
+ *                x / scale, ties to even; rope is rounded to bf16.
+ *  d_keys        nullable [n, 128]. HS_IDX_FP8: the same with one scale per key.
+ *                HS_IDX_INT8: x / key_scale rounded to the nearest integer, ties to even,
+ *                clamped to +-127; key_scale (a normal positive fp32) is used for this
+ *                format only.
+ *  ld_*          elements from one token's values to the next (>= the width); each base
+ *                16-byte aligned, each stride a multiple of 16 bytes.
+ * The page holding each position must be resident (HS_ERR_BAD_ID otherwise, and that part
+ * of that token is not written). A NaN is written as 0 and an infinity as the largest value
+ * of its format with the group's scale taken from its finite values; both set
+ * HS_ERR_RANGE. */
+hs_status hs_append_quantized(hs_pool* pool, int32_t layer, int32_t n_tokens, const int32_t* d_req,
+                              const int32_t* d_pos, int32_t dtype, const void* d_latent, int64_t ld_latent,
+                              const void* d_rope, int64_t ld_rope, const void* d_keys, int64_t ld_keys,
+                              float key_scale, hs_stream_t stream);
+
+/* Read cached positions of one layer back as values: code * scale in fp32, rounded once to
+ * dtype. d_req, d_pos, dtype, ld_* and key_scale as for hs_append_quantized; d_latent
+ * [n, 512], d_rope [n, 64] and d_keys [n, 128] are outputs, any of them NULL. A row whose
+ * page is a placeholder is read from its host copy; one that has neither sets
+ * HS_ERR_HOST_MISSING and leaves that token's outputs as they were, as a bad id
+ * (HS_ERR_BAD_ID) and req -1 do. The outputs must not overlap. */
+hs_status hs_read_rows(hs_pool* pool, int32_t layer, int32_t n_tokens, const int32_t* d_req, const int32_t* d_pos,
+                       int32_t dtype, void* d_latent, int64_t ld_latent, void* d_rope, int64_t ld_rope,
+                       void* d_keys, int64_t ld_keys, float key_scale, hs_stream_t stream);
+
+/* Most segments and tokens of one hs_chunk_attention call. */
+#define HS_CHUNK_MAX_SEGMENTS 4096
+#define HS_CHUNK_MAX_TOKENS 65536
+
+/* Bytes of device workspace that hs_chunk_attention needs on this pool's device, whatever
+ * the call's sizes. */
+hs_status hs_chunk_workspace(const hs_pool* pool, int64_t* bytes);
+
+/* Attention of new tokens over the paged cache of one layer (MQA form, [P2] footnote 1):
+ * per token j and head h, over every position t < limit_j of the token's request,
+ *   z_t = sm_scale * q . k_t over the 576 dims, out = softmax(z) . v over the 512 latent
+ * dims, lse = log sum exp z. A prefill chunk appends its rows (hs_append_quantized), then
+ * attends with limit_j = pos_j + 1; a decode is a segment of one token.
+ *  d_seg_req, d_seg_start  [n_segments] and [n_segments + 1]: segment i is the tokens
+ *               [start_i, start_(i+1)) of request req_i, 0 <= start_0, ascending, the last
+ *               at most n_tokens. A segment may be empty. Tokens outside every segment are
+ *               left alone. A start out of order or range sets HS_ERR_BAD_ID and is clamped.
+ *  d_limit      [n_tokens] int32, 0 <= limit <= max_ctx, in any order. A token of limit 0
+ *               gets out 0 and lse -inf, and so does one of a bad request or limit
+ *               (HS_ERR_BAD_ID).
+ *  dtype        of q and out: HS_BF16 or HS_FP16.
+ *  d_q, d_out   element (j, h, d) at j * stride_token + h * stride_head + d; d < 576 for q,
+ *               < 512 for out. 16-byte aligned, strides multiples of 8 elements (q: >= 0;
+ *               out: >= 512, no two rows overlapping).
+ *  d_lse        nullable [n_tokens, H] fp32.
+ *  d_work       at least hs_chunk_workspace bytes, 16-byte aligned, used by this call
+ *               alone from its start to its end: calls on one stream may share it, calls
+ *               (or graphs) that may overlap may not. Its contents do not matter.
+ * Rows of placeholder pages are read from the host copy through the mapping, once for every
+ * 128 / H tokens that see them; a page with neither sets HS_ERR_HOST_MISSING and counts as
+ * not seen. The cache may hold anything at positions that no token of the call sees.
+ * Precision: z from exact products of the codes in fp32 (q rounded to fp16 where it is
+ * bf16: exact from 2^-14 to 65504), softmax statistics fp32, P fp16 with 11 significant
+ * bits down to 2^-21 of its row's largest, v = code * scale rounded once to fp16 (an
+ * absolute 2^-25 below 2^-14). Limits: |scale| below 146, rope and q below 65504 in
+ * magnitude, no e4m3 NaN code. Beyond them HS_ERR_RANGE is set; such a cached value counts
+ * as 0 for every token that sees its row. */
+hs_status hs_chunk_attention(hs_pool* pool, int32_t layer, int32_t n_segments, const int32_t* d_seg_req,
+                             const int32_t* d_seg_start, int32_t n_tokens, const int32_t* d_limit, int32_t dtype,
+                             const void* d_q, int64_t q_stride_token, int64_t q_stride_head, float sm_scale,
+                             void* d_out, int64_t out_stride_token, int64_t out_stride_head, float* d_lse,
+                             void* d_work, int64_t work_bytes, hs_stream_t stream);
 
 /* hs_indexer_topk for callers that cannot allocate device memory. The pages have
  * no counterpart; this is a deployment variant of the call above.

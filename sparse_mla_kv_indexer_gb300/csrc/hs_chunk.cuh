@@ -1,0 +1,47 @@
+// Shared by the cache operators of prefill (hs_cache.cu, hs_chunk.cu): element types and
+// the place of a request's page.
+#pragma once
+
+#include "hs_internal.cuh"
+
+namespace hs {
+
+inline int dtype_size(int32_t dtype) {
+  return dtype == HS_BF16 || dtype == HS_FP16 ? 2 : dtype == HS_FP32 ? 4 : 0;
+}
+// The pool's metadata lives on its own device, and launches go to the current one.
+inline bool on_pool_device(const hs_pool* p) {
+  int dev = -1;
+  return cudaGetDevice(&dev) == cudaSuccess && dev == p->device;
+}
+
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <typename T>
+__device__ __forceinline__ T from_f32(float x);
+template <>
+__device__ __forceinline__ float from_f32<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ __half from_f32<__half>(float x) { return __float2half_rn(x); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+
+// The 64 rows of logical page `page` (0 <= page < max_pages) of request r in `layer`: the
+// pool page when it is resident, else its host copy through the mapping, else null with
+// *err set.
+__device__ __forceinline__ const uint8_t* page_rows(const Dev& D, int layer, int r, int page, int* err) {
+  const size_t at = (size_t)r * D.max_pages + page;
+  const int pg = D.bt[at];
+  if (pg >= 0) {
+    if (pg < D.num_pages) return D.kv[layer] + (size_t)pg * PAGE * ROW;
+    *err = HS_ERR_BAD_ID;
+    return nullptr;
+  }
+  const int64_t hp = D.host_pg[at];
+  if (hp >= 0 && hp < D.host_pages) return D.host + ((size_t)hp * D.n_layers + layer) * PAGE * ROW;
+  *err = hp < 0 ? HS_ERR_HOST_MISSING : HS_ERR_BAD_ID;
+  return nullptr;
+}
+
+}  // namespace hs

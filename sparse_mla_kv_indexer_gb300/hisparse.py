@@ -48,8 +48,13 @@ class Counters(ctypes.Structure):
                [("reserved", ctypes.c_uint64 * 3)]
 
 
+BF16, FP16, FP32 = 0, 1, 2   # HS_BF16, HS_FP16, HS_FP32
+CHUNK_MAX_SEGMENTS = 4096    # HS_CHUNK_MAX_SEGMENTS
+CHUNK_MAX_TOKENS = 65536     # HS_CHUNK_MAX_TOKENS
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int32
+_L = ctypes.c_int64
 _SIGS = {
     "hs_pool_config_check": [ctypes.POINTER(PoolConfig)],
     "hs_pool_init": [ctypes.POINTER(PoolConfig), ctypes.POINTER(_P), ctypes.POINTER(_P), _P, ctypes.POINTER(_P)],
@@ -65,6 +70,10 @@ _SIGS = {
     "hs_replay_topk": [_P, _I, _I, _P, _P, _P, _P],
     "hs_sparse_mla_decode": [_P, _I, _I, _P, _P, ctypes.c_float, _P, _P, _P],
     "hs_offload_pages": [_P, _I, _P, _P, _P],
+    "hs_append_quantized": [_P, _I, _I, _P, _P, _I, _P, _L, _P, _L, _P, _L, ctypes.c_float, _P],
+    "hs_read_rows": [_P, _I, _I, _P, _P, _I, _P, _L, _P, _L, _P, _L, ctypes.c_float, _P],
+    "hs_chunk_workspace": [_P, ctypes.POINTER(_L)],
+    "hs_chunk_attention": [_P, _I, _I, _P, _P, _I, _P, _I, _P, _L, _L, ctypes.c_float, _P, _L, _L, _P, _P, _L, _P],
     "hs_get_error": [_P, ctypes.POINTER(ctypes.c_int), _P],
     "hs_set_select_mode": [_P, _I],
     "hs_select_selftest": [_P, _I, _P, _P, _P],
@@ -107,6 +116,11 @@ def _stream(stream) -> Optional[int]:
     return stream.cuda_stream
 
 
+def _current_device() -> int:
+    import torch
+    return torch.cuda.current_device() if torch.cuda.is_available() else -1
+
+
 def _check(name: str, st: int) -> None:
     if st != 0:
         raise HisparseError(name, st)
@@ -117,6 +131,37 @@ def _host_array(values, ctype):
         return None
     arr = (ctype * len(values))(*[int(v) for v in values])
     return ctypes.cast(arr, _P), arr
+
+
+def _dtype(t) -> int:
+    import torch
+    code = {torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32}.get(t.dtype)
+    if code is None:
+        raise ValueError(f"element type {t.dtype}: bfloat16, float16 or float32 is wanted")
+    return code
+
+
+def _ids(name: str, t, n: int, device: int) -> int:
+    """The address of an int32 array of n elements."""
+    if t.dim() != 1 or t.shape[0] != n or t.element_size() != 4 or t.is_floating_point() or not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous int32 tensor of {n} elements is wanted")
+    _on(name, t, device)
+    return t.data_ptr()
+
+
+def _on(name: str, t, device: int) -> None:
+    if t.get_device() != device:
+        raise ValueError(f"{name}: on {t.device}, the pool is on cuda:{device}")
+
+
+def _values(name: str, t, n: int, width: int, dtype: int, device: int):
+    """Address and row stride of [n, width] values whose last dimension is contiguous."""
+    if t is None:
+        return None, 0
+    if t.dim() != 2 or t.shape[0] != n or t.shape[1] != width or t.stride(1) != 1 or _dtype(t) != dtype:
+        raise ValueError(f"{name}: a [{n}, {width}] tensor of the call's element type is wanted, last stride 1")
+    _on(name, t, device)
+    return t.data_ptr(), t.stride(0) if n > 1 else width
 
 
 def config_ok(cfg: PoolConfig) -> bool:
@@ -137,6 +182,7 @@ class Pool:
     def __init__(self, cfg: PoolConfig, kv_layers: Sequence, idx_layers: Sequence, host_kv):
         self.cfg = cfg
         self._keep = (list(kv_layers), list(idx_layers), host_kv)
+        self.device = _current_device()
         kv = (_P * len(kv_layers))(*[_ptr(t) for t in kv_layers])
         ix = (_P * len(idx_layers))(*[_ptr(t) for t in idx_layers])
         handle = _P()
@@ -210,6 +256,59 @@ class Pool:
     def offload_pages(self, pool_pages, host_pages, stream=None) -> None:
         _check("hs_offload_pages", lib.hs_offload_pages(self.handle, pool_pages.numel(), _ptr(pool_pages),
                                                         _ptr(host_pages), _stream(stream)))
+
+    # -- prefill and dense decode, one layer at a time ---------------------------------
+    def _cache_args(self, req, pos, latent, rope, keys):
+        first = next((t for t in (latent, rope, keys) if t is not None), None)
+        if first is None:
+            raise ValueError("none of latent, rope and keys is given")
+        n, dtype, dev = req.shape[0], _dtype(first), self.device
+        return (n, _ids("req", req, n, dev), _ids("pos", pos, n, dev), dtype,
+                *_values("latent", latent, n, 512, dtype, dev), *_values("rope", rope, n, 64, dtype, dev),
+                *_values("keys", keys, n, 128, dtype, dev))
+
+    def append_quantized(self, layer: int, req, pos, latent=None, rope=None, keys=None, key_scale: float = 1.0,
+                         stream=None) -> None:
+        """Quantise new rows of one layer into the cache: latent [n, 512] and rope [n, 64]
+        (both or neither), index keys [n, 128]; bf16, fp16 or fp32, rows may be strided.
+        key_scale: the step of int8 index keys."""
+        _check("hs_append_quantized", lib.hs_append_quantized(
+            self.handle, layer, *self._cache_args(req, pos, latent, rope, keys), key_scale, _stream(stream)))
+
+    def read_rows(self, layer: int, req, pos, latent=None, rope=None, keys=None, key_scale: float = 1.0,
+                  stream=None) -> None:
+        """Read cached positions of one layer back into latent [n, 512], rope [n, 64] and
+        keys [n, 128] (any of them), in their element type."""
+        _check("hs_read_rows", lib.hs_read_rows(
+            self.handle, layer, *self._cache_args(req, pos, latent, rope, keys), key_scale, _stream(stream)))
+
+    def chunk_workspace_bytes(self) -> int:
+        """Bytes of device workspace that chunk_attention needs, whatever the call's sizes."""
+        n = _L(0)
+        _check("hs_chunk_workspace", lib.hs_chunk_workspace(self.handle, ctypes.byref(n)))
+        return n.value
+
+    def chunk_attention(self, layer: int, seg_req, seg_start, limit, q, sm_scale: float, out, work, lse=None,
+                        stream=None) -> None:
+        """Attention of new tokens over every cached row below their limits. Segment i is the
+        tokens [seg_start[i], seg_start[i + 1]) of request seg_req[i]; limit [n]; q [n, H, 576]
+        and out [n, H, 512] bf16 or fp16, the last dimension contiguous; lse [n, H] fp32;
+        work: chunk_workspace_bytes() bytes that no overlapping call uses."""
+        n, segs, heads, dtype, dev = limit.shape[0], seg_req.shape[0], self.cfg.n_heads, _dtype(q), self.device
+        if q.shape != (n, heads, 576) or out.shape != (n, heads, 512) or out.dtype != q.dtype or \
+                q.stride(2) != 1 or out.stride(2) != 1:
+            raise ValueError(f"q [{n}, {heads}, 576] and out [{n}, {heads}, 512] of one type are wanted, last stride 1")
+        if lse is not None and (lse.shape != (n, heads) or _dtype(lse) != FP32 or not lse.is_contiguous()):
+            raise ValueError(f"lse: a contiguous fp32 [{n}, {heads}] tensor is wanted")
+        if not work.is_contiguous():
+            raise ValueError("work: a contiguous tensor is wanted")
+        for name, t in (("q", q), ("out", out), ("work", work)) + ((("lse", lse),) if lse is not None else ()):
+            _on(name, t, dev)
+        _check("hs_chunk_attention", lib.hs_chunk_attention(
+            self.handle, layer, segs, _ids("seg_req", seg_req, segs, dev), _ids("seg_start", seg_start, segs + 1, dev),
+            n, _ids("limit", limit, n, dev), dtype, q.data_ptr(), q.stride(0) if n > 1 else heads * 576, q.stride(1),
+            sm_scale, out.data_ptr(), out.stride(0) if n > 1 else heads * 512, out.stride(1), _ptr(lse),
+            work.data_ptr(), work.numel() * work.element_size(), _stream(stream)))
 
     # -- status --------------------------------------------------------------------
     def get_error(self, stream=None) -> int:
