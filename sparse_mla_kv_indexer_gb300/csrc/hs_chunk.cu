@@ -6,8 +6,40 @@
 // heads. Per token j and head h, over the positions t < limit_j of its request:
 //   z_t = sm_scale * q_jh . k_t,  o = sum_t softmax(z)_t v_t,  lse = log sum_t exp z_t.
 //
-// One warp per (token, head), one pass over the rows with the running maximum and sum of
-// the softmax, in fp32 throughout.
+// Work. A (token, head) pair is a row; a block is 128 rows (128 / H tokens of one segment);
+// a tile is a block against one page of 64 cached rows. The tiles of all blocks, in order,
+// are dealt in equal contiguous ranges to the pairs of SMs, so that one token over a long
+// context and a long prompt both fill the GPU. A range cuts at most two blocks; their parts
+// go to the workspace (fp32 sums, maxima) and chunk_merge_kernel joins them in a fixed
+// order. Every CTA finds its range itself from the segments and limits.
+//
+// Split of a block over a pair. The output of 128 rows is 128 x 512 fp32, all of one SM's
+// tensor memory, with no room for scores; so two CTAs form a pair (tcgen05.mma of
+// cta_group::2, M = 128): each holds 64 rows, 256 columns of tensor memory for their
+// output, and supplies half of each B operand: the keys of half the page for QK, half the
+// output dims for PV. The full rate of M = 128 then needs one copy of Q (64 rows, 72 KB),
+// and shared memory holds two stages of everything else.
+//
+// Roles (448 threads per CTA):
+//   warps 0-3   softmax: thread t has row t % 64 and the keys (in the output: the 128-dim
+//               groups) of half t / 64, the tensor-memory lane t
+//   warp 4      tensor memory; in the pair's first CTA the tcgen05.mma issue for both
+//   warp 5      the pieces (block, pages) of this pair's range, ahead of the other roles
+//   warps 6-13  cache rows -> fp16 operands: loads one tile ahead into registers, then
+//               K: the e4m3 codes of this CTA's 32 rows as fp16 (exact), and the rope;
+//               V: code x scale of all 64 rows for this CTA's two 128-dim groups
+// Tile t:  QK   S_g = Q_g K_g^T for the four 128-value groups and the rope (five
+//               accumulators), so that s = sum_g scale_g S_g + S_rope is exact up to fp32
+//          softmax  running maximum with a lazy rescale (the reference moves when a row
+//               exceeds it by more than 2^8), P = 2^(z - m + 7) in fp16, sums in fp32
+//          PV   O += P V, in tensor memory for the whole piece
+// QK(t+1) is issued before PV(t), so the softmax of one tile runs under the products of
+// its neighbours.
+//
+// Numbers. K codes and bf16 rope are exact in fp16 (rope to 65504); V is code * scale rounded
+// once to fp16 (scale in two fp16 parts); P keeps 11 bits from 2^15 down to 2^-14, that is
+// to 2^-21 of the row's largest (the shift by 2^7 buys seven binades under a dominant row).
+// Scores, maxima, sums and the output accumulate in fp32.
 #include <cuda_fp8.h>
 #include <math.h>
 #include <nvtx3/nvToolsExt.h>
@@ -18,100 +50,956 @@ namespace hs {
 
 namespace {
 
-constexpr int CK_WARPS = 8;
-constexpr float CK_LOG2E = 1.4426950408889634f;
-constexpr float CK_MAX_SCALE = 146.f;   // 448 x scale < 65504
+constexpr int CK_THREADS = 448;
+constexpr int CK_MMA_WARP = 4, CK_PLAN_WARP = 5, CK_CONV_WARP0 = 6;
+constexpr int CK_CONV_WARPS = 8, CK_CONV = CK_CONV_WARPS * 32;
+constexpr int CK_ROWS = 128;       // rows of a block
+constexpr int CK_HALF = 64;        // rows of a block per CTA
+constexpr int CK_MIN_PAGES = 2;    // least pages of a pair's range
+constexpr int CK_RING = 4;         // pieces the planning warp runs ahead
+constexpr int CK_SCL = 4;          // tiles of scales held
+// shared memory
+constexpr int CK_QATOM = CK_HALF * 128;            // 64 rows x 64 dims fp16
+constexpr int CK_KATOM = 32 * 128;                 // 32 keys x 64 dims
+constexpr int CK_VATOM = 64 * 128;                 // 64 keys x 64 dims
+constexpr int CK_KSTAGE = 9 * CK_KATOM;            // 36,864
+constexpr int CK_VSTAGE = 4 * CK_VATOM;            // 32,768
+constexpr int CK_OFF_Q = 0;
+constexpr int CK_OFF_K = 9 * CK_QATOM;
+constexpr int CK_OFF_V = CK_OFF_K + 2 * CK_KSTAGE;
+constexpr int CK_OFF_P = CK_OFF_V + 2 * CK_VSTAGE;
+constexpr int CK_OFF_SCL = CK_OFF_P + CK_HALF * 128;           // float [CK_SCL][4][64]
+constexpr int CK_OFF_RED = CK_OFF_SCL + CK_SCL * 4 * 64 * 4;   // float [2][128]
+constexpr int CK_OFF_RING = CK_OFF_RED + 2 * 128 * 4;          // Piece [CK_RING]
+constexpr int CK_PIECE_BYTES = 48;
+constexpr int CK_OFF_BAR = CK_OFF_RING + CK_RING * CK_PIECE_BYTES;
+enum Bar { B_KF = 0, B_VF = 2, B_PF = 4, B_SD = 6, B_PD = 8, B_SR = 10, B_FIN = 11, B_RF = 12, B_RE = 12 + CK_RING,
+           B_N = 12 + 2 * CK_RING };
+constexpr int CK_OFF_MISC = CK_OFF_BAR + B_N * 8;   // tensor-memory slot, dead flag, plan scalars
+constexpr int CK_SMEM = CK_OFF_MISC + 64 + 1024;
+static_assert(CK_SMEM <= 232448, "shared memory budget");
+// tensor memory: O [2][128 columns], then the five score accumulators of 32 columns
+constexpr uint32_t CK_TM_O = 0, CK_TM_S = 256;
+// the plan's arrays, in the operand buffers before the roles start
+constexpr int CK_PLAN_START = 0;                                        // int [HS_CHUNK_MAX_SEGMENTS + 1]
+constexpr int CK_PLAN_BLK = CK_PLAN_START + (HS_CHUNK_MAX_SEGMENTS + 1) * 4;
+constexpr int CK_MAX_BLOCKS = HS_CHUNK_MAX_SEGMENTS + HS_CHUNK_MAX_TOKENS / 2;
+constexpr int CK_MAX_CHUNKS = (CK_MAX_BLOCKS + CK_THREADS - 1) / CK_THREADS;
+constexpr int CK_PLAN_SUM = CK_PLAN_BLK + (HS_CHUNK_MAX_SEGMENTS + 1) * 4;   // int [CK_MAX_CHUNKS]
+constexpr int CK_PLAN_WARP_TMP = CK_PLAN_SUM + CK_MAX_CHUNKS * 4;       // int [32]
+static_assert(CK_PLAN_WARP_TMP + 32 * 4 <= CK_OFF_SCL, "plan arrays");
 
-__device__ __forceinline__ void values8(uint2 w, float s, float* v) {
-  const uint32_t u[2] = {w.x, w.y};
+constexpr float CK_LOG2E = 1.4426950408889634f;
+constexpr float CK_MAX_SCALE = 146.f;      // 448 x scale < 65504
+constexpr float CK_RESCALE_LOG2 = 8.f;     // the reference maximum moves beyond this
+constexpr float CK_P_SHIFT = 7.f;          // P = 2^(z - m + 7) <= 2^15
+
+// A pair's partial results: for each of its two cut blocks 128 rows of unnormalised
+// outputs and (reference in log2 units, sum); and the block that starts in its range and
+// ends in a later pair's.
+struct ChunkCut {
+  int32_t tok0, n_tok, last_pair, pad;
+};
+struct ChunkWork {
+  ChunkCut* cut;     // [pairs]
+  float2* stats;     // [pairs][2][128]
+  float* part;       // [pairs][2][128][512]
+};
+constexpr int64_t CK_SLOT_ROWS = 2 * CK_ROWS;
+__host__ __device__ inline int64_t work_stats_at(int pairs) { return ((int64_t)pairs * 16 + 255) / 256 * 256; }
+__host__ __device__ inline int64_t work_part_at(int pairs) { return work_stats_at(pairs) + (int64_t)pairs * CK_SLOT_ROWS * 8; }
+inline int64_t work_bytes_for(int pairs) { return work_part_at(pairs) + (int64_t)pairs * CK_SLOT_ROWS * 512 * 4; }
+__host__ __device__ inline ChunkWork work_at(void* base, int pairs) {
+  uint8_t* b = static_cast<uint8_t*>(base);
+  return {reinterpret_cast<ChunkCut*>(b), reinterpret_cast<float2*>(b + work_stats_at(pairs)),
+          reinterpret_cast<float*>(b + work_part_at(pairs))};
+}
+
+struct ChunkArgs {
+  int layer, n_seg, n_tok, pairs;
+  const int32_t *seg_req, *seg_start, *limit;
+  const void* q;
+  long long q_tok, q_head;
+  float scale_log2;
+  void* out;
+  long long o_tok, o_head;
+  float* lse;
+  void* work;
+};
+
+// One block's pages [pg0, pg1) of one pair's range.
+struct Piece {
+  int32_t tok0, n_tok;      // tokens of the block (n_tok -1: no more pieces)
+  int32_t req;              // -1: a bad request, nothing is read
+  int32_t limit;            // the largest limit of the block's tokens
+  int32_t pg0, pg1;
+  int32_t slot;             // -1: the whole block, else the workspace slot 0 or 1
+  int32_t pad[5];
+};
+static_assert(sizeof(Piece) == CK_PIECE_BYTES, "piece size");
+
+// Named barrier over n threads that ORs `flag` across them: a role whose threads saw a wait
+// run out stops as one, and no thread is left behind at a barrier.
+__device__ __forceinline__ bool bar_any(int id, int n, bool flag) {
+  int out;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.s32 p, %1, 0;\n bar.red.or.pred q, %2, %3, p;\n selp.s32 %0, 1, 0, q;\n}"
+      : "=r"(out)
+      : "r"(flag ? 1 : 0), "r"(id), "r"(n)
+      : "memory");
+  return out != 0;
+}
+__device__ __forceinline__ void arrive_local(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// Arrive on a barrier of either CTA of the pair (cluster address), releasing to the cluster.
+__device__ __forceinline__ void arrive_cluster(uint32_t cbar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cbar) : "memory");
+}
+__device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// Bounded wait for a phase, with the ordering of the whole pair: false after `seconds` (or
+// when another role of this CTA gave up), with HS_ERR_TIMEOUT recorded.
+__device__ __noinline__ bool ck_wait_slow(uint32_t bar, uint32_t parity, int32_t* status, volatile int32_t* dead,
+                                          int seconds) {
+  const uint64_t t0 = globaltimer();
+  for (uint32_t it = 1;; ++it) {
+    if (try_wait_cluster(bar, parity)) return true;
+    if ((it & 63u) == 0) {
+      if (*dead) return false;
+      if (globaltimer() - t0 > (uint64_t)seconds * WAIT_NS) {
+        set_status(status, HS_ERR_TIMEOUT);
+        *dead = 1;
+        return false;
+      }
+    }
+  }
+}
+__device__ __forceinline__ bool ck_wait(uint32_t bar, uint32_t parity, int32_t* status, volatile int32_t* dead,
+                                        int seconds = 2) {
+  if (try_wait_cluster(bar, parity)) return true;
+  return ck_wait_slow(bar, parity, status, dead, seconds);
+}
+
+// ---- tcgen05 over the pair -----------------------------------------------------------
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t dst_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols) : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+__device__ __forceinline__ void umma_f16_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                              uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Arrive on the barrier at this offset in both CTAs once every MMA issued so far completes.
+__device__ __forceinline__ void umma_commit_pair(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+      "h"((uint16_t)3)
+      : "memory");
+}
+// The same on this CTA's barrier alone.
+__device__ __forceinline__ void umma_commit_own(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ float ex2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// ---- conversions ----------------------------------------------------------------------
+__device__ __forceinline__ uint32_t h2_bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
+__device__ __forceinline__ __half2 e4m3x2_to_h2(uint32_t two) {
+  return __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3));
+}
+// Bytes 0x7F and 0xFF (NaN) of four codes become zero.
+__device__ __forceinline__ uint32_t drop_nan4(uint32_t w) {
+  const uint32_t m = __vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+  return w & ~m;
+}
+__device__ __forceinline__ bool any_nan(uint4 v) {
+  const uint32_t k = 0x7F7F7F7Fu, one = 0x01010101u;
+  return (((((v.x & k) + one) | ((v.y & k) + one)) | (((v.z & k) + one) | ((v.w & k) + one))) & 0x80808080u) != 0;
+}
+__device__ __forceinline__ void codes_to_f16(uint4 v, uint4& lo, uint4& hi) {
+  lo = make_uint4(h2_bits(e4m3x2_to_h2(v.x & 0xFFFFu)), h2_bits(e4m3x2_to_h2(v.x >> 16)),
+                  h2_bits(e4m3x2_to_h2(v.y & 0xFFFFu)), h2_bits(e4m3x2_to_h2(v.y >> 16)));
+  hi = make_uint4(h2_bits(e4m3x2_to_h2(v.z & 0xFFFFu)), h2_bits(e4m3x2_to_h2(v.z >> 16)),
+                  h2_bits(e4m3x2_to_h2(v.w & 0xFFFFu)), h2_bits(e4m3x2_to_h2(v.w >> 16)));
+}
+// A scale for code x scale in fp16 with one rounding: 64 x scale in two fp16 parts, to be
+// multiplied by code / 64 (exact). Below 2^-14 the parts lose bits and fp32 is used.
+struct VScale {
+  __half2 hi, lo;
+  float s;
+};
+__device__ __forceinline__ VScale v_scale(float s) {
+  VScale r;
+  r.s = s;
+  const __half h = __float2half_rn(64.f * s);
+  r.hi = __half2half2(h);
+  r.lo = __half2half2(__float2half_rn(64.f * s - __half2float(h)));
+  return r;
+}
+__device__ __forceinline__ uint32_t scaled2(uint32_t two, const VScale& v) {
+  const __half2 c = e4m3x2_to_h2(two);
+  if (fabsf(v.s) >= 6.103515625e-05f) {
+    const __half2 c64 = __hmul2(c, __half2half2(__float2half_rn(0.015625f)));
+    return h2_bits(__hfma2(c64, v.hi, __hmul2(c64, v.lo)));
+  }
+  const float2 f = __half22float2(c);
+  return h2_bits(__floats2half2_rn(f.x * v.s, f.y * v.s));
+}
+__device__ __forceinline__ void codes_to_scaled_f16(uint4 v, const VScale& s, uint4& lo, uint4& hi) {
+  lo = make_uint4(scaled2(v.x & 0xFFFFu, s), scaled2(v.x >> 16, s), scaled2(v.y & 0xFFFFu, s), scaled2(v.y >> 16, s));
+  hi = make_uint4(scaled2(v.z & 0xFFFFu, s), scaled2(v.z >> 16, s), scaled2(v.w & 0xFFFFu, s), scaled2(v.w >> 16, s));
+}
+// Eight bf16 -> fp16 (exact inside its normal range); *bad when one is beyond it.
+__device__ __forceinline__ uint4 bf16x8_to_f16(uint4 v, bool* bad) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t o[4];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const float2 a = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(u[i] & 0xFFFFu), __NV_E4M3)));
-    const float2 b = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(u[i] >> 16), __NV_E4M3)));
-    v[4 * i] = a.x * s, v[4 * i + 1] = a.y * s, v[4 * i + 2] = b.x * s, v[4 * i + 3] = b.y * s;
+  for (int i = 0; i < 4; ++i) {
+    o[i] = h2_bits(__floats2half2_rn(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u)));
+    *bad |= (o[i] & 0x7C00u) == 0x7C00u || (o[i] & 0x7C000000u) == 0x7C000000u;
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+// fp16 infinities and NaN of eight values become zero.
+__device__ __forceinline__ uint4 drop_inf8(uint4 v) {
+  uint32_t o[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if ((o[i] & 0x7C00u) == 0x7C00u) o[i] &= 0xFFFF0000u;
+    if ((o[i] & 0x7C000000u) == 0x7C000000u) o[i] &= 0xFFFFu;
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+template <typename T>
+__device__ __forceinline__ uint4 q_to_f16(uint4 v, bool* bad) {
+  if constexpr (sizeof(T) == 2 && !__is_same(T, __half)) {
+    return bf16x8_to_f16(v, bad);
+  } else {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) *bad |= (w[i] & 0x7C00u) == 0x7C00u || (w[i] & 0x7C000000u) == 0x7C000000u;
+    return v;
+  }
+}
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  if constexpr (__is_same(T, __half)) {
+    return h2_bits(__floats2half2_rn(a, b));
+  } else {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
   }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(CK_WARPS * 32)
-chunk_attention_kernel(Dev D, int layer, int n_seg, const int32_t* __restrict__ seg_req,
-                       const int32_t* __restrict__ seg_start, int n_tok, const int32_t* __restrict__ limit,
-                       const T* __restrict__ q, long long q_tok, long long q_head, float scale_log2,
-                       T* __restrict__ out, long long o_tok, long long o_head, float* __restrict__ lse_out) {
-  griddep_wait();
-  const int lane = threadIdx.x & 31;
-  const long long w = (long long)blockIdx.x * CK_WARPS + (threadIdx.x >> 5);
-  const int tok = (int)(w / D.n_heads), h = (int)(w % D.n_heads);
-  if (tok >= n_tok) return;
-  int s = -1, lo = 0;
-  for (int i = 0; i <= n_seg; ++i) {
-    const int at = seg_start[i], hi = min(max(at, lo), n_tok);
-    if (at != hi && lane == 0) set_status(D.status, HS_ERR_BAD_ID);
-    if (i > 0 && tok >= lo && tok < hi) s = i - 1;
-    lo = hi;
+// ---- the plan -------------------------------------------------------------------------
+// Inclusive scan over the CTA's 448 threads (sum or maximum); tmp: 32 ints; returns the
+// inclusive value, *total the whole.
+template <bool MAX>
+__device__ __forceinline__ int block_scan(int v, int* tmp, int* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  auto op = [](int a, int b) { return MAX ? max(a, b) : a + b; };
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v = op(v, u);
   }
-  if (s < 0) return;
-  const int r = seg_req[s];
-  int L = limit[tok];
-  if (r < 0 || r >= D.max_requests || L < 0 || L > D.max_ctx) {
-    if (lane == 0) set_status(D.status, HS_ERR_BAD_ID);
-    L = 0;
+  __syncthreads();
+  if (lane == 31) tmp[warp] = v;
+  __syncthreads();
+  int before = 0, all = tmp[0];
+  for (int w = 0; w < CK_THREADS / 32; ++w) {
+    if (w < warp) before = w == 0 ? tmp[0] : op(before, tmp[w]);
+    if (w > 0) all = op(all, tmp[w]);
   }
-  float qv[18], acc[16], m = -INFINITY, l = 0.f;
-  const T* qp = q + tok * q_tok + h * q_head;
+  *total = all;
+  return warp == 0 ? v : op(before, v);
+}
+
+__device__ __forceinline__ int clamp_limit(const Dev& D, int l, bool* bad) {
+  if (l < 0 || l > D.max_ctx) {
+    *bad = true;
+    return 0;
+  }
+  return l;
+}
+
+// Tokens and largest limit of block b of a segment [t0, t1).
+__device__ __forceinline__ int block_limit(const Dev& D, const int32_t* limit, int t0, int t1, bool* bad) {
+  int m = 0;
+  for (int t = t0; t < t1; ++t) m = max(m, clamp_limit(D, __ldg(limit + t), bad));
+  return m;
+}
+__device__ __forceinline__ int pages_of(int limit) { return max(1, (limit + PAGE - 1) / PAGE); }
+
+struct Range {
+  int seg, seg_t0, seg_t1;   // the segment of the first block, clamped
+  int tok0;                  // the first block's first token
+  int page;                  // its first page of this range
+  int at;                    // the range's first tile
+  int n;                     // its tiles
+  int per_pair;              // tiles of each pair's range
+};
+
+// This pair's range of tiles. All threads of the CTA take part; sm: the operand buffers.
+__device__ Range plan_range(const Dev& D, const ChunkArgs& A, int pair, int tpb, uint8_t* sm, int32_t* found) {
+  int* start = reinterpret_cast<int*>(sm + CK_PLAN_START);
+  int* blk = reinterpret_cast<int*>(sm + CK_PLAN_BLK);
+  int* sums = reinterpret_cast<int*>(sm + CK_PLAN_SUM);
+  int* tmp = reinterpret_cast<int*>(sm + CK_PLAN_WARP_TMP);
+  const int tid = threadIdx.x;
   bool bad = false;
-#pragma unroll
-  for (int i = 0; i < 18; ++i) {
-    const int d = i < 16 ? (i >> 3) * 256 + lane * 8 + (i & 7) : LATENT + lane * 2 + (i - 16);
-    qv[i] = to_f32(qp[d]);
-    bad |= !(fabsf(qv[i]) < 65504.f);
+  // segment starts, clamped to [0, n_tok] and to ascend
+  const int per = (A.n_seg + CK_THREADS) / CK_THREADS;   // of the n_seg + 1 starts
+  const int lo = min(tid * per, A.n_seg + 1), hi = min(lo + per, A.n_seg + 1);
+  int m = 0, total;
+  for (int i = lo; i < hi; ++i) {
+    const int s = __ldg(A.seg_start + i), c = min(max(s, 0), A.n_tok);
+    m = max(m, c);
+    bad |= c != s || m != c;
+    start[i] = m;
   }
-#pragma unroll
-  for (int i = 0; i < 16; ++i) acc[i] = 0.f;
-  for (int pg = 0; pg * PAGE < L; ++pg) {
-    int err = HS_OK;
-    const uint8_t* rows = page_rows(D, layer, r, pg, &err);
-    if (!rows) {
-      if (lane == 0) set_status(D.status, err);
-      continue;
+  const int upto = block_scan<true>(m, tmp, &total);
+  // exclusive maximum of the threads before
+  int before = __shfl_up_sync(0xffffffffu, upto, 1);
+  __syncthreads();
+  if ((tid & 31) == 31) tmp[tid >> 5] = upto;
+  __syncthreads();
+  if ((tid & 31) == 0) before = tid == 0 ? 0 : tmp[(tid >> 5) - 1];
+  for (int i = lo; i < hi; ++i) {
+    bad |= start[i] < before;
+    start[i] = max(start[i], before);
+  }
+  __syncthreads();
+  // blocks before each segment
+  int nb = 0;
+  for (int i = lo; i < min(hi, A.n_seg); ++i) nb += (start[i + 1] - start[i] + tpb - 1) / tpb;
+  int n_blocks;
+  int at = block_scan<false>(nb, tmp, &n_blocks) - nb;
+  for (int i = lo; i < min(hi, A.n_seg); ++i) {
+    blk[i] = at;
+    at += (start[i + 1] - start[i] + tpb - 1) / tpb;
+  }
+  if (tid == 0) blk[A.n_seg] = n_blocks;
+  __syncthreads();
+  // the tiles of 448 blocks at a time
+  auto segment_of = [&](int b) {   // the last segment whose first block is <= b (never an empty one)
+    int l = 0, h = A.n_seg;
+    while (h - l > 1) {
+      const int mid = (l + h) >> 1;
+      if (blk[mid] <= b) l = mid; else h = mid;
     }
-    const int nr = min(PAGE, L - pg * PAGE);
-    for (int t = 0; t < nr; ++t) {
-      const uint8_t* row = rows + (size_t)t * ROW;
-      const float4 s4 = *reinterpret_cast<const float4*>(row + LATENT);
-      const uint32_t rw = *reinterpret_cast<const uint32_t*>(row + LATENT + 16 + lane * 4);
-      float v[18];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const float sj = j == 0 ? (lane < 16 ? s4.x : s4.y) : (lane < 16 ? s4.z : s4.w);
-        values8(*reinterpret_cast<const uint2*>(row + j * 256 + lane * 8), sj, v + 8 * j);
-        bad |= !(fabsf(sj) < CK_MAX_SCALE);
+    return l;
+  };
+  auto tiles_of = [&](int b, bool* bad_id) {
+    const int s = segment_of(b), t0 = start[s] + (b - blk[s]) * tpb;
+    return pages_of(block_limit(D, A.limit, t0, min(t0 + tpb, start[s + 1]), bad_id));
+  };
+  const int chunks = (n_blocks + CK_THREADS - 1) / CK_THREADS;
+  int all = 0;
+  for (int c = 0; c < chunks; ++c) {
+    const int b = c * CK_THREADS + tid;
+    int sum;
+    block_scan<false>(b < n_blocks ? tiles_of(b, &bad) : 0, tmp, &sum);
+    if (tid == 0) sums[c] = sum;
+    all += sum;
+  }
+  if (bad) set_status(D.status, HS_ERR_BAD_ID);
+  Range r = {};
+  r.per_pair = max((all + A.pairs - 1) / A.pairs, CK_MIN_PAGES);
+  r.at = pair * r.per_pair;
+  r.n = min(r.per_pair, all - r.at);
+  __syncthreads();
+  if (r.n <= 0) {
+    r.n = 0;
+    return r;
+  }
+  // the block that holds tile r.at
+  int c = 0, first = 0;
+  while (first + sums[c] <= r.at) first += sums[c++];
+  const int b = c * CK_THREADS + tid;
+  bool ignore = false;
+  const int t = b < n_blocks ? tiles_of(b, &ignore) : 0;
+  int sum;
+  const int end = first + block_scan<false>(t, tmp, &sum);
+  if (t > 0 && end - t <= r.at && r.at < end) {
+    const int s = segment_of(b);
+    found[0] = s;
+    found[1] = start[s];
+    found[2] = start[s + 1];
+    found[3] = start[s] + (b - blk[s]) * tpb;
+    found[4] = r.at - (end - t);
+  }
+  __syncthreads();
+  r.seg = found[0];
+  r.seg_t0 = found[1];
+  r.seg_t1 = found[2];
+  r.tok0 = found[3];
+  r.page = found[4];
+  return r;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const Dev D, const ChunkArgs A) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  // at the same offset in both CTAs: the dynamic shared memory of one kernel starts at one address
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  float* scl = reinterpret_cast<float*>(smem + CK_OFF_SCL);
+  float* red = reinterpret_cast<float*>(smem + CK_OFF_RED);
+  Piece* ring = reinterpret_cast<Piece*>(smem + CK_OFF_RING);
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + CK_OFF_MISC);
+  volatile int32_t* dead = reinterpret_cast<int32_t*>(smem + CK_OFF_MISC) + 1;
+  int32_t* found = reinterpret_cast<int32_t*>(smem + CK_OFF_MISC) + 2;
+  int32_t* there = reinterpret_cast<int32_t*>(smem + CK_OFF_MISC) + 8;   // [CK_SCL] whether a tile's page exists
+  auto bar = [&](int i) { return sbase + CK_OFF_BAR + 8 * i; };
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = blockIdx.x & 1;
+  const int pair = blockIdx.x >> 1;
+  const int H = D.n_heads, tpb = CK_ROWS / H;
+
+  if (warp == CK_MMA_WARP) tmem_alloc_pair(smem_u32(tslot), 512);
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(B_KF + i), 2 * CK_CONV_WARPS);
+      mbar_init(bar(B_VF + i), 2 * CK_CONV_WARPS);
+      mbar_init(bar(B_PF + i), 2 * 4);
+      mbar_init(bar(B_SD + i), 1);
+      mbar_init(bar(B_PD + i), 1);
+    }
+    mbar_init(bar(B_SR), 2 * 4);
+    mbar_init(bar(B_FIN), 1);
+    for (int i = 0; i < CK_RING; ++i) {
+      mbar_init(bar(B_RF + i), 1);
+      mbar_init(bar(B_RE + i), CK_CONV_WARPS + 4 + (rank == 0 ? 1 : 0));
+    }
+    fence_mbar_init();
+    *dead = 0;
+  }
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = *tslot;
+  griddep_wait();
+  griddep_launch();   // only the merge of this call depends on it, and waits for its end
+
+  const Range R = plan_range(D, A, pair, tpb, smem, found);
+  __syncthreads();   // the plan's arrays are done with
+  const ChunkWork W = work_at(A.work, A.pairs);
+
+  if (warp == CK_PLAN_WARP) {
+    // ------------------------------- pieces of the range -------------------------------
+    int seg = R.seg, t0 = R.tok0, seg_end = R.seg_t1, page = R.page, left = R.n, at = R.at;
+    uint32_t k = 0;
+    ChunkCut cut = {0, 0, 0, 0};
+    bool ok = true;
+    for (;; ++k) {
+      Piece p = {};
+      p.n_tok = -1;
+      if (left > 0) {
+        const int t1 = min(t0 + tpb, seg_end);
+        const int r = __ldg(A.seg_req + seg);
+        bool bad = r < 0 || r >= D.max_requests, ignore = false;
+        const int lim = block_limit(D, A.limit, t0, t1, &ignore), n_pages = pages_of(lim);
+        if (bad && lane == 0) set_status(D.status, HS_ERR_BAD_ID);
+        p.tok0 = t0;
+        p.n_tok = t1 - t0;
+        p.req = bad ? -1 : r;
+        p.limit = bad ? 0 : lim;
+        p.pg0 = page;
+        p.pg1 = min(n_pages, page + left);
+        const bool first = page == 0, last = p.pg1 == n_pages;
+        p.slot = first && last ? -1 : first ? 1 : 0;
+        if (first && !last) cut = {t0, p.n_tok, (at + n_pages - 1) / R.per_pair, 0};
+        const int used = p.pg1 - p.pg0;
+        left -= used;
+        at += used;
+        page = 0;
+        t0 = t1;
+        while (left > 0 && t0 >= seg_end) {   // the next segment with tokens
+          ++seg;
+          t0 = seg_end;
+          seg_end = max(seg_end, min(max(__ldg(A.seg_start + seg + 1), 0), A.n_tok));
+        }
       }
-      v[16] = __uint_as_float(rw << 16);
-      v[17] = __uint_as_float(rw & 0xFFFF0000u);
-      float z = 0.f;
+      const uint32_t slot = k % CK_RING;
+      // a piece may be a whole context read over the host link: a long bound
+      if (k >= CK_RING) ok = ck_wait(bar(B_RE + slot), (k / CK_RING - 1) & 1, D.status, dead, 30);
+      if (!ok) break;
+      if (lane == 0) {
+        ring[slot] = p;
+        arrive_local(bar(B_RF + slot));
+      }
+      __syncwarp();
+      if (p.n_tok < 0) break;
+    }
+    if (lane == 0 && rank == 0) W.cut[pair] = cut;
+  } else if (warp == CK_MMA_WARP) {
+    // ---------------------------------- MMA issue ----------------------------------
+    if (rank == 0 && lane == 0) {
+      const uint32_t idesc_qk = idesc_f16(128, 64, false, false, false);
+      const uint32_t idesc_pv = idesc_f16(128, 256, false, true, false);
+      const uint32_t q0 = sbase + CK_OFF_Q, k0 = sbase + CK_OFF_K, v0 = sbase + CK_OFF_V, p0 = sbase + CK_OFF_P;
+      uint32_t it = 0;
+      bool ok = true;
+      for (uint32_t k = 0; ok; ++k) {
+        const uint32_t slot = k % CK_RING;
+        if (!ck_wait(bar(B_RF + slot), (k / CK_RING) & 1, D.status, dead, 30)) break;
+        const int n_tok = ring[slot].n_tok, n = ring[slot].pg1 - ring[slot].pg0;
+        arrive_local(bar(B_RE + slot));
+        if (n_tok < 0) break;
+        for (int i = 0; i <= n && ok; ++i) {
+          if (i < n) {
+            const uint32_t t = it + i, st = t & 1;
+            ok = ck_wait(bar(B_KF + st), (t >> 1) & 1, D.status, dead);
+            if (ok && t > 0) ok = ck_wait(bar(B_SR), (t - 1) & 1, D.status, dead);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t kb = k0 + st * CK_KSTAGE;
 #pragma unroll
-      for (int i = 0; i < 18; ++i) {
-        if (!(fabsf(v[i]) < 65504.f)) bad = true, v[i] = 0.f;
-        z += qv[i] * v[i];
+            for (int g = 0; g < 5; ++g)
+#pragma unroll
+              for (int kk = 0; kk < (g < 4 ? 8 : 4); ++kk) {
+                const int atom = 2 * g + (kk >> 2);
+                umma_f16_pair(tmem + CK_TM_S + g * 32, smem_desc_sw128(q0 + atom * CK_QATOM + (kk & 3) * 32, 16, 1024),
+                              smem_desc_sw128(kb + atom * CK_KATOM + (kk & 3) * 32, 16, 1024), idesc_qk, kk > 0);
+              }
+            umma_commit_pair(bar(B_SD + st));
+          }
+          if (i > 0) {
+            const uint32_t t = it + i - 1, st = t & 1;
+            ok = ck_wait(bar(B_VF + st), (t >> 1) & 1, D.status, dead) &&
+                 ck_wait(bar(B_PF + st), (t >> 1) & 1, D.status, dead);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t vb = v0 + st * CK_VSTAGE;
+#pragma unroll
+            for (int g = 0; g < 2; ++g)
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                umma_f16_pair(tmem + CK_TM_O + g * 128, smem_desc_sw128(p0 + kk * 32, 16, 1024),
+                              smem_desc_sw128(vb + g * 2 * CK_VATOM + kk * 2048, CK_VATOM, 1024), idesc_pv,
+                              (i > 1 || kk > 0) ? 1u : 0u);
+            umma_commit_pair(bar(B_PD + st));
+          }
+        }
+        it += n;
+      }
+    }
+  } else if (warp >= CK_CONV_WARP0) {
+    // ------------------------------ cache rows to operands ------------------------------
+    const int ct = tid - CK_CONV_WARP0 * 32;
+    const uint32_t kf0 = mapa(bar(B_KF), 0), vf0 = mapa(bar(B_VF), 0);   // the first CTA's
+    // 16-byte parts of a row: this thread has part `part` (a 128-value group is 8 parts) of
+    // the rows 8 k + row0 of its CTA's half page; 8 neighbouring threads store 4 parts of two
+    // rows, which the swizzle puts on 8 different bank groups
+    const int part = 4 * ((ct >> 3) & 7) + (ct & 3), row0 = 2 * (ct >> 6) + ((ct >> 2) & 1);
+    const int grp = part >> 3;
+    // V needs the groups `rank` and 2 + rank of all 64 rows: a thread of such a group takes its
+    // own rows again, the others take the neighbour group's part of the other half page
+    const bool own_v = (grp & 1) == (int)rank;
+    const int part_v = own_v ? part : part ^ 8, grp_v = part_v >> 3;
+    const int half_v = own_v ? (int)rank : 1 - (int)rank;
+    const int rope_row = ct >> 3, rope_part = ct & 7;
+    const uint32_t k_dst = (uint32_t)((part >> 2) * CK_KATOM), v_dst = (uint32_t)((grp_v >> 1) * 2 * CK_VATOM + ((part_v >> 2) & 1) * CK_VATOM);
+    const int chunk = (part & 3) * 2;
+    uint4 own[4], oth[4], rope;
+    float vsc[4];
+    float4 sc4;
+    bool bad_range = false;
+
+    Piece P;
+    uint32_t kp = 0, it = 0;
+    int page = 0;
+    const uint8_t* rows = nullptr;
+    int next_pg = -1;                       // block-table entry of the page after `page`
+    auto fetch_entry = [&](int pg) {
+      next_pg = -1;
+      if (P.req >= 0 && pg < P.pg1) next_pg = __ldg(D.bt + (size_t)P.req * D.max_pages + pg);
+    };
+    auto base_of = [&](int entry, int pg) -> const uint8_t* {
+      if (P.req < 0 || pg * PAGE >= P.limit) return nullptr;   // nothing is seen
+      if (entry >= 0 && entry < D.num_pages) return D.kv[A.layer] + (size_t)entry * PAGE * ROW;
+      int err = HS_OK;
+      const uint8_t* b = page_rows(D, A.layer, P.req, pg, &err);
+      if (!b) set_status(D.status, err);
+      return b;
+    };
+    auto issue = [&]() {                    // loads of the tile (P, page)
+      const int nv = rows ? min(PAGE, P.limit - page * PAGE) : 0;   // rows some token sees
+      const uint4 z = make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int r = (int)rank * 32 + 8 * k + row0;
+        own[k] = r < nv ? __ldg(reinterpret_cast<const uint4*>(rows + (size_t)r * ROW) + part) : z;
       }
 #pragma unroll
-      for (int o = 16; o >= 1; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-      z *= scale_log2;
-      const float mn = fmaxf(m, z), f = exp2f(m - mn), p = exp2f(z - mn);
-      m = mn;
-      l = l * f + p;
+      for (int k = 0; k < 4; ++k) {
+        const int r = half_v * 32 + 8 * k + row0;
+        oth[k] = !own_v && r < nv ? __ldg(reinterpret_cast<const uint4*>(rows + (size_t)r * ROW) + part_v) : z;
+        vsc[k] = r < nv ? __ldg(reinterpret_cast<const float*>(rows + (size_t)r * ROW + LATENT) + grp_v) : 0.f;
+      }
+      {
+        const int r = (int)rank * 32 + rope_row;
+        rope = r < nv ? __ldg(reinterpret_cast<const uint4*>(rows + (size_t)r * ROW) + 33 + rope_part) : z;
+      }
+      if (ct < PAGE) {
+        sc4 = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (ct < nv) sc4 = __ldg(reinterpret_cast<const float4*>(rows + (size_t)ct * ROW + LATENT));
+      }
+    };
+    auto good_scale = [&](float s) {
+      if (fabsf(s) < CK_MAX_SCALE) return s;
+      bad_range = true;
+      return 0.f;
+    };
+    auto take_piece = [&]() {               // the next piece, if there is one
+      const uint32_t slot = kp % CK_RING;
+      if (!ck_wait(bar(B_RF + slot), (kp / CK_RING) & 1, D.status, dead, 30)) return false;
+      P = ring[slot];
+      __syncwarp();
+      if (lane == 0) arrive_local(bar(B_RE + slot));
+      ++kp;
+      if (P.n_tok < 0) return false;
+      page = P.pg0;
+      fetch_entry(page);
+      rows = base_of(next_pg, page);
+      fetch_entry(page + 1);
+      issue();
+      return true;
+    };
+    bool first = true;
+    bool more = take_piece();
+    while (more) {
+      const uint32_t st = it & 1;
+      if (first) {
+        // Q of the block's rows, once the products of the previous piece have read theirs
+        if (it > 0 && !ck_wait(bar(B_SD + ((it - 1) & 1)), ((it - 1) >> 1) & 1, D.status, dead)) break;
+        const T* q = static_cast<const T*>(A.q);
+#pragma unroll 1
+        for (int b = 0; b < 2; ++b) {
+          uint4 v[9];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) acc[i] = acc[i] * f + p * v[i];
+          for (int k = 0; k < 9; ++k) {
+            const int c = ct + (b * 9 + k) * CK_CONV, r = c / 72, ch = c - r * 72;
+            const int gr = (int)rank * CK_HALF + r, tk = gr / H, h = gr - tk * H;
+            v[k] = tk < P.n_tok ? __ldg(reinterpret_cast<const uint4*>(q + (P.tok0 + tk) * A.q_tok + h * A.q_head) + ch)
+                                : make_uint4(0, 0, 0, 0);
+          }
+#pragma unroll
+          for (int k = 0; k < 9; ++k) {
+            const int c = ct + (b * 9 + k) * CK_CONV, r = c / 72, ch = c - r * 72;
+            *reinterpret_cast<uint4*>(smem + CK_OFF_Q + (ch >> 3) * CK_QATOM + sw128_chunk(r, ch & 7)) =
+                q_to_f16<T>(v[k], &bad_range);
+          }
+        }
+        first = false;
+      }
+      // K, the rope and the scales
+      if (it >= 2 && !ck_wait(bar(B_SD + st), ((it - 2) >> 1) & 1, D.status, dead)) break;
+      uint8_t* kt = smem + CK_OFF_K + st * CK_KSTAGE;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (any_nan(own[k])) {
+          bad_range = true;
+          own[k] = make_uint4(drop_nan4(own[k].x), drop_nan4(own[k].y), drop_nan4(own[k].z), drop_nan4(own[k].w));
+        }
+        uint4 lo, hi;
+        codes_to_f16(own[k], lo, hi);
+        const int r = 8 * k + row0;
+        *reinterpret_cast<uint4*>(kt + k_dst + sw128_chunk(r, chunk)) = lo;
+        *reinterpret_cast<uint4*>(kt + k_dst + sw128_chunk(r, chunk + 1)) = hi;
+      }
+      {
+        bool bad = false;
+        uint4 v = bf16x8_to_f16(rope, &bad);
+        if (bad) {
+          bad_range = true;
+          v = drop_inf8(v);
+        }
+        *reinterpret_cast<uint4*>(kt + 8 * CK_KATOM + sw128_chunk(rope_row, rope_part)) = v;
+      }
+      if (ct < PAGE) {
+        float* s = scl + (it % CK_SCL) * 256 + ct;
+        s[0] = good_scale(sc4.x);
+        s[64] = good_scale(sc4.y);
+        s[128] = good_scale(sc4.z);
+        s[192] = good_scale(sc4.w);
+        if (ct == 0) there[it % CK_SCL] = rows != nullptr;
+      }
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) arrive_cluster(kf0 + 8 * st);
+      // V
+      if (it >= 2 && !ck_wait(bar(B_PD + st), ((it - 2) >> 1) & 1, D.status, dead)) break;
+      uint8_t* vt = smem + CK_OFF_V + st * CK_VSTAGE;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint4 c = own[k];
+        if (!own_v) {
+          c = oth[k];
+          if (any_nan(c)) c = make_uint4(drop_nan4(c.x), drop_nan4(c.y), drop_nan4(c.z), drop_nan4(c.w));
+        }
+        uint4 lo, hi;
+        codes_to_scaled_f16(c, v_scale(good_scale(vsc[k])), lo, hi);
+        const int r = half_v * 32 + 8 * k + row0;
+        *reinterpret_cast<uint4*>(vt + v_dst + sw128_chunk(r, chunk)) = lo;
+        *reinterpret_cast<uint4*>(vt + v_dst + sw128_chunk(r, chunk + 1)) = hi;
+      }
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) arrive_cluster(vf0 + 8 * st);
+      ++it;
+      if (page + 1 < P.pg1) {
+        ++page;
+        rows = base_of(next_pg, page);
+        fetch_entry(page + 1);
+        issue();
+      } else {
+        more = take_piece();
+        first = true;
+      }
+    }
+    if (__any_sync(0xffffffffu, bad_range) && lane == 0) set_status(D.status, HS_ERR_RANGE);
+  } else {
+    // ------------------------------ softmax and output ------------------------------
+    const int row = tid & 63, half = tid >> 6;
+    const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
+    const uint32_t pf0 = mapa(bar(B_PF), 0), sr0 = mapa(bar(B_SR), 0);
+    const int gr = (int)rank * CK_HALF + row, tk = gr / H, h = gr - tk * H;
+    uint32_t it = 0;
+    bool ok = true, dead_all = false;
+    for (uint32_t kp = 0;; ++kp) {
+      const uint32_t slot = kp % CK_RING;
+      ok &= ck_wait(bar(B_RF + slot), (kp / CK_RING) & 1, D.status, dead, 30);
+      if (bar_any(1, 128, !ok)) break;
+      const Piece P = ring[slot];
+      __syncwarp();
+      if (lane == 0) arrive_local(bar(B_RE + slot));
+      if (P.n_tok < 0) break;
+      const bool live = tk < P.n_tok;
+      int lim = 0;
+      if (live && P.req >= 0) {
+        bool ignore = false;
+        lim = clamp_limit(D, __ldg(A.limit + P.tok0 + tk), &ignore);
+      }
+      float m = -INFINITY, l = 0.f;   // the row's reference (both halves alike), this half's sum
+      for (int pg = P.pg0; pg < P.pg1; ++pg, ++it) {
+        const uint32_t st = it & 1;
+        ok &= ck_wait(bar(B_SD + st), (it >> 1) & 1, D.status, dead);
+        tc_fence_after();
+        const float* sc = scl + (it % CK_SCL) * 256 + half * 32;
+        float s[32];
+        {
+          uint32_t a[32], b[32];
+          tmem_ld32(lanes + CK_TM_S, a);
+          tmem_ld32(lanes + CK_TM_S + 32, b);
+          tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 32; j += 4) {
+            const float4 x = *reinterpret_cast<const float4*>(sc + j), y = *reinterpret_cast<const float4*>(sc + 64 + j);
+            s[j] = x.x * __uint_as_float(a[j]) + y.x * __uint_as_float(b[j]);
+            s[j + 1] = x.y * __uint_as_float(a[j + 1]) + y.y * __uint_as_float(b[j + 1]);
+            s[j + 2] = x.z * __uint_as_float(a[j + 2]) + y.z * __uint_as_float(b[j + 2]);
+            s[j + 3] = x.w * __uint_as_float(a[j + 3]) + y.w * __uint_as_float(b[j + 3]);
+          }
+          tmem_ld32(lanes + CK_TM_S + 64, a);
+          tmem_ld32(lanes + CK_TM_S + 96, b);
+          tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 32; j += 4) {
+            const float4 x = *reinterpret_cast<const float4*>(sc + 128 + j), y = *reinterpret_cast<const float4*>(sc + 192 + j);
+            s[j] += x.x * __uint_as_float(a[j]) + y.x * __uint_as_float(b[j]);
+            s[j + 1] += x.y * __uint_as_float(a[j + 1]) + y.y * __uint_as_float(b[j + 1]);
+            s[j + 2] += x.z * __uint_as_float(a[j + 2]) + y.z * __uint_as_float(b[j + 2]);
+            s[j + 3] += x.w * __uint_as_float(a[j + 3]) + y.w * __uint_as_float(b[j + 3]);
+          }
+          tmem_ld32(lanes + CK_TM_S + 128, a);
+          tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 32; ++j) s[j] = (s[j] + __uint_as_float(a[j])) * A.scale_log2;
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_cluster(sr0);   // the score accumulators may be written again
+        const int seen = there[it % CK_SCL] ? lim - pg * PAGE - half * 32 : 0;   // of this thread's 32 keys
+        if (seen < 32) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) s[j] = j < seen ? s[j] : -INFINITY;
+        }
+        float mt = s[0];
+#pragma unroll
+        for (int j = 1; j < 32; ++j) mt = fmaxf(mt, s[j]);
+        red[(it & 1) * 128 + tid] = mt;
+        if (bar_any(1, 128, !ok)) {
+          dead_all = true;
+          break;
+        }
+        mt = fmaxf(mt, red[(it & 1) * 128 + (tid ^ 64)]);
+        float f = 1.f;
+        if (mt > m + CK_RESCALE_LOG2) {   // also the first finite maximum, when m is -inf
+          if (m > -INFINITY) f = ex2_approx(m - mt);
+          m = mt;
+        }
+        const float off = m > -INFINITY ? CK_P_SHIFT - m : -INFINITY;
+        float ls = 0.f;
+        uint32_t ph[16];
+#pragma unroll
+        for (int j = 0; j < 32; j += 2) {
+          const float p0 = ex2_approx(s[j] + off), p1 = ex2_approx(s[j + 1] + off);
+          ls += p0 + p1;
+          ph[j >> 1] = h2_bits(__floats2half2_rn(p0, p1));
+        }
+        l = l * f + ls;
+        // PV(t - 1) has read P and written O
+        if (it > 0) ok = ck_wait(bar(B_PD + ((it - 1) & 1)), ((it - 1) >> 1) & 1, D.status, dead);
+        tc_fence_after();
+        if (pg > P.pg0 && __any_sync(0xffffffffu, f != 1.f)) {
+#pragma unroll 1
+          for (int c = 0; c < 256; c += 32) {
+            uint32_t o[32];
+            tmem_ld32(lanes + CK_TM_O + c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+            tmem_st32(lanes + CK_TM_O + c, o);
+          }
+          tmem_wait_st();
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          *reinterpret_cast<uint4*>(smem + CK_OFF_P + sw128_chunk(row, half * 4 + c)) =
+              make_uint4(ph[4 * c], ph[4 * c + 1], ph[4 * c + 2], ph[4 * c + 3]);
+        fence_proxy_async();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_cluster(pf0 + 8 * st);
+      }
+      // left at the barrier above, all four warps alike, or at the piece's end: then one more
+      if (dead_all) break;
+      ok &= ck_wait(bar(B_PD + ((it - 1) & 1)), ((it - 1) >> 1) & 1, D.status, dead);
+      tc_fence_after();
+      red[(it & 1) * 128 + tid] = l;
+      if (bar_any(1, 128, !ok)) break;
+      l += red[(it & 1) * 128 + (tid ^ 64)];
+      if (P.slot < 0) {
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        T* op = static_cast<T*>(A.out) + (P.tok0 + (long long)tk) * A.o_tok + h * A.o_head + half * 128;
+#pragma unroll 1
+        for (int c = 0; c < 8; ++c) {
+          uint32_t o[32];
+          tmem_ld32(lanes + CK_TM_O + c * 32, o);
+          tmem_wait_ld();
+          T* dst = op + (c >> 2) * 256 + (c & 3) * 32;
+          if (live) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 8) {
+              uint4 v;
+              v.x = pack2<T>(__uint_as_float(o[j]) * inv, __uint_as_float(o[j + 1]) * inv);
+              v.y = pack2<T>(__uint_as_float(o[j + 2]) * inv, __uint_as_float(o[j + 3]) * inv);
+              v.z = pack2<T>(__uint_as_float(o[j + 4]) * inv, __uint_as_float(o[j + 5]) * inv);
+              v.w = pack2<T>(__uint_as_float(o[j + 6]) * inv, __uint_as_float(o[j + 7]) * inv);
+              *reinterpret_cast<uint4*>(dst + j) = v;
+            }
+          }
+        }
+        if (A.lse && live && half == 0)
+          A.lse[(size_t)(P.tok0 + tk) * H + h] = l > 0.f ? (m - CK_P_SHIFT + log2f(l)) * 0.6931471805599453f : -INFINITY;
+      } else {
+        const size_t at = ((size_t)pair * 2 + P.slot) * CK_ROWS + gr;
+        float* dst = W.part + at * 512 + half * 128;
+#pragma unroll 1
+        for (int c = 0; c < 8; ++c) {
+          uint32_t o[32];
+          tmem_ld32(lanes + CK_TM_O + c * 32, o);
+          tmem_wait_ld();
+          if (live) {
+            uint4* d = reinterpret_cast<uint4*>(dst + (c >> 2) * 256 + (c & 3) * 32);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) d[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+          }
+        }
+        if (live && half == 0) W.stats[at] = make_float2(m - CK_P_SHIFT, l);
+      }
+      tc_fence_before();   // O may be written again once the next tile's P has arrived
     }
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  T* op = out + tok * o_tok + h * o_head;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) op[(i >> 3) * 256 + lane * 8 + (i & 7)] = from_f32<T>(acc[i] * inv);
-  if (lse_out && lane == 0)
-    lse_out[(size_t)tok * D.n_heads + h] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
-  if (__any_sync(0xffffffffu, bad) && lane == 0) set_status(D.status, HS_ERR_RANGE);
+  __syncthreads();
+  if (rank == 0 && warp == CK_MMA_WARP && lane == 0) {   // every issued MMA has completed before TMEM is freed
+    umma_commit_own(bar(B_FIN));
+    for (int i = 0; i < 4096 && !try_wait_cluster(bar(B_FIN), 0); ++i) __nanosleep(200);
+  }
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();   // neither CTA's memory is touched by the other any more
+  tc_fence_after();
+  if (warp == CK_MMA_WARP) tmem_dealloc_pair(tmem, 512);
+}
+
+// The rows of cut blocks: out = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i over the parts,
+// in pair order. CTA (row, group) looks at the cut of every group-th pair.
+constexpr int CM_THREADS = 128, CM_GROUPS = 8;
+template <typename T>
+__global__ void __launch_bounds__(CM_THREADS) chunk_merge_kernel(const Dev D, const ChunkArgs A) {
+  griddep_wait();
+  const ChunkWork W = work_at(A.work, A.pairs);
+  const int row = blockIdx.x, tid = threadIdx.x, H = D.n_heads;
+  for (int p = blockIdx.y; p < A.pairs; p += CM_GROUPS) {
+    const ChunkCut cut = W.cut[p];
+    if (row >= cut.n_tok * H) continue;
+    float m = -INFINITY;
+    for (int i = p; i <= cut.last_pair; ++i)
+      m = fmaxf(m, W.stats[((size_t)i * 2 + (i == p ? 1 : 0)) * CK_ROWS + row].x);
+    float l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (m > -INFINITY) {
+#pragma unroll 4
+      for (int i = p; i <= cut.last_pair; ++i) {
+        const size_t at = ((size_t)i * 2 + (i == p ? 1 : 0)) * CK_ROWS + row;
+        const float2 s = W.stats[at];
+        const float w = exp2f(s.x - m);
+        const float4 v = *(reinterpret_cast<const float4*>(W.part + at * 512) + tid);
+        l += w * s.y;
+        o.x += w * v.x, o.y += w * v.y, o.z += w * v.z, o.w += w * v.w;
+      }
+    }
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const int tok = cut.tok0 + row / H, h = row % H;
+    T* op = static_cast<T*>(A.out) + tok * A.o_tok + h * A.o_head + tid * 4;
+    *reinterpret_cast<uint2*>(op) = make_uint2(pack2<T>(o.x * inv, o.y * inv), pack2<T>(o.z * inv, o.w * inv));
+    if (A.lse && tid == 0) A.lse[(size_t)tok * H + h] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+  }
 }
 
 struct CallRange {
@@ -121,17 +1009,14 @@ struct CallRange {
 
 bool stride_ok(int64_t s, int64_t least) { return s >= least && s < (1ll << 40) && s % 8 == 0; }
 
-int64_t workspace_bytes(const hs_pool*) { return 256; }
+int chunk_pairs() { return num_sms() / 2 > 0 ? num_sms() / 2 : 1; }
 
 template <typename T>
-hs_status launch_chunk(hs_pool* p, int layer, int n_seg, const int32_t* d_seg_req, const int32_t* d_seg_start, int n,
-                       const int32_t* d_limit, const void* d_q, int64_t q_tok, int64_t q_head, float sm_scale,
-                       void* d_out, int64_t o_tok, int64_t o_head, float* d_lse, cudaStream_t st) {
-  const long long warps = (long long)n * p->cfg.n_heads;
-  return launch_pdl(chunk_attention_kernel<T>, dim3((unsigned)((warps + CK_WARPS - 1) / CK_WARPS)), dim3(CK_WARPS * 32), 0,
-                    st, 0, p->d, layer, n_seg, d_seg_req, d_seg_start, n, d_limit, static_cast<const T*>(d_q),
-                    (long long)q_tok, (long long)q_head, sm_scale * CK_LOG2E, static_cast<T*>(d_out), (long long)o_tok,
-                    (long long)o_head, d_lse);
+hs_status launch_chunk(hs_pool* p, const ChunkArgs& a, cudaStream_t st) {
+  if (ensure_kernel_attrs(chunk_attention_kernel<T>, CK_SMEM) != HS_OK) return HS_ERR_CUDA;
+  const hs_status s = launch_pdl(chunk_attention_kernel<T>, dim3(2 * a.pairs), dim3(CK_THREADS), CK_SMEM, st, 2, p->d, a);
+  if (s != HS_OK) return s;
+  return launch_pdl(chunk_merge_kernel<T>, dim3(CK_ROWS, CM_GROUPS), dim3(CM_THREADS), 0, st, 0, p->d, a);
 }
 
 }  // namespace
@@ -141,8 +1026,8 @@ hs_status launch_chunk(hs_pool* p, int layer, int n_seg, const int32_t* d_seg_re
 using namespace hs;
 
 extern "C" hs_status hs_chunk_workspace(const hs_pool* p, int64_t* bytes) {
-  if (!p || !bytes) return HS_ERR_INVALID;
-  *bytes = workspace_bytes(p);
+  if (!p || !bytes || !on_pool_device(p)) return HS_ERR_INVALID;
+  *bytes = work_bytes_for(chunk_pairs());
   return HS_OK;
 }
 
@@ -155,17 +1040,19 @@ extern "C" hs_status hs_chunk_attention(hs_pool* p, int32_t layer, int32_t n_seg
   if (!p || layer < 0 || layer >= p->cfg.n_layers || n_seg < 0 || n_seg > HS_CHUNK_MAX_SEGMENTS || n < 0 ||
       n > HS_CHUNK_MAX_TOKENS || (dtype != HS_BF16 && dtype != HS_FP16) || !on_pool_device(p))
     return HS_ERR_INVALID;
+  const int pairs = chunk_pairs();
   if (n > 0 && n_seg > 0) {
     const auto aligned = [](const void* x) { return x && (reinterpret_cast<uintptr_t>(x) & 15) == 0; };
     if (!d_seg_req || !d_seg_start || !d_limit || !aligned(d_q) || !aligned(d_out) || !aligned(d_work) ||
-        work_bytes < workspace_bytes(p) || !(fabsf(sm_scale) <= 3.0e38f))
+        work_bytes < work_bytes_for(pairs) || !(fabsf(sm_scale) <= 2.0e38f))
       return HS_ERR_INVALID;
     if (!stride_ok(q_tok, 0) || !stride_ok(q_head, 0) || !stride_ok(o_tok, LATENT) || !stride_ok(o_head, LATENT))
       return HS_ERR_INVALID;
   }
   p->settled_rows = nullptr;
   if (n == 0 || n_seg == 0) return HS_OK;
-  auto f = dtype == HS_BF16 ? launch_chunk<__nv_bfloat16> : launch_chunk<__half>;
-  return f(p, layer, n_seg, d_seg_req, d_seg_start, n, d_limit, d_q, q_tok, q_head, sm_scale, d_out, o_tok, o_head,
-           d_lse, reinterpret_cast<cudaStream_t>(stream));
+  const ChunkArgs a = {layer, n_seg, n, pairs, d_seg_req, d_seg_start, d_limit, d_q, q_tok, q_head, sm_scale * CK_LOG2E,
+                       d_out, o_tok, o_head, d_lse, d_work};
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  return dtype == HS_BF16 ? launch_chunk<__nv_bfloat16>(p, a, st) : launch_chunk<__half>(p, a, st);
 }
