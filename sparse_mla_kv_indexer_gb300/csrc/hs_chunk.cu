@@ -20,14 +20,15 @@
 // output dims for PV. The full rate of M = 128 then needs one copy of Q (64 rows, 72 KB),
 // and shared memory holds two stages of everything else.
 //
-// Roles (448 threads per CTA):
-//   warps 0-3   softmax: thread t has row t % 64 and the keys (in the output: the 128-dim
-//               groups) of half t / 64, the tensor-memory lane t
-//   warp 4      tensor memory; in the pair's first CTA the tcgen05.mma issue for both
-//   warp 5      the pieces (block, pages) of this pair's range, ahead of the other roles
-//   warps 6-13  cache rows -> fp16 operands: loads one tile ahead into registers, then
-//               K: the e4m3 codes of this CTA's 32 rows as fp16 (exact), and the rope;
-//               V: code x scale of all 64 rows for this CTA's two 128-dim groups
+// Roles (576 threads per CTA):
+//   warps 0-7   softmax: a thread has one row and 16 keys of the tile (in the output: one
+//               128-dim group); four threads share a row
+//   warps 8-11  cache rows -> K: the e4m3 codes of this CTA's 32 rows as fp16 (exact), the rope
+//   warps 12-15 cache rows -> V: code x scale of all 64 rows for this CTA's two 128-dim groups;
+//               both load one tile ahead into registers
+//   warp 16     tensor memory; in the pair's first CTA the tcgen05.mma issue for both
+//   warp 17     the pieces (block, pages) of this pair's range and their tiles' rows, ahead of the
+//               other roles
 // Tile t:  QK   S_g = Q_g K_g^T for the four 128-value groups and the rope (five
 //               accumulators), so that s = sum_g scale_g S_g + S_rope is exact up to fp32
 //          softmax  running maximum with a lazy rescale (the reference moves when a row
@@ -50,14 +51,19 @@ namespace hs {
 
 namespace {
 
-constexpr int CK_THREADS = 448;
-constexpr int CK_MMA_WARP = 4, CK_PLAN_WARP = 5, CK_CONV_WARP0 = 6;
-constexpr int CK_CONV_WARPS = 8, CK_CONV = CK_CONV_WARPS * 32;
+constexpr int CK_THREADS = 576;
+constexpr int CK_SM_WARPS = 8, CK_SM = CK_SM_WARPS * 32;         // softmax
+constexpr int CK_K_WARP0 = 8, CK_V_WARP0 = 12;
+constexpr int CK_CONV_WARPS = 4, CK_CONV = CK_CONV_WARPS * 32;   // of K, and of V
+constexpr int CK_MMA_WARP = 16, CK_PLAN_WARP = 17;
 constexpr int CK_ROWS = 128;       // rows of a block
 constexpr int CK_HALF = 64;        // rows of a block per CTA
 constexpr int CK_MIN_PAGES = 2;    // least pages of a pair's range
 constexpr int CK_RING = 4;         // pieces the planning warp runs ahead
+constexpr int CK_TILES = 16;       // tiles it runs ahead
 constexpr int CK_SCL = 4;          // tiles of scales held
+constexpr int CK_SCL_G = 68 * 4;   // bytes from one group's 64 scales to the next (other banks for the same row)
+constexpr int CK_SCL_T = 4 * CK_SCL_G;
 // shared memory
 constexpr int CK_QATOM = CK_HALF * 128;            // 64 rows x 64 dims fp16
 constexpr int CK_KATOM = 32 * 128;                 // 32 keys x 64 dims
@@ -68,17 +74,19 @@ constexpr int CK_OFF_Q = 0;
 constexpr int CK_OFF_K = 9 * CK_QATOM;
 constexpr int CK_OFF_V = CK_OFF_K + 2 * CK_KSTAGE;
 constexpr int CK_OFF_P = CK_OFF_V + 2 * CK_VSTAGE;
-constexpr int CK_OFF_SCL = CK_OFF_P + CK_HALF * 128;           // float [CK_SCL][4][64]
-constexpr int CK_OFF_RED = CK_OFF_SCL + CK_SCL * 4 * 64 * 4;   // float [2][128]
-constexpr int CK_OFF_RING = CK_OFF_RED + 2 * 128 * 4;          // Piece [CK_RING]
-constexpr int CK_PIECE_BYTES = 48;
-constexpr int CK_OFF_BAR = CK_OFF_RING + CK_RING * CK_PIECE_BYTES;
+constexpr int CK_OFF_SCL = CK_OFF_P + CK_HALF * 128;           // float [CK_SCL][4][64 of 68]
+constexpr int CK_OFF_RED = CK_OFF_SCL + CK_SCL * CK_SCL_T;   // float [2][4][64]
+constexpr int CK_OFF_RING = CK_OFF_RED + 2 * 256 * 4;          // Piece [CK_RING]
+constexpr int CK_PIECE_BYTES = 32;
+constexpr int CK_OFF_TILES = CK_OFF_RING + CK_RING * CK_PIECE_BYTES;   // Tile [CK_TILES]
+constexpr int CK_OFF_BAR = CK_OFF_TILES + CK_TILES * CK_PIECE_BYTES;
 enum Bar { B_KF = 0, B_VF = 2, B_PF = 4, B_SD = 6, B_PD = 8, B_SR = 10, B_FIN = 11, B_RF = 12, B_RE = 12 + CK_RING,
-           B_N = 12 + 2 * CK_RING };
+           B_TF = 12 + 2 * CK_RING, B_TE = B_TF + CK_TILES, B_SC = B_TE + CK_TILES, B_N = B_SC + CK_SCL };
 constexpr int CK_OFF_MISC = CK_OFF_BAR + B_N * 8;   // tensor-memory slot, dead flag, plan scalars
 constexpr int CK_SMEM = CK_OFF_MISC + 64 + 1024;
 static_assert(CK_SMEM <= 232448, "shared memory budget");
-// tensor memory: O [2][128 columns], then the five score accumulators of 32 columns
+// tensor memory: O [2][128 columns], then a ring of eight score accumulators of 32 columns, of
+// which a tile takes five: the next tile's first three are written while this one's are read
 constexpr uint32_t CK_TM_O = 0, CK_TM_S = 256;
 // the plan's arrays, in the operand buffers before the roles start
 constexpr int CK_PLAN_START = 0;                                        // int [HS_CHUNK_MAX_SEGMENTS + 1]
@@ -127,16 +135,24 @@ struct ChunkArgs {
   void* work;
 };
 
-// One block's pages [pg0, pg1) of one pair's range.
+// One block's pages [pg0, pg1) of one pair's range, two 16-byte words in the ring:
+//   tok0, n_tok (tokens of the block; -1: no more pieces), req (-1: a bad request, nothing is
+//   read), limit (the largest of the block's tokens)
+//   pg0, pg1, slot (-1: the whole block, else the workspace slot 0 or 1), 0
 struct Piece {
-  int32_t tok0, n_tok;      // tokens of the block (n_tok -1: no more pieces)
-  int32_t req;              // -1: a bad request, nothing is read
-  int32_t limit;            // the largest limit of the block's tokens
-  int32_t pg0, pg1;
-  int32_t slot;             // -1: the whole block, else the workspace slot 0 or 1
-  int32_t pad[5];
+  int4 a, b;
+  __device__ int tok0() const { return a.x; }
+  __device__ int n_tok() const { return a.y; }
+  __device__ int req() const { return a.z; }
+  __device__ int limit() const { return a.w; }
+  __device__ int pg0() const { return b.x; }
+  __device__ int pg1() const { return b.y; }
+  __device__ int slot() const { return b.z; }
 };
-static_assert(sizeof(Piece) == CK_PIECE_BYTES, "piece size");
+
+// One tile in its ring, two 16-byte words: the address of its 64 rows (8 bytes), how many of
+// them some token sees (-1: no more tiles), whether it begins a piece; then the piece's tok0
+// and n_tok.
 
 // Named barrier over n threads that ORs `flag` across them: a role whose threads saw a wait
 // run out stops as one, and no thread is left behind at a barrier.
@@ -152,40 +168,60 @@ __device__ __forceinline__ bool bar_any(int id, int n, bool flag) {
 __device__ __forceinline__ void arrive_local(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// Arrive on a barrier of either CTA of the pair (cluster address), releasing to the cluster.
+// Arrive on a barrier of either CTA of the pair (cluster address). What the arrival announces
+// (operands, scores read) lies in the arriving CTA's own shared or tensor memory, made visible
+// there by the proxy and tcgen05 fences before it, and is read there by the tensor core: no
+// data crosses the pair through this barrier, and the default scope is enough. A release at
+// cluster scope measured 1,400 cycles per arrival (four per tile).
 __device__ __forceinline__ void arrive_cluster(uint32_t cbar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cbar) : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cbar) : "memory");
 }
-__device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) {
+// Shared memory by 32-bit address: the aligned base is computed as an integer, from which the
+// compiler would make generic accesses with 64-bit addresses.
+__device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ void sts32(uint32_t a, uint32_t v) { asm volatile("st.shared.b32 [%0], %1;" ::"r"(a), "r"(v) : "memory"); }
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
       " selp.u32 %0, 1, 0, p;\n}\n"
       : "=r"(ok)
       : "r"(bar), "r"(parity)
       : "memory");
   return ok != 0;
 }
-// Bounded wait for a phase, with the ordering of the whole pair: false after `seconds` (or
+// Bounded wait for a phase: false after `seconds` (or
 // when another role of this CTA gave up), with HS_ERR_TIMEOUT recorded.
-__device__ __noinline__ bool ck_wait_slow(uint32_t bar, uint32_t parity, int32_t* status, volatile int32_t* dead,
+__device__ __forceinline__ bool ck_wait_slow(uint32_t bar, uint32_t parity, int32_t* status, uint32_t dead,
                                           int seconds) {
   const uint64_t t0 = globaltimer();
   for (uint32_t it = 1;; ++it) {
-    if (try_wait_cluster(bar, parity)) return true;
+    if (try_wait(bar, parity)) return true;
     if ((it & 63u) == 0) {
-      if (*dead) return false;
+      if (lds32(dead)) return false;
       if (globaltimer() - t0 > (uint64_t)seconds * WAIT_NS) {
         set_status(status, HS_ERR_TIMEOUT);
-        *dead = 1;
+        sts32(dead, 1);
         return false;
       }
     }
   }
 }
-__device__ __forceinline__ bool ck_wait(uint32_t bar, uint32_t parity, int32_t* status, volatile int32_t* dead,
+__device__ __forceinline__ bool ck_wait(uint32_t bar, uint32_t parity, int32_t* status, uint32_t dead,
                                         int seconds = 2) {
-  if (try_wait_cluster(bar, parity)) return true;
+  if (try_wait(bar, parity)) return true;
   return ck_wait_slow(bar, parity, status, dead, seconds);
 }
 
@@ -197,12 +233,23 @@ __device__ __forceinline__ void tmem_alloc_pair(uint32_t dst_smem, uint32_t ncol
 __device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
   asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
-__device__ __forceinline__ void umma_f16_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                              uint32_t accumulate) {
+// One lane of a converged warp, the same at every call. The issuing loop runs on the whole
+// warp with warp-uniform operands and only the instruction itself is predicated: issued by
+// one lane of a diverged warp, each tcgen05.mma takes 57 cycles to issue (its descriptors
+// are moved to uniform registers one by one), against 25 that the smallest of them needs.
+__device__ __forceinline__ bool elect_lane() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n selp.u32 %0, 1, 0, e;\n}\n" : "=r"(p));
+  return p != 0;
+}
+// The operands are the low words of their descriptors (address / 16, leading offset); the
+// high word is the same for all.
+__device__ __forceinline__ void umma_f16_pair(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t desc_hi,
+                                              uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.b32 p, %5, 0;\n mov.b64 a, {%1, %3};\n mov.b64 b, {%2, %3};\n"
+      " tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %4, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(desc_hi), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 // Arrive on the barrier at this offset in both CTAs once every MMA issued so far completes.
@@ -216,17 +263,21 @@ __device__ __forceinline__ void umma_commit_pair(uint32_t bar) {
 __device__ __forceinline__ void umma_commit_own(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+          taddr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// The larger of two, NaN when either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
 __device__ __forceinline__ float ex2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -238,43 +289,28 @@ __device__ __forceinline__ uint32_t h2_bits(__half2 h) { return *reinterpret_cas
 __device__ __forceinline__ __half2 e4m3x2_to_h2(uint32_t two) {
   return __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3));
 }
-// Bytes 0x7F and 0xFF (NaN) of four codes become zero.
-__device__ __forceinline__ uint32_t drop_nan4(uint32_t w) {
-  const uint32_t m = __vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-  return w & ~m;
-}
-__device__ __forceinline__ bool any_nan(uint4 v) {
-  const uint32_t k = 0x7F7F7F7Fu, one = 0x01010101u;
-  return (((((v.x & k) + one) | ((v.y & k) + one)) | (((v.z & k) + one) | ((v.w & k) + one))) & 0x80808080u) != 0;
-}
 __device__ __forceinline__ void codes_to_f16(uint4 v, uint4& lo, uint4& hi) {
   lo = make_uint4(h2_bits(e4m3x2_to_h2(v.x & 0xFFFFu)), h2_bits(e4m3x2_to_h2(v.x >> 16)),
                   h2_bits(e4m3x2_to_h2(v.y & 0xFFFFu)), h2_bits(e4m3x2_to_h2(v.y >> 16)));
   hi = make_uint4(h2_bits(e4m3x2_to_h2(v.z & 0xFFFFu)), h2_bits(e4m3x2_to_h2(v.z >> 16)),
                   h2_bits(e4m3x2_to_h2(v.w & 0xFFFFu)), h2_bits(e4m3x2_to_h2(v.w >> 16)));
 }
-// A scale for code x scale in fp16 with one rounding: 64 x scale in two fp16 parts, to be
-// multiplied by code / 64 (exact). Below 2^-14 the parts lose bits and fp32 is used.
+// code x scale in fp16, rounded once: 256 x scale in two fp16 parts times code / 256 (both
+// exact products of the code; |scale| < 146 keeps the first part finite). A NaN code becomes
+// a finite value: its row's scores are NaN, so it is not seen, and 0 x it has to be 0.
 struct VScale {
   __half2 hi, lo;
-  float s;
 };
 __device__ __forceinline__ VScale v_scale(float s) {
   VScale r;
-  r.s = s;
-  const __half h = __float2half_rn(64.f * s);
+  const __half h = __float2half_rn(256.f * s);
   r.hi = __half2half2(h);
-  r.lo = __half2half2(__float2half_rn(64.f * s - __half2float(h)));
+  r.lo = __half2half2(__float2half_rn(256.f * s - __half2float(h)));
   return r;
 }
 __device__ __forceinline__ uint32_t scaled2(uint32_t two, const VScale& v) {
-  const __half2 c = e4m3x2_to_h2(two);
-  if (fabsf(v.s) >= 6.103515625e-05f) {
-    const __half2 c64 = __hmul2(c, __half2half2(__float2half_rn(0.015625f)));
-    return h2_bits(__hfma2(c64, v.hi, __hmul2(c64, v.lo)));
-  }
-  const float2 f = __half22float2(c);
-  return h2_bits(__floats2half2_rn(f.x * v.s, f.y * v.s));
+  const __half2 c = __hmul2(e4m3x2_to_h2(two), __half2half2(__ushort_as_half(0x1C00)));   // 2^-8
+  return h2_bits(__hmin2(__hfma2(c, v.hi, __hmul2(c, v.lo)), __half2half2(__ushort_as_half(0x7BFF))));
 }
 __device__ __forceinline__ void codes_to_scaled_f16(uint4 v, const VScale& s, uint4& lo, uint4& hi) {
   lo = make_uint4(scaled2(v.x & 0xFFFFu, s), scaled2(v.x >> 16, s), scaled2(v.y & 0xFFFFu, s), scaled2(v.y >> 16, s));
@@ -288,16 +324,6 @@ __device__ __forceinline__ uint4 bf16x8_to_f16(uint4 v, bool* bad) {
   for (int i = 0; i < 4; ++i) {
     o[i] = h2_bits(__floats2half2_rn(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u)));
     *bad |= (o[i] & 0x7C00u) == 0x7C00u || (o[i] & 0x7C000000u) == 0x7C000000u;
-  }
-  return make_uint4(o[0], o[1], o[2], o[3]);
-}
-// fp16 infinities and NaN of eight values become zero.
-__device__ __forceinline__ uint4 drop_inf8(uint4 v) {
-  uint32_t o[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if ((o[i] & 0x7C00u) == 0x7C00u) o[i] &= 0xFFFF0000u;
-    if ((o[i] & 0x7C000000u) == 0x7C000000u) o[i] &= 0xFFFFu;
   }
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
@@ -323,7 +349,7 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 }
 
 // ---- the plan -------------------------------------------------------------------------
-// Inclusive scan over the CTA's 448 threads (sum or maximum); tmp: 32 ints; returns the
+// Inclusive scan over the CTA's threads (sum or maximum); tmp: 32 ints; returns the
 // inclusive value, *total the whole.
 template <bool MAX>
 __device__ __forceinline__ int block_scan(int v, int* tmp, int* total) {
@@ -412,7 +438,7 @@ __device__ Range plan_range(const Dev& D, const ChunkArgs& A, int pair, int tpb,
   }
   if (tid == 0) blk[A.n_seg] = n_blocks;
   __syncthreads();
-  // the tiles of 448 blocks at a time
+  // the tiles of as many blocks at a time as the CTA has threads
   auto segment_of = [&](int b) {   // the last segment whose first block is <= b (never an empty one)
     int l = 0, h = A.n_seg;
     while (h - l > 1) {
@@ -475,74 +501,75 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
   // at the same offset in both CTAs: the dynamic shared memory of one kernel starts at one address
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
-  float* scl = reinterpret_cast<float*>(smem + CK_OFF_SCL);
-  float* red = reinterpret_cast<float*>(smem + CK_OFF_RED);
-  Piece* ring = reinterpret_cast<Piece*>(smem + CK_OFF_RING);
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + CK_OFF_MISC);
-  volatile int32_t* dead = reinterpret_cast<int32_t*>(smem + CK_OFF_MISC) + 1;
+  const uint32_t tslot = sbase + CK_OFF_MISC, dead = tslot + 4;
   int32_t* found = reinterpret_cast<int32_t*>(smem + CK_OFF_MISC) + 2;
-  int32_t* there = reinterpret_cast<int32_t*>(smem + CK_OFF_MISC) + 8;   // [CK_SCL] whether a tile's page exists
+  const uint32_t there = sbase + CK_OFF_MISC + 32;   // int [CK_SCL]: whether a tile's page exists
   auto bar = [&](int i) { return sbase + CK_OFF_BAR + 8 * i; };
+  auto piece_at = [&](uint32_t slot) {
+    const uint32_t at = sbase + CK_OFF_RING + slot * CK_PIECE_BYTES;
+    const uint4 a = lds128(at), b = lds128(at + 16);
+    return Piece{make_int4(a.x, a.y, a.z, a.w), make_int4(b.x, b.y, b.z, b.w)};
+  };
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = blockIdx.x & 1;
   const int pair = blockIdx.x >> 1;
   const int H = D.n_heads, tpb = CK_ROWS / H;
 
-  if (warp == CK_MMA_WARP) tmem_alloc_pair(smem_u32(tslot), 512);
+  if (warp == CK_MMA_WARP) tmem_alloc_pair(tslot, 512);
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(B_KF + i), 2 * CK_CONV_WARPS);
       mbar_init(bar(B_VF + i), 2 * CK_CONV_WARPS);
-      mbar_init(bar(B_PF + i), 2 * 4);
+      mbar_init(bar(B_PF + i), 2 * CK_SM_WARPS);
       mbar_init(bar(B_SD + i), 1);
       mbar_init(bar(B_PD + i), 1);
     }
-    mbar_init(bar(B_SR), 2 * 4);
+    for (int i = 0; i < CK_SCL; ++i) mbar_init(bar(B_SC + i), 2);
+    mbar_init(bar(B_SR), 2 * CK_SM_WARPS);
     mbar_init(bar(B_FIN), 1);
     for (int i = 0; i < CK_RING; ++i) {
       mbar_init(bar(B_RF + i), 1);
-      mbar_init(bar(B_RE + i), CK_CONV_WARPS + 4 + (rank == 0 ? 1 : 0));
+      mbar_init(bar(B_RE + i), CK_SM_WARPS + (rank == 0 ? 1 : 0));
+    }
+    for (int i = 0; i < CK_TILES; ++i) {
+      mbar_init(bar(B_TF + i), 1);
+      mbar_init(bar(B_TE + i), 2 * CK_CONV_WARPS);
     }
     fence_mbar_init();
-    *dead = 0;
+    sts32(dead, 0);
   }
   tc_fence_before();
   cluster_sync();
   tc_fence_after();
-  const uint32_t tmem = *tslot;
+  const uint32_t tmem = lds32(tslot);
   griddep_wait();
   griddep_launch();   // only the merge of this call depends on it, and waits for its end
 
   const Range R = plan_range(D, A, pair, tpb, smem, found);
   __syncthreads();   // the plan's arrays are done with
-  const ChunkWork W = work_at(A.work, A.pairs);
 
   if (warp == CK_PLAN_WARP) {
     // ------------------------------- pieces of the range -------------------------------
     int seg = R.seg, t0 = R.tok0, seg_end = R.seg_t1, page = R.page, left = R.n, at = R.at;
-    uint32_t k = 0;
+    uint32_t k = 0, t = 0;
+    int entries = -1;
+    const uint8_t* const kv = D.kv[A.layer];
     ChunkCut cut = {0, 0, 0, 0};
     bool ok = true;
     for (;; ++k) {
-      Piece p = {};
-      p.n_tok = -1;
+      int4 pa = make_int4(0, -1, -1, 0), pb = make_int4(0, 0, -1, 0);
       if (left > 0) {
         const int t1 = min(t0 + tpb, seg_end);
         const int r = __ldg(A.seg_req + seg);
         bool bad = r < 0 || r >= D.max_requests, ignore = false;
         const int lim = block_limit(D, A.limit, t0, t1, &ignore), n_pages = pages_of(lim);
         if (bad && lane == 0) set_status(D.status, HS_ERR_BAD_ID);
-        p.tok0 = t0;
-        p.n_tok = t1 - t0;
-        p.req = bad ? -1 : r;
-        p.limit = bad ? 0 : lim;
-        p.pg0 = page;
-        p.pg1 = min(n_pages, page + left);
-        const bool first = page == 0, last = p.pg1 == n_pages;
-        p.slot = first && last ? -1 : first ? 1 : 0;
-        if (first && !last) cut = {t0, p.n_tok, (at + n_pages - 1) / R.per_pair, 0};
-        const int used = p.pg1 - p.pg0;
+        const int p1 = min(n_pages, page + left), used = p1 - page;
+        const bool whole = page == 0 && p1 == n_pages;
+        pa = make_int4(t0, t1 - t0, bad ? -1 : r, bad ? 0 : lim);
+        pb = make_int4(page, p1, whole ? -1 : page == 0 ? 1 : 0, 0);
+        if (page == 0 && !whole) cut = {t0, t1 - t0, (at + n_pages - 1) / R.per_pair, 0};
         left -= used;
         at += used;
         page = 0;
@@ -558,315 +585,390 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
       if (k >= CK_RING) ok = ck_wait(bar(B_RE + slot), (k / CK_RING - 1) & 1, D.status, dead, 30);
       if (!ok) break;
       if (lane == 0) {
-        ring[slot] = p;
+        const uint32_t dst = sbase + CK_OFF_RING + slot * CK_PIECE_BYTES;
+        sts128(dst, make_uint4(pa.x, pa.y, pa.z, pa.w));
+        sts128(dst + 16, make_uint4(pb.x, pb.y, pb.z, pb.w));
         arrive_local(bar(B_RF + slot));
       }
       __syncwarp();
-      if (p.n_tok < 0) break;
+      for (int pg = pb.x; pg < pb.y || pa.y < 0; ++pg, ++t) {
+        const uint32_t ts = t % CK_TILES, dst = sbase + CK_OFF_TILES + ts * CK_PIECE_BYTES;
+        if (((pg - pb.x) & 31) == 0)   // 32 block-table entries at a time, one per lane
+          entries = pa.z >= 0 && pg + lane < pb.y ? __ldg(D.bt + (size_t)pa.z * D.max_pages + pg + lane) : -1;
+        const int entry = __shfl_sync(0xffffffffu, entries, (pg - pb.x) & 31);
+        int n_rows = pa.y < 0 ? -1 : pa.z >= 0 ? max(0, min(PAGE, pa.w - pg * PAGE)) : 0;
+        const uint8_t* rows = kv;
+        if (n_rows > 0) {
+          if (entry >= 0 && entry < D.num_pages) {
+            rows = kv + (size_t)entry * PAGE * ROW;
+          } else {
+            int err = HS_OK;
+            rows = page_rows(D, A.layer, pa.z, pg, &err);
+            if (!rows) {
+              if (lane == 0) set_status(D.status, err);
+              n_rows = 0;
+            }
+          }
+        }
+        if (t >= CK_TILES) ok = ck_wait(bar(B_TE + ts), (t / CK_TILES - 1) & 1, D.status, dead, 30);
+        if (!ok) break;
+        if (lane == 0) {
+          const uint64_t at = reinterpret_cast<uint64_t>(rows);
+          sts128(dst, make_uint4((uint32_t)at, (uint32_t)(at >> 32), (uint32_t)n_rows, pg == pb.x));
+          sts128(dst + 16, make_uint4(pa.x, pa.y, 0, 0));
+          arrive_local(bar(B_TF + ts));
+        }
+        __syncwarp();
+        if (pa.y < 0) break;
+      }
+      if (!ok || pa.y < 0) break;
     }
-    if (lane == 0 && rank == 0) W.cut[pair] = cut;
+    if (lane == 0 && rank == 0) work_at(A.work, A.pairs).cut[pair] = cut;
   } else if (warp == CK_MMA_WARP) {
     // ---------------------------------- MMA issue ----------------------------------
-    if (rank == 0 && lane == 0) {
+    if (rank == 0) {
       const uint32_t idesc_qk = idesc_f16(128, 64, false, false, false);
       const uint32_t idesc_pv = idesc_f16(128, 256, false, true, false);
-      const uint32_t q0 = sbase + CK_OFF_Q, k0 = sbase + CK_OFF_K, v0 = sbase + CK_OFF_V, p0 = sbase + CK_OFF_P;
+      const uint32_t base = __shfl_sync(0xffffffffu, sbase, 0), tm = __shfl_sync(0xffffffffu, tmem, 0);
+      // low words of the descriptors of the operands' first parts; steps add address / 16
+      const uint32_t hi = (uint32_t)(smem_desc_sw128(0, 0, 1024) >> 32);
+      uint32_t qd = (uint32_t)smem_desc_sw128(base + CK_OFF_Q, 16, 1024), kd = (uint32_t)smem_desc_sw128(base + CK_OFF_K, 16, 1024);
+      uint32_t pd = (uint32_t)smem_desc_sw128(base + CK_OFF_P, 16, 1024), vd = (uint32_t)smem_desc_sw128(base + CK_OFF_V, CK_VATOM, 1024);
       uint32_t it = 0;
       bool ok = true;
       for (uint32_t k = 0; ok; ++k) {
         const uint32_t slot = k % CK_RING;
-        if (!ck_wait(bar(B_RF + slot), (k / CK_RING) & 1, D.status, dead, 30)) break;
-        const int n_tok = ring[slot].n_tok, n = ring[slot].pg1 - ring[slot].pg0;
-        arrive_local(bar(B_RE + slot));
+        ok = __all_sync(0xffffffffu, ck_wait(bar(B_RF + slot), (k / CK_RING) & 1, D.status, dead, 30));
+        if (!ok) break;
+        const Piece p = piece_at(slot);
+        const int n_tok = __shfl_sync(0xffffffffu, p.n_tok(), 0), n = __shfl_sync(0xffffffffu, p.pg1() - p.pg0(), 0);
+        if (lane == 0) arrive_local(bar(B_RE + slot));
+        __syncwarp();
         if (n_tok < 0) break;
-        for (int i = 0; i <= n && ok; ++i) {
+        for (int i = 0; i <= n; ++i) {
           if (i < n) {
             const uint32_t t = it + i, st = t & 1;
             ok = ck_wait(bar(B_KF + st), (t >> 1) & 1, D.status, dead);
-            if (ok && t > 0) ok = ck_wait(bar(B_SR), (t - 1) & 1, D.status, dead);
+            if (ok && i == 0) ok = ck_wait(bar(B_VF + st), (t >> 1) & 1, D.status, dead);   // the other half of Q
+            ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t kb = k0 + st * CK_KSTAGE;
-#pragma unroll
-            for (int g = 0; g < 5; ++g)
+            asm volatile("" : "+r"(qd), "+r"(kd));   // the 36 descriptors are added up here, not kept in registers
+            const uint32_t ks = kd + st * (CK_KSTAGE / 16);
+            auto qk = [&](int g) {
 #pragma unroll
               for (int kk = 0; kk < (g < 4 ? 8 : 4); ++kk) {
                 const int atom = 2 * g + (kk >> 2);
-                umma_f16_pair(tmem + CK_TM_S + g * 32, smem_desc_sw128(q0 + atom * CK_QATOM + (kk & 3) * 32, 16, 1024),
-                              smem_desc_sw128(kb + atom * CK_KATOM + (kk & 3) * 32, 16, 1024), idesc_qk, kk > 0);
+                umma_f16_pair(tm + CK_TM_S + ((5 * t + g) & 7) * 32, qd + (atom * CK_QATOM + (kk & 3) * 32) / 16,
+                              ks + (atom * CK_KATOM + (kk & 3) * 32) / 16, hi, idesc_qk, kk > 0);
               }
-            umma_commit_pair(bar(B_SD + st));
+            };
+            if (elect_lane()) {
+              qk(0);
+              qk(1);
+              qk(2);
+            }
+            __syncwarp();
+            // the other two take accumulators of the tile before, once its scores have been read
+            if (t > 0) ok = __all_sync(0xffffffffu, ck_wait(bar(B_SR), (t - 1) & 1, D.status, dead));
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_lane()) {
+              qk(3);
+              qk(4);
+              umma_commit_pair(bar(B_SD + st));
+            }
+            __syncwarp();
           }
           if (i > 0) {
             const uint32_t t = it + i - 1, st = t & 1;
             ok = ck_wait(bar(B_VF + st), (t >> 1) & 1, D.status, dead) &&
                  ck_wait(bar(B_PF + st), (t >> 1) & 1, D.status, dead);
+            ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t vb = v0 + st * CK_VSTAGE;
+            asm volatile("" : "+r"(pd), "+r"(vd));
+            const uint32_t vs = vd + st * (CK_VSTAGE / 16);
+            const uint32_t add = i > 1 ? 1u : 0u;
+            if (elect_lane()) {
 #pragma unroll
-            for (int g = 0; g < 2; ++g)
+              for (int g = 0; g < 2; ++g)
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                umma_f16_pair(tmem + CK_TM_O + g * 128, smem_desc_sw128(p0 + kk * 32, 16, 1024),
-                              smem_desc_sw128(vb + g * 2 * CK_VATOM + kk * 2048, CK_VATOM, 1024), idesc_pv,
-                              (i > 1 || kk > 0) ? 1u : 0u);
-            umma_commit_pair(bar(B_PD + st));
+                for (int kk = 0; kk < 4; ++kk)
+                  umma_f16_pair(tm + CK_TM_O + g * 128, pd + kk * 2, vs + (g * 2 * CK_VATOM + kk * 2048) / 16, hi, idesc_pv,
+                                kk > 0 ? 1u : add);
+              umma_commit_pair(bar(B_PD + st));
+            }
+            __syncwarp();
           }
         }
         it += n;
       }
     }
-  } else if (warp >= CK_CONV_WARP0) {
+  } else if (warp >= CK_K_WARP0) {
     // ------------------------------ cache rows to operands ------------------------------
-    const int ct = tid - CK_CONV_WARP0 * 32;
-    const uint32_t kf0 = mapa(bar(B_KF), 0), vf0 = mapa(bar(B_VF), 0);   // the first CTA's
-    // 16-byte parts of a row: this thread has part `part` (a 128-value group is 8 parts) of
-    // the rows 8 k + row0 of its CTA's half page; 8 neighbouring threads store 4 parts of two
-    // rows, which the swizzle puts on 8 different bank groups
-    const int part = 4 * ((ct >> 3) & 7) + (ct & 3), row0 = 2 * (ct >> 6) + ((ct >> 2) & 1);
-    const int grp = part >> 3;
-    // V needs the groups `rank` and 2 + rank of all 64 rows: a thread of such a group takes its
-    // own rows again, the others take the neighbour group's part of the other half page
-    const bool own_v = (grp & 1) == (int)rank;
-    const int part_v = own_v ? part : part ^ 8, grp_v = part_v >> 3;
-    const int half_v = own_v ? (int)rank : 1 - (int)rank;
-    const int rope_row = ct >> 3, rope_part = ct & 7;
-    const uint32_t k_dst = (uint32_t)((part >> 2) * CK_KATOM), v_dst = (uint32_t)((grp_v >> 1) * 2 * CK_VATOM + ((part_v >> 2) & 1) * CK_VATOM);
-    const int chunk = (part & 3) * 2;
-    uint4 own[4], oth[4], rope;
-    float vsc[4];
-    float4 sc4;
+    const bool is_k = warp < CK_V_WARP0;
+    const int ct = tid - (is_k ? CK_K_WARP0 : CK_V_WARP0) * 32;
     bool bad_range = false;
-
-    Piece P;
-    uint32_t kp = 0, it = 0;
-    int page = 0;
+    // the tile whose rows are in registers
+    uint32_t it = 0;
     const uint8_t* rows = nullptr;
-    int next_pg = -1;                       // block-table entry of the page after `page`
-    auto fetch_entry = [&](int pg) {
-      next_pg = -1;
-      if (P.req >= 0 && pg < P.pg1) next_pg = __ldg(D.bt + (size_t)P.req * D.max_pages + pg);
+    int n_rows = 0;
+    bool more = true, first = true;         // first: it begins a piece
+    auto advance = [&](uint32_t t) {
+      const uint32_t ts = t % CK_TILES;
+      more = __all_sync(0xffffffffu, ck_wait(bar(B_TF + ts), (t / CK_TILES) & 1, D.status, dead, 30));
+      if (!more) return;
+      const uint4 x = lds128(sbase + CK_OFF_TILES + ts * CK_PIECE_BYTES);
+      rows = reinterpret_cast<const uint8_t*>((uint64_t)x.x | (uint64_t)x.y << 32);
+      n_rows = (int)x.z;
+      first = x.w != 0;
+      more = n_rows >= 0;
     };
-    auto base_of = [&](int entry, int pg) -> const uint8_t* {
-      if (P.req < 0 || pg * PAGE >= P.limit) return nullptr;   // nothing is seen
-      if (entry >= 0 && entry < D.num_pages) return D.kv[A.layer] + (size_t)entry * PAGE * ROW;
-      int err = HS_OK;
-      const uint8_t* b = page_rows(D, A.layer, P.req, pg, &err);
-      if (!b) set_status(D.status, err);
-      return b;
-    };
-    auto issue = [&]() {                    // loads of the tile (P, page)
-      const int nv = rows ? min(PAGE, P.limit - page * PAGE) : 0;   // rows some token sees
-      const uint4 z = make_uint4(0, 0, 0, 0);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int r = (int)rank * 32 + 8 * k + row0;
-        own[k] = r < nv ? __ldg(reinterpret_cast<const uint4*>(rows + (size_t)r * ROW) + part) : z;
-      }
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int r = half_v * 32 + 8 * k + row0;
-        oth[k] = !own_v && r < nv ? __ldg(reinterpret_cast<const uint4*>(rows + (size_t)r * ROW) + part_v) : z;
-        vsc[k] = r < nv ? __ldg(reinterpret_cast<const float*>(rows + (size_t)r * ROW + LATENT) + grp_v) : 0.f;
-      }
-      {
-        const int r = (int)rank * 32 + rope_row;
-        rope = r < nv ? __ldg(reinterpret_cast<const uint4*>(rows + (size_t)r * ROW) + 33 + rope_part) : z;
-      }
-      if (ct < PAGE) {
-        sc4 = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (ct < nv) sc4 = __ldg(reinterpret_cast<const float4*>(rows + (size_t)ct * ROW + LATENT));
-      }
+    // the tile's entry is not needed any more
+    auto passed = [&](uint32_t t) {
+      __syncwarp();
+      if (lane == 0) arrive_local(bar(B_TE + t % CK_TILES));
     };
     auto good_scale = [&](float s) {
       if (fabsf(s) < CK_MAX_SCALE) return s;
       bad_range = true;
       return 0.f;
     };
-    auto take_piece = [&]() {               // the next piece, if there is one
-      const uint32_t slot = kp % CK_RING;
-      if (!ck_wait(bar(B_RF + slot), (kp / CK_RING) & 1, D.status, dead, 30)) return false;
-      P = ring[slot];
-      __syncwarp();
-      if (lane == 0) arrive_local(bar(B_RE + slot));
-      ++kp;
-      if (P.n_tok < 0) return false;
-      page = P.pg0;
-      fetch_entry(page);
-      rows = base_of(next_pg, page);
-      fetch_entry(page + 1);
-      issue();
+    // Half of Q's 64 rows (K's warps the first, V's the second), once the products of the previous
+    // piece have read theirs: copied as they are, then each thread converts what it copied.
+    auto load_q = [&](int r0) {
+      if (it > 0 && !ck_wait(bar(B_SD + ((it - 1) & 1)), ((it - 1) >> 1) & 1, D.status, dead)) return false;
+      const T* q = static_cast<const T*>(A.q);
+      const uint4 x = lds128(sbase + CK_OFF_TILES + it % CK_TILES * CK_PIECE_BYTES + 16);
+      const int tok0 = (int)x.x, n_tok = (int)x.y;
+#pragma unroll 2
+      for (int k = 0; k < 18; ++k) {
+        const int c = ct + k * CK_CONV, r = r0 + c / 72, ch = c % 72;
+        const int gr = (int)rank * CK_HALF + r, tk = gr / H, h = gr - tk * H;
+        const uint32_t dst = sbase + CK_OFF_Q + (ch >> 3) * CK_QATOM + sw128_chunk(r, ch & 7);
+        if (tk < n_tok) {
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst),
+                       "l"(q + (tok0 + tk) * A.q_tok + h * A.q_head + ch * 8)
+                       : "memory");
+        } else {
+          sts128(dst, make_uint4(0, 0, 0, 0));
+        }
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+#pragma unroll 2
+      for (int k = 0; k < 18; ++k) {
+        const int c = ct + k * CK_CONV, r = r0 + c / 72, ch = c % 72;
+        const uint32_t dst = sbase + CK_OFF_Q + (ch >> 3) * CK_QATOM + sw128_chunk(r, ch & 7);
+        sts128(dst, q_to_f16<T>(lds128(dst), &bad_range));
+      }
       return true;
     };
-    bool first = true;
-    bool more = take_piece();
-    while (more) {
-      const uint32_t st = it & 1;
-      if (first) {
-        // Q of the block's rows, once the products of the previous piece have read theirs
-        if (it > 0 && !ck_wait(bar(B_SD + ((it - 1) & 1)), ((it - 1) >> 1) & 1, D.status, dead)) break;
-        const T* q = static_cast<const T*>(A.q);
-#pragma unroll 1
-        for (int b = 0; b < 2; ++b) {
-          uint4 v[9];
+    auto ld16 = [&](const uint8_t* at) { return __ldg(reinterpret_cast<const uint4*>(at)); };
+    const uint4 z = make_uint4(0, 0, 0, 0);
+    if (is_k) {
+      // 16-byte parts of a row: this thread has part `part` (16 codes) of the rows 4 k + row0 of its
+      // CTA's half page; 8 neighbouring threads store 4 parts of two rows, which the swizzle
+      // puts on 8 different bank groups. The two 16-byte chunks of a part differ in address
+      // bit 4, the rows 4 apart in bit 6 besides their distance of 512.
+      const uint32_t kf0 = mapa(bar(B_KF), 0);   // the first CTA's
+      const int part = 4 * ((ct >> 3) & 7) + (ct & 3), row0 = 2 * (ct >> 6) + ((ct >> 2) & 1);
+      const int base_row = (int)rank * 32, rope_row = ct >> 3;
+      const uint32_t k_at = (part >> 2) * CK_KATOM + sw128_chunk(row0, (part & 3) * 2),
+                     rope_at = 8 * CK_KATOM + sw128_chunk(rope_row, ct & 7);
+      const uint32_t src = (base_row + row0) * ROW + part * 16, src_rope = (base_row + rope_row) * ROW + (33 + (ct & 7)) * 16,
+                     src_sc = (ct & 63) * ROW + LATENT;
+      uint4 own[8], rope[2], sc = z;
+      auto load = [&]() {
+        advance(it);
+        if (!more) return;
+        if (n_rows == PAGE) {
 #pragma unroll
-          for (int k = 0; k < 9; ++k) {
-            const int c = ct + (b * 9 + k) * CK_CONV, r = c / 72, ch = c - r * 72;
-            const int gr = (int)rank * CK_HALF + r, tk = gr / H, h = gr - tk * H;
-            v[k] = tk < P.n_tok ? __ldg(reinterpret_cast<const uint4*>(q + (P.tok0 + tk) * A.q_tok + h * A.q_head) + ch)
-                                : make_uint4(0, 0, 0, 0);
-          }
+          for (int k = 0; k < 8; ++k) own[k] = ld16(rows + src + k * 4 * ROW);
 #pragma unroll
-          for (int k = 0; k < 9; ++k) {
-            const int c = ct + (b * 9 + k) * CK_CONV, r = c / 72, ch = c - r * 72;
-            *reinterpret_cast<uint4*>(smem + CK_OFF_Q + (ch >> 3) * CK_QATOM + sw128_chunk(r, ch & 7)) =
-                q_to_f16<T>(v[k], &bad_range);
-          }
-        }
-        first = false;
-      }
-      // K, the rope and the scales
-      if (it >= 2 && !ck_wait(bar(B_SD + st), ((it - 2) >> 1) & 1, D.status, dead)) break;
-      uint8_t* kt = smem + CK_OFF_K + st * CK_KSTAGE;
+          for (int k = 0; k < 2; ++k) rope[k] = ld16(rows + src_rope + k * 16 * ROW);
+          if (ct < PAGE) sc = ld16(rows + src_sc);
+        } else {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (any_nan(own[k])) {
-          bad_range = true;
-          own[k] = make_uint4(drop_nan4(own[k].x), drop_nan4(own[k].y), drop_nan4(own[k].z), drop_nan4(own[k].w));
-        }
-        uint4 lo, hi;
-        codes_to_f16(own[k], lo, hi);
-        const int r = 8 * k + row0;
-        *reinterpret_cast<uint4*>(kt + k_dst + sw128_chunk(r, chunk)) = lo;
-        *reinterpret_cast<uint4*>(kt + k_dst + sw128_chunk(r, chunk + 1)) = hi;
-      }
-      {
-        bool bad = false;
-        uint4 v = bf16x8_to_f16(rope, &bad);
-        if (bad) {
-          bad_range = true;
-          v = drop_inf8(v);
-        }
-        *reinterpret_cast<uint4*>(kt + 8 * CK_KATOM + sw128_chunk(rope_row, rope_part)) = v;
-      }
-      if (ct < PAGE) {
-        float* s = scl + (it % CK_SCL) * 256 + ct;
-        s[0] = good_scale(sc4.x);
-        s[64] = good_scale(sc4.y);
-        s[128] = good_scale(sc4.z);
-        s[192] = good_scale(sc4.w);
-        if (ct == 0) there[it % CK_SCL] = rows != nullptr;
-      }
-      fence_proxy_async();
-      __syncwarp();
-      if (lane == 0) arrive_cluster(kf0 + 8 * st);
-      // V
-      if (it >= 2 && !ck_wait(bar(B_PD + st), ((it - 2) >> 1) & 1, D.status, dead)) break;
-      uint8_t* vt = smem + CK_OFF_V + st * CK_VSTAGE;
+          for (int k = 0; k < 8; ++k) own[k] = base_row + 4 * k + row0 < n_rows ? ld16(rows + src + k * 4 * ROW) : z;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        uint4 c = own[k];
-        if (!own_v) {
-          c = oth[k];
-          if (any_nan(c)) c = make_uint4(drop_nan4(c.x), drop_nan4(c.y), drop_nan4(c.z), drop_nan4(c.w));
+          for (int k = 0; k < 2; ++k) rope[k] = base_row + 16 * k + rope_row < n_rows ? ld16(rows + src_rope + k * 16 * ROW) : z;
+          if (ct < PAGE) sc = ct < n_rows ? ld16(rows + src_sc) : z;
         }
-        uint4 lo, hi;
-        codes_to_scaled_f16(c, v_scale(good_scale(vsc[k])), lo, hi);
-        const int r = half_v * 32 + 8 * k + row0;
-        *reinterpret_cast<uint4*>(vt + v_dst + sw128_chunk(r, chunk)) = lo;
-        *reinterpret_cast<uint4*>(vt + v_dst + sw128_chunk(r, chunk + 1)) = hi;
+      };
+      load();
+      while (more) {
+        const uint32_t st = it & 1;
+        if (first && !load_q(0)) break;
+        passed(it);
+        if (it >= 2 && !ck_wait(bar(B_SD + st), ((it - 2) >> 1) & 1, D.status, dead)) break;
+        if (ct < PAGE) {
+          const uint32_t x = sbase + CK_OFF_SCL + (it % CK_SCL) * CK_SCL_T + ct * 4;
+          sts32(x, __float_as_uint(good_scale(__uint_as_float(sc.x))));
+          sts32(x + CK_SCL_G, __float_as_uint(good_scale(__uint_as_float(sc.y))));
+          sts32(x + 2 * CK_SCL_G, __float_as_uint(good_scale(__uint_as_float(sc.z))));
+          sts32(x + 3 * CK_SCL_G, __float_as_uint(good_scale(__uint_as_float(sc.w))));
+          if (ct == 0) sts32(there + (it % CK_SCL) * 4, n_rows > 0);
+          __syncwarp();
+          if (lane == 0) arrive_local(bar(B_SC + it % CK_SCL));   // V's warps read the scales too
+        }
+        const uint32_t kt = sbase + CK_OFF_K + st * CK_KSTAGE, dst = kt + k_at;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          uint4 lo, hi;
+          codes_to_f16(own[k], lo, hi);
+          const uint32_t d = (dst + k * 512) ^ ((k & 1) * 64);
+          sts128(d, lo);
+          sts128(d ^ 16, hi);
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const uint32_t w[4] = {rope[k].x, rope[k].y, rope[k].z, rope[k].w};
+          uint32_t o[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            o[i] = h2_bits(__floats2half2_rn(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u)));
+          sts128(kt + rope_at + k * 2048, make_uint4(o[0], o[1], o[2], o[3]));
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) arrive_cluster(kf0 + 8 * st);
+        ++it;
+        load();
       }
-      fence_proxy_async();
-      __syncwarp();
-      if (lane == 0) arrive_cluster(vf0 + 8 * st);
-      ++it;
-      if (page + 1 < P.pg1) {
-        ++page;
-        rows = base_of(next_pg, page);
-        fetch_entry(page + 1);
-        issue();
-      } else {
-        more = take_piece();
-        first = true;
+    } else {
+      // part `part` of the groups 2 rank and 2 rank + 1 (16 parts in a row) of the rows 8 k + row0
+      const uint32_t vf0 = mapa(bar(B_VF), 0);
+      const int pv = 4 * ((ct >> 3) & 3) + (ct & 3), grp = 2 * (int)rank + (pv >> 3), part = 16 * (int)rank + pv;
+      const int row0 = 2 * (ct >> 5) + ((ct >> 2) & 1);
+      const uint32_t v_at = ((pv >> 3) * 2 + ((pv >> 2) & 1)) * CK_VATOM + sw128_chunk(row0, (pv & 3) * 2);
+      const uint32_t src = row0 * ROW + part * 16, sc_at = sbase + CK_OFF_SCL + grp * CK_SCL_G + row0 * 4;
+      uint4 val[8];
+      auto load = [&]() {
+        advance(it);
+        if (!more) return;
+        if (n_rows == PAGE) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) val[k] = ld16(rows + src + k * 8 * ROW);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) val[k] = 8 * k + row0 < n_rows ? ld16(rows + src + k * 8 * ROW) : z;
+        }
+      };
+      load();
+      while (more) {
+        const uint32_t st = it & 1;
+        if (first && !load_q(32)) break;
+        passed(it);
+        if (it >= 2 && !ck_wait(bar(B_PD + st), ((it - 2) >> 1) & 1, D.status, dead)) break;
+        if (!ck_wait(bar(B_SC + it % CK_SCL), (it / CK_SCL) & 1, D.status, dead)) break;
+        const uint32_t dst = sbase + CK_OFF_V + st * CK_VSTAGE + v_at, sc = sc_at + (it % CK_SCL) * CK_SCL_T;
+        uint32_t sv[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) sv[k] = lds32(sc + k * 32);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          uint4 lo, hi;
+          codes_to_scaled_f16(val[k], v_scale(__uint_as_float(sv[k])), lo, hi);
+          sts128(dst + k * 1024, lo);
+          sts128((dst + k * 1024) ^ 16, hi);
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) arrive_cluster(vf0 + 8 * st);
+        ++it;
+        load();
       }
     }
-    if (__any_sync(0xffffffffu, bad_range) && lane == 0) set_status(D.status, HS_ERR_RANGE);
+    if (bad_range) set_status(D.status, HS_ERR_RANGE);
   } else {
     // ------------------------------ softmax and output ------------------------------
-    const int row = tid & 63, half = tid >> 6;
-    const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
+    // four threads of a row: `half` (tensor-memory lanes 64 half ..) and `sub` (columns)
+    const int quad = warp & 3, sub = warp >> 2, half = quad >> 1, row = (quad & 1) * 32 + lane;
+    const int key0 = half * 32 + sub * 16;       // this thread's 16 keys of the page
+    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
+    const uint32_t s_col = lanes + CK_TM_S + sub * 16, o_col = lanes + CK_TM_O + sub * 128;
     const uint32_t pf0 = mapa(bar(B_PF), 0), sr0 = mapa(bar(B_SR), 0);
+    const uint32_t p_lo = sbase + CK_OFF_P + sw128_chunk(row, key0 >> 3),
+                   p_hi = sbase + CK_OFF_P + sw128_chunk(row, (key0 >> 3) + 1);
     const int gr = (int)rank * CK_HALF + row, tk = gr / H, h = gr - tk * H;
+    const uint32_t red_row = sbase + CK_OFF_RED + row * 4, red_mine = red_row + (half * 2 + sub) * 256;
+    auto red_at = [&](uint32_t at) { return __uint_as_float(lds32(at)); };
     uint32_t it = 0;
-    bool ok = true, dead_all = false;
+    bool ok = true, dead_all = false, bad_range = false;
     for (uint32_t kp = 0;; ++kp) {
       const uint32_t slot = kp % CK_RING;
       ok &= ck_wait(bar(B_RF + slot), (kp / CK_RING) & 1, D.status, dead, 30);
-      if (bar_any(1, 128, !ok)) break;
-      const Piece P = ring[slot];
+      if (bar_any(1, CK_SM, !ok)) break;
+      const Piece P = piece_at(slot);
       __syncwarp();
       if (lane == 0) arrive_local(bar(B_RE + slot));
-      if (P.n_tok < 0) break;
-      const bool live = tk < P.n_tok;
+      if (P.n_tok() < 0) break;
+      const bool live = tk < P.n_tok();
       int lim = 0;
-      if (live && P.req >= 0) {
+      if (live && P.req() >= 0) {
         bool ignore = false;
-        lim = clamp_limit(D, __ldg(A.limit + P.tok0 + tk), &ignore);
+        lim = clamp_limit(D, __ldg(A.limit + P.tok0() + tk), &ignore);
       }
-      float m = -INFINITY, l = 0.f;   // the row's reference (both halves alike), this half's sum
-      for (int pg = P.pg0; pg < P.pg1; ++pg, ++it) {
+      float m = -INFINITY, l = 0.f;   // the row's reference (its four threads alike), this thread's sum
+      for (int pg = P.pg0(); pg < P.pg1(); ++pg, ++it) {
         const uint32_t st = it & 1;
         ok &= ck_wait(bar(B_SD + st), (it >> 1) & 1, D.status, dead);
         tc_fence_after();
-        const float* sc = scl + (it % CK_SCL) * 256 + half * 32;
-        float s[32];
+        const uint32_t sc = sbase + CK_OFF_SCL + (it % CK_SCL) * CK_SCL_T + key0 * 4;
+        float s[16];
+#pragma unroll
+        for (int g = 0; g < 4; g += 2) {
+          uint32_t a[16], b[16];
+          tmem_ld16(s_col + ((5 * it + g) & 7) * 32, a);
+          tmem_ld16(s_col + ((5 * it + g + 1) & 7) * 32, b);
+          tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 16; j += 4) {
+            const uint4 x = lds128(sc + g * CK_SCL_G + j * 4), y = lds128(sc + (g + 1) * CK_SCL_G + j * 4);
+            const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float u = __uint_as_float(xs[i]), w = __uint_as_float(ys[i]);
+              const float v = g == 0 ? u * __uint_as_float(a[j + i]) : fmaf(u, __uint_as_float(a[j + i]), s[j + i]);
+              s[j + i] = fmaf(w, __uint_as_float(b[j + i]), v);
+            }
+          }
+        }
         {
-          uint32_t a[32], b[32];
-          tmem_ld32(lanes + CK_TM_S, a);
-          tmem_ld32(lanes + CK_TM_S + 32, b);
+          uint32_t a[16];
+          tmem_ld16(s_col + ((5 * it + 4) & 7) * 32, a);
           tmem_wait_ld();
 #pragma unroll
-          for (int j = 0; j < 32; j += 4) {
-            const float4 x = *reinterpret_cast<const float4*>(sc + j), y = *reinterpret_cast<const float4*>(sc + 64 + j);
-            s[j] = x.x * __uint_as_float(a[j]) + y.x * __uint_as_float(b[j]);
-            s[j + 1] = x.y * __uint_as_float(a[j + 1]) + y.y * __uint_as_float(b[j + 1]);
-            s[j + 2] = x.z * __uint_as_float(a[j + 2]) + y.z * __uint_as_float(b[j + 2]);
-            s[j + 3] = x.w * __uint_as_float(a[j + 3]) + y.w * __uint_as_float(b[j + 3]);
-          }
-          tmem_ld32(lanes + CK_TM_S + 64, a);
-          tmem_ld32(lanes + CK_TM_S + 96, b);
-          tmem_wait_ld();
-#pragma unroll
-          for (int j = 0; j < 32; j += 4) {
-            const float4 x = *reinterpret_cast<const float4*>(sc + 128 + j), y = *reinterpret_cast<const float4*>(sc + 192 + j);
-            s[j] += x.x * __uint_as_float(a[j]) + y.x * __uint_as_float(b[j]);
-            s[j + 1] += x.y * __uint_as_float(a[j + 1]) + y.y * __uint_as_float(b[j + 1]);
-            s[j + 2] += x.z * __uint_as_float(a[j + 2]) + y.z * __uint_as_float(b[j + 2]);
-            s[j + 3] += x.w * __uint_as_float(a[j + 3]) + y.w * __uint_as_float(b[j + 3]);
-          }
-          tmem_ld32(lanes + CK_TM_S + 128, a);
-          tmem_wait_ld();
-#pragma unroll
-          for (int j = 0; j < 32; ++j) s[j] = (s[j] + __uint_as_float(a[j])) * A.scale_log2;
+          for (int j = 0; j < 16; ++j) s[j] = (s[j] + __uint_as_float(a[j])) * A.scale_log2;
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) arrive_cluster(sr0);   // the score accumulators may be written again
-        const int seen = there[it % CK_SCL] ? lim - pg * PAGE - half * 32 : 0;   // of this thread's 32 keys
-        if (seen < 32) {
+        const int seen = lds32(there + (it % CK_SCL) * 4) ? lim - pg * PAGE - key0 : 0;   // of this thread's keys
+        if (seen < 16) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) s[j] = j < seen ? s[j] : -INFINITY;
+          for (int j = 0; j < 16; ++j) s[j] = j < seen ? s[j] : -INFINITY;
         }
         float mt = s[0];
 #pragma unroll
-        for (int j = 1; j < 32; ++j) mt = fmaxf(mt, s[j]);
-        red[(it & 1) * 128 + tid] = mt;
-        if (bar_any(1, 128, !ok)) {
+        for (int j = 1; j < 16; ++j) mt = max_nan(mt, s[j]);
+        if (!(mt < INFINITY)) {   // a row with a value that is not finite (or a query beyond fp16): not seen
+          bad_range = true;
+          mt = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            if (!(s[j] < INFINITY)) s[j] = -INFINITY;
+            mt = fmaxf(mt, s[j]);
+          }
+        }
+        const uint32_t buf = (it & 1) * 1024;
+        sts32(red_mine + buf, __float_as_uint(mt));
+        if (bar_any(1, CK_SM, !ok)) {
           dead_all = true;
           break;
         }
-        mt = fmaxf(mt, red[(it & 1) * 128 + (tid ^ 64)]);
+        mt = fmaxf(fmaxf(red_at(red_row + buf), red_at(red_row + buf + 256)), fmaxf(red_at(red_row + buf + 512), red_at(red_row + buf + 768)));
         float f = 1.f;
         if (mt > m + CK_RESCALE_LOG2) {   // also the first finite maximum, when m is -inf
           if (m > -INFINITY) f = ex2_approx(m - mt);
@@ -874,9 +976,9 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
         }
         const float off = m > -INFINITY ? CK_P_SHIFT - m : -INFINITY;
         float ls = 0.f;
-        uint32_t ph[16];
+        uint32_t ph[8];
 #pragma unroll
-        for (int j = 0; j < 32; j += 2) {
+        for (int j = 0; j < 16; j += 2) {
           const float p0 = ex2_approx(s[j] + off), p1 = ex2_approx(s[j + 1] + off);
           ls += p0 + p1;
           ph[j >> 1] = h2_bits(__floats2half2_rn(p0, p1));
@@ -885,80 +987,82 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
         // PV(t - 1) has read P and written O
         if (it > 0) ok = ck_wait(bar(B_PD + ((it - 1) & 1)), ((it - 1) >> 1) & 1, D.status, dead);
         tc_fence_after();
-        if (pg > P.pg0 && __any_sync(0xffffffffu, f != 1.f)) {
+        if (pg > P.pg0() && __any_sync(0xffffffffu, f != 1.f)) {
 #pragma unroll 1
-          for (int c = 0; c < 256; c += 32) {
-            uint32_t o[32];
-            tmem_ld32(lanes + CK_TM_O + c, o);
+          for (int c = 0; c < 128; c += 16) {
+            uint32_t o[16];
+            tmem_ld16(o_col + c, o);
             tmem_wait_ld();
 #pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-            tmem_st32(lanes + CK_TM_O + c, o);
+            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+            tmem_st16(o_col + c, o);
           }
           tmem_wait_st();
         }
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          *reinterpret_cast<uint4*>(smem + CK_OFF_P + sw128_chunk(row, half * 4 + c)) =
-              make_uint4(ph[4 * c], ph[4 * c + 1], ph[4 * c + 2], ph[4 * c + 3]);
+        sts128(p_lo, make_uint4(ph[0], ph[1], ph[2], ph[3]));
+        sts128(p_hi, make_uint4(ph[4], ph[5], ph[6], ph[7]));
         fence_proxy_async();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) arrive_cluster(pf0 + 8 * st);
       }
-      // left at the barrier above, all four warps alike, or at the piece's end: then one more
+      // left at the barrier above, all warps alike, or at the piece's end: then one more
       if (dead_all) break;
       ok &= ck_wait(bar(B_PD + ((it - 1) & 1)), ((it - 1) >> 1) & 1, D.status, dead);
       tc_fence_after();
-      red[(it & 1) * 128 + tid] = l;
-      if (bar_any(1, 128, !ok)) break;
-      l += red[(it & 1) * 128 + (tid ^ 64)];
-      if (P.slot < 0) {
+      const uint32_t buf = (it & 1) * 1024;
+      sts32(red_mine + buf, __float_as_uint(l));
+      if (bar_any(1, CK_SM, !ok)) break;
+      l = (red_at(red_row + buf) + red_at(red_row + buf + 256)) + (red_at(red_row + buf + 512) + red_at(red_row + buf + 768));
+      const int dim = (2 * half + sub) * 128;      // this thread's output dims
+      if (P.slot() < 0) {
         const float inv = l > 0.f ? 1.f / l : 0.f;
-        T* op = static_cast<T*>(A.out) + (P.tok0 + (long long)tk) * A.o_tok + h * A.o_head + half * 128;
+        T* op = static_cast<T*>(A.out) + (P.tok0() + (long long)tk) * A.o_tok + h * A.o_head + dim;
 #pragma unroll 1
-        for (int c = 0; c < 8; ++c) {
-          uint32_t o[32];
-          tmem_ld32(lanes + CK_TM_O + c * 32, o);
+        for (int c = 0; c < 128; c += 16) {
+          uint32_t o[16];
+          tmem_ld16(o_col + c, o);
           tmem_wait_ld();
-          T* dst = op + (c >> 2) * 256 + (c & 3) * 32;
           if (live) {
 #pragma unroll
-            for (int j = 0; j < 32; j += 8) {
+            for (int j = 0; j < 16; j += 8) {
               uint4 v;
               v.x = pack2<T>(__uint_as_float(o[j]) * inv, __uint_as_float(o[j + 1]) * inv);
               v.y = pack2<T>(__uint_as_float(o[j + 2]) * inv, __uint_as_float(o[j + 3]) * inv);
               v.z = pack2<T>(__uint_as_float(o[j + 4]) * inv, __uint_as_float(o[j + 5]) * inv);
               v.w = pack2<T>(__uint_as_float(o[j + 6]) * inv, __uint_as_float(o[j + 7]) * inv);
-              *reinterpret_cast<uint4*>(dst + j) = v;
+              *reinterpret_cast<uint4*>(op + c + j) = v;
             }
           }
         }
-        if (A.lse && live && half == 0)
-          A.lse[(size_t)(P.tok0 + tk) * H + h] = l > 0.f ? (m - CK_P_SHIFT + log2f(l)) * 0.6931471805599453f : -INFINITY;
+        if (A.lse && live && dim == 0)
+          A.lse[(size_t)(P.tok0() + tk) * H + h] = l > 0.f ? (m - CK_P_SHIFT + log2f(l)) * 0.6931471805599453f : -INFINITY;
       } else {
-        const size_t at = ((size_t)pair * 2 + P.slot) * CK_ROWS + gr;
-        float* dst = W.part + at * 512 + half * 128;
+        const ChunkWork W = work_at(A.work, A.pairs);
+        const size_t at = ((size_t)pair * 2 + P.slot()) * CK_ROWS + gr;
+        float* dst = W.part + at * 512 + dim;
 #pragma unroll 1
-        for (int c = 0; c < 8; ++c) {
-          uint32_t o[32];
-          tmem_ld32(lanes + CK_TM_O + c * 32, o);
+        for (int c = 0; c < 128; c += 16) {
+          uint32_t o[16];
+          tmem_ld16(o_col + c, o);
           tmem_wait_ld();
           if (live) {
-            uint4* d = reinterpret_cast<uint4*>(dst + (c >> 2) * 256 + (c & 3) * 32);
+            uint4* d = reinterpret_cast<uint4*>(dst + c);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) d[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+            for (int j = 0; j < 4; ++j) d[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
           }
         }
-        if (live && half == 0) W.stats[at] = make_float2(m - CK_P_SHIFT, l);
+        if (live && dim == 0) W.stats[at] = make_float2(m - CK_P_SHIFT, l);
       }
       tc_fence_before();   // O may be written again once the next tile's P has arrived
     }
+    if (bad_range) set_status(D.status, HS_ERR_RANGE);
   }
   __syncthreads();
-  if (rank == 0 && warp == CK_MMA_WARP && lane == 0) {   // every issued MMA has completed before TMEM is freed
-    umma_commit_own(bar(B_FIN));
-    for (int i = 0; i < 4096 && !try_wait_cluster(bar(B_FIN), 0); ++i) __nanosleep(200);
+  if (rank == 0 && warp == CK_MMA_WARP) {   // every issued MMA has completed before TMEM is freed
+    if (elect_lane()) umma_commit_own(bar(B_FIN));
+    __syncwarp();
+    for (int i = 0; i < 4096 && !try_wait(bar(B_FIN), 0); ++i) __nanosleep(200);
   }
   __syncwarp();
   tc_fence_before();
