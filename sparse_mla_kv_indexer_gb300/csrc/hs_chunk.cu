@@ -20,12 +20,12 @@
 // output dims for PV. The full rate of M = 128 then needs one copy of Q (64 rows, 72 KB),
 // and shared memory holds two stages of everything else.
 //
-// Roles (576 threads per CTA):
+// Roles (640 threads per CTA, five warpgroups):
 //   warps 0-7   softmax: a thread has one row and 16 keys of the tile (in the output: one
 //               128-dim group); four threads share a row
-//   warps 8-11  cache rows -> K: the e4m3 codes of this CTA's 32 rows as fp16 (exact), the rope
-//   warps 12-15 cache rows -> V: code x scale of all 64 rows for this CTA's two 128-dim groups;
-//               both load one tile ahead into registers
+//   warps 8-15  cache rows -> fp16 operands, loaded one tile ahead into registers.
+//               K: the e4m3 codes of this CTA's 32 rows as fp16 (exact), and the rope;
+//               V: code x scale of all 64 rows for this CTA's two 128-dim groups
 //   warp 16     tensor memory; in the pair's first CTA the tcgen05.mma issue for both
 //   warp 17     the pieces (block, pages) of this pair's range and their tiles' rows, ahead of the
 //               other roles
@@ -45,17 +45,22 @@
 #include <math.h>
 #include <nvtx3/nvToolsExt.h>
 
+#include <atomic>
+
 #include "hs_chunk.cuh"
 
 namespace hs {
 
 namespace {
 
-constexpr int CK_THREADS = 576;
+constexpr int CK_THREADS = 640;
 constexpr int CK_SM_WARPS = 8, CK_SM = CK_SM_WARPS * 32;         // softmax
-constexpr int CK_K_WARP0 = 8, CK_V_WARP0 = 12;
-constexpr int CK_CONV_WARPS = 4, CK_CONV = CK_CONV_WARPS * 32;   // of K, and of V
+constexpr int CK_CONV_WARP0 = 8, CK_CONV_WARPS = 8, CK_CONV = CK_CONV_WARPS * 32;
 constexpr int CK_MMA_WARP = 16, CK_PLAN_WARP = 17;
+// Registers per thread: 96 at the launch (five warpgroups), then shifted between warpgroups,
+// whose sum stays within the launch's.
+constexpr int CK_REGS = 96, CK_SM_REGS = 96, CK_CONV_REGS = 104, CK_MISC_REGS = 80;
+static_assert(2 * CK_SM_REGS + 2 * CK_CONV_REGS + CK_MISC_REGS <= CK_THREADS / 128 * CK_REGS, "register shares");
 constexpr int CK_ROWS = 128;       // rows of a block
 constexpr int CK_HALF = 64;        // rows of a block per CTA
 constexpr int CK_MIN_PAGES = 2;    // least pages of a pair's range
@@ -224,6 +229,11 @@ __device__ __forceinline__ bool ck_wait(uint32_t bar, uint32_t parity, int32_t* 
   if (try_wait(bar, parity)) return true;
   return ck_wait_slow(bar, parity, status, dead, seconds);
 }
+
+template <int N>
+__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 
 // ---- tcgen05 over the pair -----------------------------------------------------------
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t dst_smem, uint32_t ncols) {
@@ -534,7 +544,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
     }
     for (int i = 0; i < CK_TILES; ++i) {
       mbar_init(bar(B_TF + i), 1);
-      mbar_init(bar(B_TE + i), 2 * CK_CONV_WARPS);
+      mbar_init(bar(B_TE + i), CK_CONV_WARPS);
     }
     fence_mbar_init();
     sts32(dead, 0);
@@ -549,7 +559,9 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
   const Range R = plan_range(D, A, pair, tpb, smem, found);
   __syncthreads();   // the plan's arrays are done with
 
-  if (warp == CK_PLAN_WARP) {
+  if (warp >= CK_MMA_WARP) {
+    regs_dec<CK_MISC_REGS>();
+   if (warp == CK_PLAN_WARP) {
     // ------------------------------- pieces of the range -------------------------------
     int seg = R.seg, t0 = R.tok0, seg_end = R.seg_t1, page = R.page, left = R.n, at = R.at;
     uint32_t k = 0, t = 0;
@@ -624,7 +636,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
       if (!ok || pa.y < 0) break;
     }
     if (lane == 0 && rank == 0) work_at(A.work, A.pairs).cut[pair] = cut;
-  } else if (warp == CK_MMA_WARP) {
+   } else if (warp == CK_MMA_WARP) {
     // ---------------------------------- MMA issue ----------------------------------
     if (rank == 0) {
       const uint32_t idesc_qk = idesc_f16(128, 64, false, false, false);
@@ -649,7 +661,6 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
           if (i < n) {
             const uint32_t t = it + i, st = t & 1;
             ok = ck_wait(bar(B_KF + st), (t >> 1) & 1, D.status, dead);
-            if (ok && i == 0) ok = ck_wait(bar(B_VF + st), (t >> 1) & 1, D.status, dead);   // the other half of Q
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc_fence_after();
@@ -705,46 +716,46 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
         it += n;
       }
     }
-  } else if (warp >= CK_K_WARP0) {
+   }
+  } else if (warp >= CK_CONV_WARP0) {
+    regs_inc<CK_CONV_REGS>();
     // ------------------------------ cache rows to operands ------------------------------
-    const bool is_k = warp < CK_V_WARP0;
-    const int ct = tid - (is_k ? CK_K_WARP0 : CK_V_WARP0) * 32;
+    const int ct = tid - CK_CONV_WARP0 * 32;
     bool bad_range = false;
-    // the tile whose rows are in registers
     uint32_t it = 0;
+    // the tile whose rows are in registers
     const uint8_t* rows = nullptr;
-    int n_rows = 0;
+    int n_rows = 0, tok0 = 0, n_tok = 0;
     bool more = true, first = true;         // first: it begins a piece
     auto advance = [&](uint32_t t) {
-      const uint32_t ts = t % CK_TILES;
+      const uint32_t ts = t % CK_TILES, at = sbase + CK_OFF_TILES + ts * CK_PIECE_BYTES;
       more = __all_sync(0xffffffffu, ck_wait(bar(B_TF + ts), (t / CK_TILES) & 1, D.status, dead, 30));
       if (!more) return;
-      const uint4 x = lds128(sbase + CK_OFF_TILES + ts * CK_PIECE_BYTES);
+      const uint4 x = lds128(at);
       rows = reinterpret_cast<const uint8_t*>((uint64_t)x.x | (uint64_t)x.y << 32);
       n_rows = (int)x.z;
       first = x.w != 0;
       more = n_rows >= 0;
-    };
-    // the tile's entry is not needed any more
-    auto passed = [&](uint32_t t) {
+      if (first) {
+        const uint4 y = lds128(at + 16);
+        tok0 = (int)y.x, n_tok = (int)y.y;
+      }
       __syncwarp();
-      if (lane == 0) arrive_local(bar(B_TE + t % CK_TILES));
+      if (lane == 0) arrive_local(bar(B_TE + ts));
     };
     auto good_scale = [&](float s) {
       if (fabsf(s) < CK_MAX_SCALE) return s;
       bad_range = true;
       return 0.f;
     };
-    // Half of Q's 64 rows (K's warps the first, V's the second), once the products of the previous
-    // piece have read theirs: copied as they are, then each thread converts what it copied.
-    auto load_q = [&](int r0) {
+    // Q's rows, once the products of the previous piece have read theirs: copied as they are, then
+    // each thread converts what it copied.
+    auto load_q = [&]() {
       if (it > 0 && !ck_wait(bar(B_SD + ((it - 1) & 1)), ((it - 1) >> 1) & 1, D.status, dead)) return false;
       const T* q = static_cast<const T*>(A.q);
-      const uint4 x = lds128(sbase + CK_OFF_TILES + it % CK_TILES * CK_PIECE_BYTES + 16);
-      const int tok0 = (int)x.x, n_tok = (int)x.y;
-#pragma unroll 2
+#pragma unroll 1
       for (int k = 0; k < 18; ++k) {
-        const int c = ct + k * CK_CONV, r = r0 + c / 72, ch = c % 72;
+        const int c = ct + k * CK_CONV, r = c / 72, ch = c - r * 72;
         const int gr = (int)rank * CK_HALF + r, tk = gr / H, h = gr - tk * H;
         const uint32_t dst = sbase + CK_OFF_Q + (ch >> 3) * CK_QATOM + sw128_chunk(r, ch & 7);
         if (tk < n_tok) {
@@ -756,129 +767,125 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
         }
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
-#pragma unroll 2
+#pragma unroll 1
       for (int k = 0; k < 18; ++k) {
-        const int c = ct + k * CK_CONV, r = r0 + c / 72, ch = c % 72;
+        const int c = ct + k * CK_CONV, r = c / 72, ch = c - r * 72;
         const uint32_t dst = sbase + CK_OFF_Q + (ch >> 3) * CK_QATOM + sw128_chunk(r, ch & 7);
         sts128(dst, q_to_f16<T>(lds128(dst), &bad_range));
       }
       return true;
     };
-    auto ld16 = [&](const uint8_t* at) { return __ldg(reinterpret_cast<const uint4*>(at)); };
+    // K: 16-byte parts (16 codes) of this CTA's 32 rows: a warp reads 16 parts of two rows at a
+    // time, 128 contiguous bytes for every 8 threads, of 8 rows in all. A part is two 16-byte
+    // chunks of fp16; of 8 neighbouring threads, 4 store the second chunk first, so that the 8
+    // chunks of one store lie on 8 different bank groups under the swizzle.
+    // V: the 16 parts of the groups 2 rank and 2 rank + 1 of all 64 rows: the warps that have
+    // them for this CTA's rows take them again, the others read the other half page's.
+    const uint32_t kf0 = mapa(bar(B_KF), 0), vf0 = mapa(bar(B_VF), 0);   // the first CTA's
+    const int cw = ct >> 5, pv = lane & 15, row0 = 8 * (cw >> 1) + (lane >> 4);   // rows row0 + 2 k
+    const bool own_v = (cw & 1) == (int)rank;
+    const int part = 16 * (cw & 1) + pv, base_row = (int)rank * 32, rope_row = ct >> 3;
+    const int row_v = (own_v ? base_row : 32 - base_row) + row0;
+    const bool flip = (pv >> 2) & 1;
+    const uint32_t k_at = (part >> 2) * CK_KATOM + sw128_chunk(row0, (pv & 3) * 2 + flip),
+                   rope_at = 8 * CK_KATOM + sw128_chunk(rope_row, ct & 7),
+                   v_at = (pv >> 2) * CK_VATOM + sw128_chunk(row_v, (pv & 3) * 2 + flip);
+    const uint32_t src = (base_row + row0) * ROW + part * 16, src_v = row_v * ROW + (16 * (int)rank + pv) * 16,
+                   src_rope = (base_row + rope_row) * ROW + (33 + (ct & 7)) * 16, src_sc = (ct & 63) * ROW + LATENT;
+    const uint32_t sc_v = sbase + CK_OFF_SCL + (2 * (int)rank + (pv >> 3)) * CK_SCL_G + row_v * 4;
     const uint4 z = make_uint4(0, 0, 0, 0);
-    if (is_k) {
-      // 16-byte parts of a row: this thread has part `part` (16 codes) of the rows 4 k + row0 of its
-      // CTA's half page; 8 neighbouring threads store 4 parts of two rows, which the swizzle
-      // puts on 8 different bank groups. The two 16-byte chunks of a part differ in address
-      // bit 4, the rows 4 apart in bit 6 besides their distance of 512.
-      const uint32_t kf0 = mapa(bar(B_KF), 0);   // the first CTA's
-      const int part = 4 * ((ct >> 3) & 7) + (ct & 3), row0 = 2 * (ct >> 6) + ((ct >> 2) & 1);
-      const int base_row = (int)rank * 32, rope_row = ct >> 3;
-      const uint32_t k_at = (part >> 2) * CK_KATOM + sw128_chunk(row0, (part & 3) * 2),
-                     rope_at = 8 * CK_KATOM + sw128_chunk(rope_row, ct & 7);
-      const uint32_t src = (base_row + row0) * ROW + part * 16, src_rope = (base_row + rope_row) * ROW + (33 + (ct & 7)) * 16,
-                     src_sc = (ct & 63) * ROW + LATENT;
-      uint4 own[8], rope[2], sc = z;
-      auto load = [&]() {
-        advance(it);
-        if (!more) return;
-        if (n_rows == PAGE) {
+    uint4 own[4], val[4], rope = z, sc = z;
+    auto ld16 = [&](uint32_t at) { return __ldg(reinterpret_cast<const uint4*>(rows + at)); };
+    auto flipped = [&](uint4 v) { return flip ? make_uint4(v.z, v.w, v.x, v.y) : v; };
+    auto load_k = [&]() {
+      if (n_rows == PAGE) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) own[k] = ld16(rows + src + k * 4 * ROW);
+        for (int k = 0; k < 4; ++k) own[k] = ld16(src + k * 2 * ROW);
+        rope = ld16(src_rope);
+        if (ct < PAGE) sc = ld16(src_sc);
+      } else {
 #pragma unroll
-          for (int k = 0; k < 2; ++k) rope[k] = ld16(rows + src_rope + k * 16 * ROW);
-          if (ct < PAGE) sc = ld16(rows + src_sc);
-        } else {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) own[k] = base_row + 4 * k + row0 < n_rows ? ld16(rows + src + k * 4 * ROW) : z;
-#pragma unroll
-          for (int k = 0; k < 2; ++k) rope[k] = base_row + 16 * k + rope_row < n_rows ? ld16(rows + src_rope + k * 16 * ROW) : z;
-          if (ct < PAGE) sc = ct < n_rows ? ld16(rows + src_sc) : z;
-        }
-      };
-      load();
-      while (more) {
-        const uint32_t st = it & 1;
-        if (first && !load_q(0)) break;
-        passed(it);
-        if (it >= 2 && !ck_wait(bar(B_SD + st), ((it - 2) >> 1) & 1, D.status, dead)) break;
-        if (ct < PAGE) {
-          const uint32_t x = sbase + CK_OFF_SCL + (it % CK_SCL) * CK_SCL_T + ct * 4;
-          sts32(x, __float_as_uint(good_scale(__uint_as_float(sc.x))));
-          sts32(x + CK_SCL_G, __float_as_uint(good_scale(__uint_as_float(sc.y))));
-          sts32(x + 2 * CK_SCL_G, __float_as_uint(good_scale(__uint_as_float(sc.z))));
-          sts32(x + 3 * CK_SCL_G, __float_as_uint(good_scale(__uint_as_float(sc.w))));
-          if (ct == 0) sts32(there + (it % CK_SCL) * 4, n_rows > 0);
-          __syncwarp();
-          if (lane == 0) arrive_local(bar(B_SC + it % CK_SCL));   // V's warps read the scales too
-        }
-        const uint32_t kt = sbase + CK_OFF_K + st * CK_KSTAGE, dst = kt + k_at;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          uint4 lo, hi;
-          codes_to_f16(own[k], lo, hi);
-          const uint32_t d = (dst + k * 512) ^ ((k & 1) * 64);
-          sts128(d, lo);
-          sts128(d ^ 16, hi);
-        }
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const uint32_t w[4] = {rope[k].x, rope[k].y, rope[k].z, rope[k].w};
-          uint32_t o[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            o[i] = h2_bits(__floats2half2_rn(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u)));
-          sts128(kt + rope_at + k * 2048, make_uint4(o[0], o[1], o[2], o[3]));
-        }
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) arrive_cluster(kf0 + 8 * st);
-        ++it;
-        load();
+        for (int k = 0; k < 4; ++k) own[k] = base_row + row0 + 2 * k < n_rows ? ld16(src + k * 2 * ROW) : z;
+        rope = base_row + rope_row < n_rows ? ld16(src_rope) : z;
+        if (ct < PAGE) sc = ct < n_rows ? ld16(src_sc) : z;
       }
-    } else {
-      // part `part` of the groups 2 rank and 2 rank + 1 (16 parts in a row) of the rows 8 k + row0
-      const uint32_t vf0 = mapa(bar(B_VF), 0);
-      const int pv = 4 * ((ct >> 3) & 3) + (ct & 3), grp = 2 * (int)rank + (pv >> 3), part = 16 * (int)rank + pv;
-      const int row0 = 2 * (ct >> 5) + ((ct >> 2) & 1);
-      const uint32_t v_at = ((pv >> 3) * 2 + ((pv >> 2) & 1)) * CK_VATOM + sw128_chunk(row0, (pv & 3) * 2);
-      const uint32_t src = row0 * ROW + part * 16, sc_at = sbase + CK_OFF_SCL + grp * CK_SCL_G + row0 * 4;
-      uint4 val[8];
-      auto load = [&]() {
-        advance(it);
-        if (!more) return;
-        if (n_rows == PAGE) {
+    };
+    auto load_v = [&]() {
+      if (own_v) return;
+      if (n_rows == PAGE) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) val[k] = ld16(rows + src + k * 8 * ROW);
-        } else {
+        for (int k = 0; k < 4; ++k) val[k] = ld16(src_v + k * 2 * ROW);
+      } else {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) val[k] = 8 * k + row0 < n_rows ? ld16(rows + src + k * 8 * ROW) : z;
-        }
-      };
-      load();
-      while (more) {
-        const uint32_t st = it & 1;
-        if (first && !load_q(32)) break;
-        passed(it);
-        if (it >= 2 && !ck_wait(bar(B_PD + st), ((it - 2) >> 1) & 1, D.status, dead)) break;
-        if (!ck_wait(bar(B_SC + it % CK_SCL), (it / CK_SCL) & 1, D.status, dead)) break;
-        const uint32_t dst = sbase + CK_OFF_V + st * CK_VSTAGE + v_at, sc = sc_at + (it % CK_SCL) * CK_SCL_T;
-        uint32_t sv[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) sv[k] = lds32(sc + k * 32);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          uint4 lo, hi;
-          codes_to_scaled_f16(val[k], v_scale(__uint_as_float(sv[k])), lo, hi);
-          sts128(dst + k * 1024, lo);
-          sts128((dst + k * 1024) ^ 16, hi);
-        }
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) arrive_cluster(vf0 + 8 * st);
-        ++it;
-        load();
+        for (int k = 0; k < 4; ++k) val[k] = row_v + 2 * k < n_rows ? ld16(src_v + k * 2 * ROW) : z;
       }
+    };
+    advance(0);
+    if (more) {
+      load_k();
+      load_v();
+    }
+    while (more) {
+      const uint32_t st = it & 1;
+      if (first && !load_q()) break;
+      if (it >= 2 && !ck_wait(bar(B_SD + st), ((it - 2) >> 1) & 1, D.status, dead)) break;
+      if (ct < PAGE) {
+        const uint32_t x = sbase + CK_OFF_SCL + (it % CK_SCL) * CK_SCL_T + ct * 4;
+        sts32(x, __float_as_uint(good_scale(__uint_as_float(sc.x))));
+        sts32(x + CK_SCL_G, __float_as_uint(good_scale(__uint_as_float(sc.y))));
+        sts32(x + 2 * CK_SCL_G, __float_as_uint(good_scale(__uint_as_float(sc.z))));
+        sts32(x + 3 * CK_SCL_G, __float_as_uint(good_scale(__uint_as_float(sc.w))));
+        if (ct == 0) sts32(there + (it % CK_SCL) * 4, n_rows > 0);
+        __syncwarp();
+        if (lane == 0) arrive_local(bar(B_SC + it % CK_SCL));   // for V
+      }
+      const uint32_t kt = sbase + CK_OFF_K + st * CK_KSTAGE;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint4 lo, hi;
+        own[k] = flipped(own[k]);
+        codes_to_f16(own[k], lo, hi);
+        const uint32_t d = (kt + k_at + k * 256) ^ (k * 32);
+        sts128(d, lo);
+        sts128(d ^ 16, hi);
+      }
+      {
+        const uint32_t w[4] = {rope.x, rope.y, rope.z, rope.w};
+        uint32_t o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          o[i] = h2_bits(__floats2half2_rn(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u)));
+        sts128(kt + rope_at, make_uint4(o[0], o[1], o[2], o[3]));
+      }
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) arrive_cluster(kf0 + 8 * st);
+      if (own_v) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) val[k] = own[k];
+      }
+      advance(it + 1);
+      if (more) load_k();
+      if (it >= 2 && !ck_wait(bar(B_PD + st), ((it - 2) >> 1) & 1, D.status, dead)) break;
+      if (!ck_wait(bar(B_SC + it % CK_SCL), (it / CK_SCL) & 1, D.status, dead)) break;
+      const uint32_t vt = sbase + CK_OFF_V + st * CK_VSTAGE + v_at, scv = sc_v + (it % CK_SCL) * CK_SCL_T;
+      uint32_t sv[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) sv[k] = lds32(scv + k * 8);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint4 lo, hi;
+        if (!own_v) val[k] = flipped(val[k]);
+        codes_to_scaled_f16(val[k], v_scale(__uint_as_float(sv[k])), lo, hi);
+        const uint32_t d = (vt + k * 256) ^ (k * 32);
+        sts128(d, lo);
+        sts128(d ^ 16, hi);
+      }
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) arrive_cluster(vf0 + 8 * st);
+      ++it;
+      if (more) load_v();
     }
     if (bad_range) set_status(D.status, HS_ERR_RANGE);
   } else {
@@ -1118,6 +1125,14 @@ int chunk_pairs() { return num_sms() / 2 > 0 ? num_sms() / 2 : 1; }
 template <typename T>
 hs_status launch_chunk(hs_pool* p, const ChunkArgs& a, cudaStream_t st) {
   if (ensure_kernel_attrs(chunk_attention_kernel<T>, CK_SMEM) != HS_OK) return HS_ERR_CUDA;
+  // the register shares were counted against a launch of CK_REGS per thread
+  static std::atomic<int> regs{0};
+  if (regs.load(std::memory_order_relaxed) == 0) {
+    cudaFuncAttributes at;
+    if (cudaFuncGetAttributes(&at, chunk_attention_kernel<T>) != cudaSuccess) return HS_ERR_CUDA;
+    regs.store(at.numRegs, std::memory_order_relaxed);
+  }
+  if (regs.load(std::memory_order_relaxed) < CK_REGS) return HS_ERR_CUDA;
   const hs_status s = launch_pdl(chunk_attention_kernel<T>, dim3(2 * a.pairs), dim3(CK_THREADS), CK_SMEM, st, 2, p->d, a);
   if (s != HS_OK) return s;
   return launch_pdl(chunk_merge_kernel<T>, dim3(CK_ROWS, CM_GROUPS), dim3(CM_THREADS), 0, st, 0, p->d, a);
