@@ -103,7 +103,8 @@ constexpr int CK_PLAN_WARP_TMP = CK_PLAN_SUM + CK_MAX_CHUNKS * 4;       // int [
 static_assert(CK_PLAN_WARP_TMP + 32 * 4 <= CK_OFF_SCL, "plan arrays");
 
 constexpr float CK_LOG2E = 1.4426950408889634f;
-constexpr float CK_MAX_SCALE = 146.f;      // 448 x scale < 65504
+constexpr float CK_V_FACTOR = 4.f, CK_V_SHIFT = 2.f;   // V is held times this; its log2
+constexpr float CK_MAX_SCALE = 36.5f;      // 4 x 448 x scale < 65504
 constexpr float CK_RESCALE_LOG2 = 8.f;     // the reference maximum moves beyond this
 constexpr float CK_P_SHIFT = 7.f;          // P = 2^(z - m + 7) <= 2^15
 
@@ -282,6 +283,38 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// Two fp32 values in one register pair.
+struct F2 {
+  uint64_t v;
+};
+__device__ __forceinline__ F2 f2(uint32_t lo, uint32_t hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "r"(lo), "r"(hi));
+  return r;
+}
+__device__ __forceinline__ F2 f2(float x) { return f2(__float_as_uint(x), __float_as_uint(x)); }
+__device__ __forceinline__ void unpack(F2 a, float& lo, float& hi) {
+  uint32_t x, y;
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(x), "=r"(y) : "l"(a.v));
+  lo = __uint_as_float(x);
+  hi = __uint_as_float(y);
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+// The largest of three, NaN when one is.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
 // The larger of two, NaN when either is.
 __device__ __forceinline__ float max_nan(float a, float b) {
   float y;
@@ -305,21 +338,23 @@ __device__ __forceinline__ void codes_to_f16(uint4 v, uint4& lo, uint4& hi) {
   hi = make_uint4(h2_bits(e4m3x2_to_h2(v.z & 0xFFFFu)), h2_bits(e4m3x2_to_h2(v.z >> 16)),
                   h2_bits(e4m3x2_to_h2(v.w & 0xFFFFu)), h2_bits(e4m3x2_to_h2(v.w >> 16)));
 }
-// code x scale in fp16, rounded once: 256 x scale in two fp16 parts times code / 256 (both
-// exact products of the code; |scale| < 146 keeps the first part finite). A NaN code becomes
-// a finite value: its row's scores are NaN, so it is not seen, and 0 x it has to be 0.
+// 4 x code x scale in fp16, rounded once: 4 x scale in two fp16 parts (the factor keeps the
+// second part's bits down to scales of 2^-16; it leaves the output again with the sum). A NaN
+// code becomes a finite value: its row's scores are NaN, so it is not seen, and 0 x it has to
+// be 0.
 struct VScale {
   __half2 hi, lo;
 };
 __device__ __forceinline__ VScale v_scale(float s) {
   VScale r;
-  const __half h = __float2half_rn(256.f * s);
+  const float s4 = CK_V_FACTOR * s;
+  const __half h = __float2half_rn(s4);
   r.hi = __half2half2(h);
-  r.lo = __half2half2(__float2half_rn(256.f * s - __half2float(h)));
+  r.lo = __half2half2(__float2half_rn(s4 - __half2float(h)));
   return r;
 }
 __device__ __forceinline__ uint32_t scaled2(uint32_t two, const VScale& v) {
-  const __half2 c = __hmul2(e4m3x2_to_h2(two), __half2half2(__ushort_as_half(0x1C00)));   // 2^-8
+  const __half2 c = e4m3x2_to_h2(two);
   return h2_bits(__hmin2(__hfma2(c, v.hi, __hmul2(c, v.lo)), __half2half2(__ushort_as_half(0x7BFF))));
 }
 __device__ __forceinline__ void codes_to_scaled_f16(uint4 v, const VScale& s, uint4& lo, uint4& hi) {
@@ -743,8 +778,9 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
       __syncwarp();
       if (lane == 0) arrive_local(bar(B_TE + ts));
     };
-    auto good_scale = [&](float s) {
-      if (fabsf(s) < CK_MAX_SCALE) return s;
+    const float sign = A.scale_log2 < 0.f ? -1.f : 1.f;
+    auto good_scale = [&](float s) {        // times the sign of sm_scale, for the scores
+      if (fabsf(s) < CK_MAX_SCALE) return s * sign;
       bad_range = true;
       return 0.f;
     };
@@ -876,7 +912,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
       for (int k = 0; k < 4; ++k) {
         uint4 lo, hi;
         if (!own_v) val[k] = flipped(val[k]);
-        codes_to_scaled_f16(val[k], v_scale(__uint_as_float(sv[k])), lo, hi);
+        codes_to_scaled_f16(val[k], v_scale(__uint_as_float(sv[k]) * sign), lo, hi);
         const uint32_t d = (vt + k * 256) ^ (k * 32);
         sts128(d, lo);
         sts128(d ^ 16, hi);
@@ -902,6 +938,10 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
     const uint32_t red_row = sbase + CK_OFF_RED + row * 4, red_mine = red_row + (half * 2 + sub) * 256;
     auto red_at = [&](uint32_t at) { return __uint_as_float(lds32(at)); };
     uint32_t it = 0;
+    // s is held times the sign of sm_scale (in the scales, and here for the rope), so that its
+    // maximum is the maximum of z; a scale of 0 becomes one that leaves every z at 0 but that
+    // of an unseen key, -inf
+    const float scale = fmaxf(fabsf(A.scale_log2), 1e-37f), sign = A.scale_log2 < 0.f ? -1.f : 1.f;
     bool ok = true, dead_all = false, bad_range = false;
     for (uint32_t kp = 0;; ++kp) {
       const uint32_t slot = kp % CK_RING;
@@ -923,7 +963,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
         ok &= ck_wait(bar(B_SD + st), (it >> 1) & 1, D.status, dead);
         tc_fence_after();
         const uint32_t sc = sbase + CK_OFF_SCL + (it % CK_SCL) * CK_SCL_T + key0 * 4;
-        float s[16];
+        F2 s2[8];   // scores, times the sign of sm_scale, in pairs of keys
 #pragma unroll
         for (int g = 0; g < 4; g += 2) {
           uint32_t a[16], b[16];
@@ -933,21 +973,23 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
 #pragma unroll
           for (int j = 0; j < 16; j += 4) {
             const uint4 x = lds128(sc + g * CK_SCL_G + j * 4), y = lds128(sc + (g + 1) * CK_SCL_G + j * 4);
-            const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float u = __uint_as_float(xs[i]), w = __uint_as_float(ys[i]);
-              const float v = g == 0 ? u * __uint_as_float(a[j + i]) : fmaf(u, __uint_as_float(a[j + i]), s[j + i]);
-              s[j + i] = fmaf(w, __uint_as_float(b[j + i]), v);
-            }
+            const F2 u = g == 0 ? mul2(f2(x.x, x.y), f2(a[j], a[j + 1])) : fma2(f2(x.x, x.y), f2(a[j], a[j + 1]), s2[j / 2]);
+            const F2 w = g == 0 ? mul2(f2(x.z, x.w), f2(a[j + 2], a[j + 3]))
+                                : fma2(f2(x.z, x.w), f2(a[j + 2], a[j + 3]), s2[j / 2 + 1]);
+            s2[j / 2] = fma2(f2(y.x, y.y), f2(b[j], b[j + 1]), u);
+            s2[j / 2 + 1] = fma2(f2(y.z, y.w), f2(b[j + 2], b[j + 3]), w);
           }
         }
+        float s[16];
         {
           uint32_t a[16];
           tmem_ld16(s_col + ((5 * it + 4) & 7) * 32, a);
           tmem_wait_ld();
 #pragma unroll
-          for (int j = 0; j < 16; ++j) s[j] = (s[j] + __uint_as_float(a[j])) * A.scale_log2;
+          for (int j = 0; j < 16; j += 2) {
+            s2[j / 2] = fma2(f2(a[j], a[j + 1]), f2(sign), s2[j / 2]);
+            unpack(s2[j / 2], s[j], s[j + 1]);
+          }
         }
         tc_fence_before();
         __syncwarp();
@@ -957,9 +999,9 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
 #pragma unroll
           for (int j = 0; j < 16; ++j) s[j] = j < seen ? s[j] : -INFINITY;
         }
-        float mt = s[0];
+        float mt = max_nan(s[0], s[1]);
 #pragma unroll
-        for (int j = 1; j < 16; ++j) mt = max_nan(mt, s[j]);
+        for (int j = 2; j < 16; j += 2) mt = max3_nan(mt, s[j], s[j + 1]);
         if (!(mt < INFINITY)) {   // a row with a value that is not finite (or a query beyond fp16): not seen
           bad_range = true;
           mt = -INFINITY;
@@ -976,20 +1018,27 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
           break;
         }
         mt = fmaxf(fmaxf(red_at(red_row + buf), red_at(red_row + buf + 256)), fmaxf(red_at(red_row + buf + 512), red_at(red_row + buf + 768)));
+        mt *= scale;
         float f = 1.f;
         if (mt > m + CK_RESCALE_LOG2) {   // also the first finite maximum, when m is -inf
           if (m > -INFINITY) f = ex2_approx(m - mt);
           m = mt;
         }
-        const float off = m > -INFINITY ? CK_P_SHIFT - m : -INFINITY;
-        float ls = 0.f;
+        const float off = m > -INFINITY ? CK_P_SHIFT - m : 0.f;   // no finite score yet: every s is -inf
+        F2 ls2 = f2(0.f);
         uint32_t ph[8];
 #pragma unroll
         for (int j = 0; j < 16; j += 2) {
-          const float p0 = ex2_approx(s[j] + off), p1 = ex2_approx(s[j + 1] + off);
-          ls += p0 + p1;
+          float p0, p1;
+          unpack(fma2(f2(__float_as_uint(s[j]), __float_as_uint(s[j + 1])), f2(scale), f2(off)), p0, p1);
+          p0 = ex2_approx(p0);
+          p1 = ex2_approx(p1);
+          ls2 = fma2(f2(__float_as_uint(p0), __float_as_uint(p1)), f2(1.f), ls2);
           ph[j >> 1] = h2_bits(__floats2half2_rn(p0, p1));
         }
+        float ls, ls_hi;
+        unpack(ls2, ls, ls_hi);
+        ls += ls_hi;
         l = l * f + ls;
         // PV(t - 1) has read P and written O
         if (it > 0) ok = ck_wait(bar(B_PD + ((it - 1) & 1)), ((it - 1) >> 1) & 1, D.status, dead);
@@ -1021,6 +1070,8 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
       sts32(red_mine + buf, __float_as_uint(l));
       if (bar_any(1, CK_SM, !ok)) break;
       l = (red_at(red_row + buf) + red_at(red_row + buf + 256)) + (red_at(red_row + buf + 512) + red_at(red_row + buf + 768));
+      l *= CK_V_FACTOR;   // as O
+      m -= CK_P_SHIFT + CK_V_SHIFT;
       const int dim = (2 * half + sub) * 128;      // this thread's output dims
       if (P.slot() < 0) {
         const float inv = l > 0.f ? 1.f / l : 0.f;
@@ -1043,7 +1094,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
           }
         }
         if (A.lse && live && dim == 0)
-          A.lse[(size_t)(P.tok0() + tk) * H + h] = l > 0.f ? (m - CK_P_SHIFT + log2f(l)) * 0.6931471805599453f : -INFINITY;
+          A.lse[(size_t)(P.tok0() + tk) * H + h] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
       } else {
         const ChunkWork W = work_at(A.work, A.pairs);
         const size_t at = ((size_t)pair * 2 + P.slot()) * CK_ROWS + gr;
@@ -1059,7 +1110,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
             for (int j = 0; j < 4; ++j) d[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
           }
         }
-        if (live && dim == 0) W.stats[at] = make_float2(m - CK_P_SHIFT, l);
+        if (live && dim == 0) W.stats[at] = make_float2(m, l);
       }
       tc_fence_before();   // O may be written again once the next tile's P has arrived
     }
