@@ -59,7 +59,7 @@ constexpr int CK_CONV_WARP0 = 8, CK_CONV_WARPS = 8, CK_CONV = CK_CONV_WARPS * 32
 constexpr int CK_MMA_WARP = 16, CK_PLAN_WARP = 17;
 // Registers per thread: 96 at the launch (five warpgroups), then shifted between warpgroups,
 // whose sum stays within the launch's.
-constexpr int CK_REGS = 96, CK_SM_REGS = 96, CK_CONV_REGS = 104, CK_MISC_REGS = 80;
+constexpr int CK_REGS = 96, CK_SM_REGS = 96, CK_CONV_REGS = 112, CK_MISC_REGS = 64;
 static_assert(2 * CK_SM_REGS + 2 * CK_CONV_REGS + CK_MISC_REGS <= CK_THREADS / 128 * CK_REGS, "register shares");
 constexpr int CK_ROWS = 128;       // rows of a block
 constexpr int CK_HALF = 64;        // rows of a block per CTA
@@ -946,7 +946,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
     for (uint32_t kp = 0;; ++kp) {
       const uint32_t slot = kp % CK_RING;
       ok &= ck_wait(bar(B_RF + slot), (kp / CK_RING) & 1, D.status, dead, 30);
-      if (bar_any(1, CK_SM, !ok)) break;
+      if (bar_any(2 + (quad & 1), CK_SM / 2, !ok)) break;
       const Piece P = piece_at(slot);
       __syncwarp();
       if (lane == 0) arrive_local(bar(B_RE + slot));
@@ -964,30 +964,36 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
         tc_fence_after();
         const uint32_t sc = sbase + CK_OFF_SCL + (it % CK_SCL) * CK_SCL_T + key0 * 4;
         F2 s2[8];   // scores, times the sign of sm_scale, in pairs of keys
+        float s[16];
+        {
+          uint32_t a[48];
 #pragma unroll
-        for (int g = 0; g < 4; g += 2) {
-          uint32_t a[16], b[16];
-          tmem_ld16(s_col + ((5 * it + g) & 7) * 32, a);
-          tmem_ld16(s_col + ((5 * it + g + 1) & 7) * 32, b);
+          for (int g = 0; g < 3; ++g) tmem_ld16(s_col + ((5 * it + g) & 7) * 32, *reinterpret_cast<uint32_t(*)[16]>(a + 16 * g));
+          tmem_wait_ld();
+#pragma unroll
+          for (int g = 0; g < 3; ++g)
+#pragma unroll
+            for (int j = 0; j < 16; j += 4) {
+              const uint4 x = lds128(sc + g * CK_SCL_G + j * 4);
+              const uint32_t* v = a + 16 * g + j;
+              s2[j / 2] = g == 0 ? mul2(f2(x.x, x.y), f2(v[0], v[1])) : fma2(f2(x.x, x.y), f2(v[0], v[1]), s2[j / 2]);
+              s2[j / 2 + 1] = g == 0 ? mul2(f2(x.z, x.w), f2(v[2], v[3])) : fma2(f2(x.z, x.w), f2(v[2], v[3]), s2[j / 2 + 1]);
+            }
+        }
+        {
+          uint32_t a[32];
+          tmem_ld16(s_col + ((5 * it + 3) & 7) * 32, *reinterpret_cast<uint32_t(*)[16]>(a));
+          tmem_ld16(s_col + ((5 * it + 4) & 7) * 32, *reinterpret_cast<uint32_t(*)[16]>(a + 16));
           tmem_wait_ld();
 #pragma unroll
           for (int j = 0; j < 16; j += 4) {
-            const uint4 x = lds128(sc + g * CK_SCL_G + j * 4), y = lds128(sc + (g + 1) * CK_SCL_G + j * 4);
-            const F2 u = g == 0 ? mul2(f2(x.x, x.y), f2(a[j], a[j + 1])) : fma2(f2(x.x, x.y), f2(a[j], a[j + 1]), s2[j / 2]);
-            const F2 w = g == 0 ? mul2(f2(x.z, x.w), f2(a[j + 2], a[j + 3]))
-                                : fma2(f2(x.z, x.w), f2(a[j + 2], a[j + 3]), s2[j / 2 + 1]);
-            s2[j / 2] = fma2(f2(y.x, y.y), f2(b[j], b[j + 1]), u);
-            s2[j / 2 + 1] = fma2(f2(y.z, y.w), f2(b[j + 2], b[j + 3]), w);
+            const uint4 x = lds128(sc + 3 * CK_SCL_G + j * 4);
+            s2[j / 2] = fma2(f2(x.x, x.y), f2(a[j], a[j + 1]), s2[j / 2]);
+            s2[j / 2 + 1] = fma2(f2(x.z, x.w), f2(a[j + 2], a[j + 3]), s2[j / 2 + 1]);
           }
-        }
-        float s[16];
-        {
-          uint32_t a[16];
-          tmem_ld16(s_col + ((5 * it + 4) & 7) * 32, a);
-          tmem_wait_ld();
 #pragma unroll
           for (int j = 0; j < 16; j += 2) {
-            s2[j / 2] = fma2(f2(a[j], a[j + 1]), f2(sign), s2[j / 2]);
+            s2[j / 2] = fma2(f2(a[16 + j], a[17 + j]), f2(sign), s2[j / 2]);
             unpack(s2[j / 2], s[j], s[j + 1]);
           }
         }
@@ -1013,7 +1019,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
         }
         const uint32_t buf = (it & 1) * 1024;
         sts32(red_mine + buf, __float_as_uint(mt));
-        if (bar_any(1, CK_SM, !ok)) {
+        if (bar_any(2 + (quad & 1), CK_SM / 2, !ok)) {   // the four warps of these 32 rows
           dead_all = true;
           break;
         }
@@ -1062,13 +1068,13 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
         __syncwarp();
         if (lane == 0) arrive_cluster(pf0 + 8 * st);
       }
-      // left at the barrier above, all warps alike, or at the piece's end: then one more
+      // left at the barrier above, the four warps of a row alike, or at the piece's end: then one more
       if (dead_all) break;
       ok &= ck_wait(bar(B_PD + ((it - 1) & 1)), ((it - 1) >> 1) & 1, D.status, dead);
       tc_fence_after();
       const uint32_t buf = (it & 1) * 1024;
       sts32(red_mine + buf, __float_as_uint(l));
-      if (bar_any(1, CK_SM, !ok)) break;
+      if (bar_any(2 + (quad & 1), CK_SM / 2, !ok)) break;
       l = (red_at(red_row + buf) + red_at(red_row + buf + 256)) + (red_at(red_row + buf + 512) + red_at(red_row + buf + 768));
       l *= CK_V_FACTOR;   // as O
       m -= CK_P_SHIFT + CK_V_SHIFT;
