@@ -8,10 +8,11 @@
 //
 // Work. A (token, head) pair is a row; a block is 128 rows (128 / H tokens of one segment);
 // a tile is a block against one page of 64 cached rows. The tiles of all blocks, in order,
-// are dealt in equal contiguous ranges to the pairs of SMs, so that one token over a long
-// context and a long prompt both fill the GPU. A range cuts at most two blocks; their parts
-// go to the workspace (fp32 sums, maxima) and chunk_merge_kernel joins them in a fixed
-// order. Every CTA finds its range itself from the segments and limits.
+// and a block's fixed cost (its queries, its outputs) before its first tile, are dealt in
+// equal contiguous ranges to the pairs of SMs, so that one token over a long context and a
+// long prompt both fill the GPU. A range cuts at most two blocks; their parts go to the
+// workspace (fp32 sums, maxima) and chunk_merge_kernel joins them in a fixed order. Every
+// CTA finds its range itself from the segments and limits.
 //
 // Split of a block over a pair. The output of 128 rows is 128 x 512 fp32, all of one SM's
 // tensor memory, with no room for scores; so two CTAs form a pair (tcgen05.mma of
@@ -59,11 +60,12 @@ constexpr int CK_CONV_WARP0 = 8, CK_CONV_WARPS = 8, CK_CONV = CK_CONV_WARPS * 32
 constexpr int CK_MMA_WARP = 16, CK_PLAN_WARP = 17;
 // Registers per thread: 96 at the launch (five warpgroups), then shifted between warpgroups,
 // whose sum stays within the launch's.
-constexpr int CK_REGS = 96, CK_SM_REGS = 96, CK_CONV_REGS = 112, CK_MISC_REGS = 64;
+constexpr int CK_REGS = 96, CK_SM_REGS = 96, CK_CONV_REGS = 104, CK_MISC_REGS = 80;
 static_assert(2 * CK_SM_REGS + 2 * CK_CONV_REGS + CK_MISC_REGS <= CK_THREADS / 128 * CK_REGS, "register shares");
 constexpr int CK_ROWS = 128;       // rows of a block
 constexpr int CK_HALF = 64;        // rows of a block per CTA
-constexpr int CK_MIN_PAGES = 2;    // least pages of a pair's range
+constexpr int CK_BLOCK_COST = 3;   // what a block costs besides its pages, in pages
+constexpr int CK_MIN_COST = CK_BLOCK_COST + 2;   // least cost of a pair's range
 constexpr int CK_RING = 4;         // pieces the planning warp runs ahead
 constexpr int CK_TILES = 16;       // tiles it runs ahead
 constexpr int CK_SCL = 4;          // tiles of scales held
@@ -231,6 +233,9 @@ __device__ __forceinline__ bool ck_wait(uint32_t bar, uint32_t parity, int32_t* 
   return ck_wait_slow(bar, parity, status, dead, seconds);
 }
 
+__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
 template <int N>
 __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N>
@@ -408,12 +413,14 @@ __device__ __forceinline__ int block_scan(int v, int* tmp, int* total) {
   __syncthreads();
   if (lane == 31) tmp[warp] = v;
   __syncthreads();
-  int before = 0, all = tmp[0];
-  for (int w = 0; w < CK_THREADS / 32; ++w) {
-    if (w < warp) before = w == 0 ? tmp[0] : op(before, tmp[w]);
-    if (w > 0) all = op(all, tmp[w]);
+  int w = lane < CK_THREADS / 32 ? tmp[lane] : 0;   // the warps' totals (values are >= 0)
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, w, o);
+    if (lane >= o) w = op(w, u);
   }
-  *total = all;
+  *total = __shfl_sync(0xffffffffu, w, 31);
+  const int before = __shfl_sync(0xffffffffu, w, warp > 0 ? warp - 1 : 0);
   return warp == 0 ? v : op(before, v);
 }
 
@@ -428,7 +435,9 @@ __device__ __forceinline__ int clamp_limit(const Dev& D, int l, bool* bad) {
 // Tokens and largest limit of block b of a segment [t0, t1).
 __device__ __forceinline__ int block_limit(const Dev& D, const int32_t* limit, int t0, int t1, bool* bad) {
   int m = 0;
-  for (int t = t0; t < t1; ++t) m = max(m, clamp_limit(D, __ldg(limit + t), bad));
+#pragma unroll
+  for (int i = 0; i < 8; ++i)   // at most 128 / 16 tokens
+    if (t0 + i < t1) m = max(m, clamp_limit(D, __ldg(limit + t0 + i), bad));
   return m;
 }
 __device__ __forceinline__ int pages_of(int limit) { return max(1, (limit + PAGE - 1) / PAGE); }
@@ -436,13 +445,13 @@ __device__ __forceinline__ int pages_of(int limit) { return max(1, (limit + PAGE
 struct Range {
   int seg, seg_t0, seg_t1;   // the segment of the first block, clamped
   int tok0;                  // the first block's first token
-  int page;                  // its first page of this range
-  int at;                    // the range's first tile
-  int n;                     // its tiles
-  int per_pair;              // tiles of each pair's range
+  int into;                  // how far into its cost the range starts
+  int at;                    // the range's first unit of cost
+  int n;                     // its units
+  int per_pair;              // units of each pair's range
 };
 
-// This pair's range of tiles. All threads of the CTA take part; sm: the operand buffers.
+// This pair's range. All threads of the CTA take part; sm: the operand buffers.
 __device__ Range plan_range(const Dev& D, const ChunkArgs& A, int pair, int tpb, uint8_t* sm, int32_t* found) {
   int* start = reinterpret_cast<int*>(sm + CK_PLAN_START);
   int* blk = reinterpret_cast<int*>(sm + CK_PLAN_BLK);
@@ -483,7 +492,7 @@ __device__ Range plan_range(const Dev& D, const ChunkArgs& A, int pair, int tpb,
   }
   if (tid == 0) blk[A.n_seg] = n_blocks;
   __syncthreads();
-  // the tiles of as many blocks at a time as the CTA has threads
+  // the cost of as many blocks at a time as the CTA has threads
   auto segment_of = [&](int b) {   // the last segment whose first block is <= b (never an empty one)
     int l = 0, h = A.n_seg;
     while (h - l > 1) {
@@ -492,22 +501,23 @@ __device__ Range plan_range(const Dev& D, const ChunkArgs& A, int pair, int tpb,
     }
     return l;
   };
-  auto tiles_of = [&](int b, bool* bad_id) {
+  auto cost_of = [&](int b, bool* bad_id) {
     const int s = segment_of(b), t0 = start[s] + (b - blk[s]) * tpb;
-    return pages_of(block_limit(D, A.limit, t0, min(t0 + tpb, start[s + 1]), bad_id));
+    return CK_BLOCK_COST + pages_of(block_limit(D, A.limit, t0, min(t0 + tpb, start[s + 1]), bad_id));
   };
   const int chunks = (n_blocks + CK_THREADS - 1) / CK_THREADS;
-  int all = 0;
+  int all = 0, t = 0, end = 0;   // this thread's block of the last chunk: its cost, and that up to it
   for (int c = 0; c < chunks; ++c) {
     const int b = c * CK_THREADS + tid;
     int sum;
-    block_scan<false>(b < n_blocks ? tiles_of(b, &bad) : 0, tmp, &sum);
+    t = b < n_blocks ? cost_of(b, &bad) : 0;
+    end = all + block_scan<false>(t, tmp, &sum);
     if (tid == 0) sums[c] = sum;
     all += sum;
   }
   if (bad) set_status(D.status, HS_ERR_BAD_ID);
   Range r = {};
-  r.per_pair = max((all + A.pairs - 1) / A.pairs, CK_MIN_PAGES);
+  r.per_pair = max((all + A.pairs - 1) / A.pairs, CK_MIN_COST);
   r.at = pair * r.per_pair;
   r.n = min(r.per_pair, all - r.at);
   __syncthreads();
@@ -515,14 +525,16 @@ __device__ Range plan_range(const Dev& D, const ChunkArgs& A, int pair, int tpb,
     r.n = 0;
     return r;
   }
-  // the block that holds tile r.at
+  // the block that holds the range's first unit
   int c = 0, first = 0;
   while (first + sums[c] <= r.at) first += sums[c++];
   const int b = c * CK_THREADS + tid;
-  bool ignore = false;
-  const int t = b < n_blocks ? tiles_of(b, &ignore) : 0;
-  int sum;
-  const int end = first + block_scan<false>(t, tmp, &sum);
+  if (c != chunks - 1) {
+    bool ignore = false;
+    t = b < n_blocks ? cost_of(b, &ignore) : 0;
+    int sum;
+    end = first + block_scan<false>(t, tmp, &sum);
+  }
   if (t > 0 && end - t <= r.at && r.at < end) {
     const int s = segment_of(b);
     found[0] = s;
@@ -536,7 +548,7 @@ __device__ Range plan_range(const Dev& D, const ChunkArgs& A, int pair, int tpb,
   r.seg_t0 = found[1];
   r.seg_t1 = found[2];
   r.tok0 = found[3];
-  r.page = found[4];
+  r.into = found[4];
   return r;
 }
 
@@ -559,7 +571,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = blockIdx.x & 1;
   const int pair = blockIdx.x >> 1;
-  const int H = D.n_heads, tpb = CK_ROWS / H;
+  const int H = D.n_heads, hs = 31 - __clz(H), tpb = CK_ROWS >> hs;   // 16, 32 or 64 heads
 
   if (warp == CK_MMA_WARP) tmem_alloc_pair(tslot, 512);
   if (tid == 0) {
@@ -598,7 +610,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
     regs_dec<CK_MISC_REGS>();
    if (warp == CK_PLAN_WARP) {
     // ------------------------------- pieces of the range -------------------------------
-    int seg = R.seg, t0 = R.tok0, seg_end = R.seg_t1, page = R.page, left = R.n, at = R.at;
+    int seg = R.seg, t0 = R.tok0, seg_end = R.seg_t1, into = R.into, left = R.n, at = R.at;
     uint32_t k = 0, t = 0;
     int entries = -1;
     const uint8_t* const kv = D.kv[A.layer];
@@ -606,25 +618,36 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
     bool ok = true;
     for (;; ++k) {
       int4 pa = make_int4(0, -1, -1, 0), pb = make_int4(0, 0, -1, 0);
-      if (left > 0) {
+      while (left > 0 && pa.y < 0) {   // the range's next pages: none of a block whose fixed cost it ends in
         const int t1 = min(t0 + tpb, seg_end);
         const int r = __ldg(A.seg_req + seg);
         bool bad = r < 0 || r >= D.max_requests, ignore = false;
         const int lim = block_limit(D, A.limit, t0, t1, &ignore), n_pages = pages_of(lim);
         if (bad && lane == 0) set_status(D.status, HS_ERR_BAD_ID);
-        const int p1 = min(n_pages, page + left), used = p1 - page;
-        const bool whole = page == 0 && p1 == n_pages;
-        pa = make_int4(t0, t1 - t0, bad ? -1 : r, bad ? 0 : lim);
-        pb = make_int4(page, p1, whole ? -1 : page == 0 ? 1 : 0, 0);
-        if (page == 0 && !whole) cut = {t0, t1 - t0, (at + n_pages - 1) / R.per_pair, 0};
+        const int end = min(CK_BLOCK_COST + n_pages, into + left), used = end - into;
+        const int p0 = max(into - CK_BLOCK_COST, 0), p1 = max(end - CK_BLOCK_COST, 0);
+        if (p1 > p0) {
+          const bool whole = p0 == 0 && p1 == n_pages;
+          pa = make_int4(t0, t1 - t0, bad ? -1 : r, bad ? 0 : lim);
+          pb = make_int4(p0, p1, whole ? -1 : p0 == 0 ? 1 : 0, 0);
+          if (p0 == 0 && !whole) cut = {t0, t1 - t0, (at - into + CK_BLOCK_COST + n_pages - 1) / R.per_pair, 0};
+        }
         left -= used;
         at += used;
-        page = 0;
+        into = 0;
         t0 = t1;
         while (left > 0 && t0 >= seg_end) {   // the next segment with tokens
           ++seg;
           t0 = seg_end;
           seg_end = max(seg_end, min(max(__ldg(A.seg_start + seg + 1), 0), A.n_tok));
+        }
+      }
+      if (pa.y > 0) {   // Q's rows on their way to L2
+        for (int c = lane; c < CK_HALF * 9; c += 32) {
+          const int r = c / 9, gr = (int)rank * CK_HALF + r, tk = gr >> hs;
+          if (tk < pa.y)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const T*>(A.q) + (pa.x + tk) * A.q_tok +
+                                                          (gr & (H - 1)) * A.q_head + (c - r * 9) * 64));
         }
       }
       const uint32_t slot = k % CK_RING;
@@ -657,6 +680,9 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
             }
           }
         }
+        // this CTA's half of the page on its way to L2 (a page of the host pool stays there)
+        if (lane == 0 && rows != nullptr && n_rows > (int)rank * 32 && entry >= 0)
+          prefetch_l2(rows + rank * 32 * ROW, 32 * ROW);
         if (t >= CK_TILES) ok = ck_wait(bar(B_TE + ts), (t / CK_TILES - 1) & 1, D.status, dead, 30);
         if (!ok) break;
         if (lane == 0) {
@@ -788,26 +814,40 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
     // each thread converts what it copied.
     auto load_q = [&]() {
       if (it > 0 && !ck_wait(bar(B_SD + ((it - 1) & 1)), ((it - 1) >> 1) & 1, D.status, dead)) return false;
-      const T* q = static_cast<const T*>(A.q);
-#pragma unroll 1
-      for (int k = 0; k < 18; ++k) {
-        const int c = ct + k * CK_CONV, r = c / 72, ch = c - r * 72;
-        const int gr = (int)rank * CK_HALF + r, tk = gr / H, h = gr - tk * H;
+      const T* q = static_cast<const T*>(A.q) + (long long)tok0 * A.q_tok;
+      int r = ct / 72, ch = ct % 72;        // row and 16-byte chunk: 256 chunks on are 3 rows and 40 chunks
+      auto next = [&]() {
+        r += 3;
+        ch += 40;
+        if (ch >= 72) ch -= 72, ++r;
+      };
+#pragma unroll 3
+      for (int k = 0; k < 18; ++k, next()) {
+        const int gr = (int)rank * CK_HALF + r, tk = gr >> hs, h = gr & (H - 1);
         const uint32_t dst = sbase + CK_OFF_Q + (ch >> 3) * CK_QATOM + sw128_chunk(r, ch & 7);
         if (tk < n_tok) {
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst),
-                       "l"(q + (tok0 + tk) * A.q_tok + h * A.q_head + ch * 8)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(q + tk * A.q_tok + h * A.q_head + ch * 8)
                        : "memory");
         } else {
           sts128(dst, make_uint4(0, 0, 0, 0));
         }
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
+      r = ct / 72, ch = ct % 72;
 #pragma unroll 1
-      for (int k = 0; k < 18; ++k) {
-        const int c = ct + k * CK_CONV, r = c / 72, ch = c - r * 72;
-        const uint32_t dst = sbase + CK_OFF_Q + (ch >> 3) * CK_QATOM + sw128_chunk(r, ch & 7);
-        sts128(dst, q_to_f16<T>(lds128(dst), &bad_range));
+      for (int k = 0; k < 18; k += 3) {
+        uint32_t dst[3];
+        uint4 v[3];
+#pragma unroll
+        for (int i = 0; i < 3; ++i, next()) {
+          dst[i] = sbase + CK_OFF_Q + (ch >> 3) * CK_QATOM + sw128_chunk(r, ch & 7);
+          v[i] = lds128(dst[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+          const uint4 f = q_to_f16<T>(v[i], &bad_range);
+          if constexpr (!__is_same(T, __half)) sts128(dst[i], f);
+        }
       }
       return true;
     };
@@ -863,7 +903,6 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
     }
     while (more) {
       const uint32_t st = it & 1;
-      if (first && !load_q()) break;
       if (it >= 2 && !ck_wait(bar(B_SD + st), ((it - 2) >> 1) & 1, D.status, dead)) break;
       if (ct < PAGE) {
         const uint32_t x = sbase + CK_OFF_SCL + (it % CK_SCL) * CK_SCL_T + ct * 4;
@@ -893,6 +932,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
           o[i] = h2_bits(__floats2half2_rn(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u)));
         sts128(kt + rope_at, make_uint4(o[0], o[1], o[2], o[3]));
       }
+      if (first && !load_q()) break;
       fence_proxy_async();
       __syncwarp();
       if (lane == 0) arrive_cluster(kf0 + 8 * st);
@@ -934,7 +974,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
     const uint32_t pf0 = mapa(bar(B_PF), 0), sr0 = mapa(bar(B_SR), 0);
     const uint32_t p_lo = sbase + CK_OFF_P + sw128_chunk(row, key0 >> 3),
                    p_hi = sbase + CK_OFF_P + sw128_chunk(row, (key0 >> 3) + 1);
-    const int gr = (int)rank * CK_HALF + row, tk = gr / H, h = gr - tk * H;
+    const int gr = (int)rank * CK_HALF + row, tk = gr >> hs, h = gr & (H - 1);
     const uint32_t red_row = sbase + CK_OFF_RED + row * 4, red_mine = red_row + (half * 2 + sub) * 256;
     auto red_at = [&](uint32_t at) { return __uint_as_float(lds32(at)); };
     uint32_t it = 0;
@@ -1081,23 +1121,34 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
       const int dim = (2 * half + sub) * 128;      // this thread's output dims
       if (P.slot() < 0) {
         const float inv = l > 0.f ? 1.f / l : 0.f;
-        T* op = static_cast<T*>(A.out) + (P.tok0() + (long long)tk) * A.o_tok + h * A.o_head + dim;
+        // 16 columns at a time through this warp's quarter of its rows' P (free until the next
+        // exchange of maxima), so that two lanes store 32 bytes of one row
+        const uint32_t stage = sbase + CK_OFF_P + (quad & 1) * 4096 + (half * 2 + sub) * 1024;
+        const uint32_t put = stage + lane * 32 + ((lane >> 2) & 1) * 16;
+        T* const out0 = static_cast<T*>(A.out) + dim + (lane & 1) * 8;
 #pragma unroll 1
         for (int c = 0; c < 128; c += 16) {
           uint32_t o[16];
           tmem_ld16(o_col + c, o);
           tmem_wait_ld();
-          if (live) {
 #pragma unroll
-            for (int j = 0; j < 16; j += 8) {
-              uint4 v;
-              v.x = pack2<T>(__uint_as_float(o[j]) * inv, __uint_as_float(o[j + 1]) * inv);
-              v.y = pack2<T>(__uint_as_float(o[j + 2]) * inv, __uint_as_float(o[j + 3]) * inv);
-              v.z = pack2<T>(__uint_as_float(o[j + 4]) * inv, __uint_as_float(o[j + 5]) * inv);
-              v.w = pack2<T>(__uint_as_float(o[j + 6]) * inv, __uint_as_float(o[j + 7]) * inv);
-              *reinterpret_cast<uint4*>(op + c + j) = v;
-            }
+          for (int j = 0; j < 16; j += 8) {
+            uint4 v;
+            v.x = pack2<T>(__uint_as_float(o[j]) * inv, __uint_as_float(o[j + 1]) * inv);
+            v.y = pack2<T>(__uint_as_float(o[j + 2]) * inv, __uint_as_float(o[j + 3]) * inv);
+            v.z = pack2<T>(__uint_as_float(o[j + 4]) * inv, __uint_as_float(o[j + 5]) * inv);
+            v.w = pack2<T>(__uint_as_float(o[j + 6]) * inv, __uint_as_float(o[j + 7]) * inv);
+            sts128(put ^ (j * 2), v);
           }
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int r = (lane >> 1) + 16 * i, g = (int)rank * CK_HALF + (quad & 1) * 32 + r, k = g >> hs;
+            const uint4 v = lds128(stage + r * 32 + (((lane & 1) ^ ((r >> 2) & 1)) * 16));
+            if (k < P.n_tok())
+              *reinterpret_cast<uint4*>(out0 + (P.tok0() + (long long)k) * A.o_tok + (g & (H - 1)) * A.o_head + c) = v;
+          }
+          __syncwarp();
         }
         if (A.lse && live && dim == 0)
           A.lse[(size_t)(P.tok0() + tk) * H + h] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
@@ -1136,38 +1187,92 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
 }
 
 // The rows of cut blocks: out = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i over the parts,
-// in pair order. CTA (row, group) looks at the cut of every group-th pair.
-constexpr int CM_THREADS = 128, CM_GROUPS = 8;
-template <typename T>
+// in pair order. A CTA has four slices of 128 threads. WIDE (few cuts, of many parts each): CTA
+// (row, k) joins that row of the k-th cut, its parts dealt to the slices. Otherwise each slice
+// joins one row of one pair's cut.
+constexpr int CM_SLICES = 4, CM_THREADS = 128 * CM_SLICES, CM_MAX_PAIRS = 128, CM_WIDE_CUTS = 32;
+template <typename T, bool WIDE>
 __global__ void __launch_bounds__(CM_THREADS) chunk_merge_kernel(const Dev D, const ChunkArgs A) {
+  __shared__ float4 acc[CM_SLICES][128];
+  __shared__ float2 ml[CM_SLICES];
+  __shared__ int mine;
   griddep_wait();
   const ChunkWork W = work_at(A.work, A.pairs);
-  const int row = blockIdx.x, tid = threadIdx.x, H = D.n_heads;
-  for (int p = blockIdx.y; p < A.pairs; p += CM_GROUPS) {
-    const ChunkCut cut = W.cut[p];
-    if (row >= cut.n_tok * H) continue;
-    float m = -INFINITY;
-    for (int i = p; i <= cut.last_pair; ++i)
-      m = fmaxf(m, W.stats[((size_t)i * 2 + (i == p ? 1 : 0)) * CK_ROWS + row].x);
-    float l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int tid = threadIdx.x, slice = tid >> 7, col = tid & 127, row = blockIdx.x, H = D.n_heads;
+  int p = blockIdx.y * CM_SLICES + slice;
+  if (WIDE) {   // the blockIdx.y-th pair that has a cut
+    if (tid == 0) mine = A.pairs;
+    __syncthreads();
+    if (tid < 32) {
+      int before = 0;
+      for (int i = tid; i - tid < A.pairs; i += 32) {
+        const bool has = i < A.pairs && W.cut[i].n_tok > 0;
+        const unsigned b = __ballot_sync(0xffffffffu, has);
+        if (has && before + __popc(b & ((1u << tid) - 1)) == (int)blockIdx.y) mine = i;
+        before += __popc(b);
+      }
+    }
+    __syncthreads();
+    p = mine;
+    if (p >= A.pairs) return;
+  } else if (p >= A.pairs) {
+    return;
+  }
+  const ChunkCut cut = W.cut[p];
+  if (row >= cut.n_tok * H) return;
+  auto part_at = [&](int i) { return ((size_t)i * 2 + (i == p ? 1 : 0)) * CK_ROWS + row; };
+  const int step = WIDE ? CM_SLICES : 1;
+  float m = -INFINITY, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i = p + (WIDE ? slice : 0); i <= cut.last_pair; i += 8 * step) {
+    // eight parts at a time, all of their loads in flight
+    float2 s[8];
+    float4 v[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const bool in = i + u * step <= cut.last_pair;
+      s[u] = in ? W.stats[part_at(i + u * step)] : make_float2(-INFINITY, 0.f);
+      v[u] = in ? *(reinterpret_cast<const float4*>(W.part + part_at(i + u * step) * 512) + col) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    float mn = m;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) mn = fmaxf(mn, s[u].x);
+    if (mn == -INFINITY) continue;
+    const float f = exp2f(m - mn);
+    m = mn;
+    l *= f;
+    o.x *= f, o.y *= f, o.z *= f, o.w *= f;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const float w = exp2f(s[u].x - mn);
+      l += w * s[u].y;
+      o.x += w * v[u].x, o.y += w * v[u].y, o.z += w * v[u].z, o.w += w * v[u].w;
+    }
+  }
+  if (WIDE) {
+    acc[slice][col] = o;
+    if (col == 0) ml[slice] = make_float2(m, l);
+    __syncthreads();
+    if (slice > 0) return;
+    m = fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x));
+    l = 0.f;
+    o = make_float4(0.f, 0.f, 0.f, 0.f);
     if (m > -INFINITY) {
-#pragma unroll 4
-      for (int i = p; i <= cut.last_pair; ++i) {
-        const size_t at = ((size_t)i * 2 + (i == p ? 1 : 0)) * CK_ROWS + row;
-        const float2 s = W.stats[at];
-        const float w = exp2f(s.x - m);
-        const float4 v = *(reinterpret_cast<const float4*>(W.part + at * 512) + tid);
-        l += w * s.y;
+#pragma unroll
+      for (int u = 0; u < CM_SLICES; ++u) {
+        const float w = exp2f(ml[u].x - m);
+        const float4 v = acc[u][col];
+        l += w * ml[u].y;
         o.x += w * v.x, o.y += w * v.y, o.z += w * v.z, o.w += w * v.w;
       }
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    const int tok = cut.tok0 + row / H, h = row % H;
-    T* op = static_cast<T*>(A.out) + tok * A.o_tok + h * A.o_head + tid * 4;
-    *reinterpret_cast<uint2*>(op) = make_uint2(pack2<T>(o.x * inv, o.y * inv), pack2<T>(o.z * inv, o.w * inv));
-    if (A.lse && tid == 0) A.lse[(size_t)tok * H + h] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
   }
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const int tok = cut.tok0 + row / H, h = row % H;
+  T* op = static_cast<T*>(A.out) + tok * A.o_tok + h * A.o_head + col * 4;
+  *reinterpret_cast<uint2*>(op) = make_uint2(pack2<T>(o.x * inv, o.y * inv), pack2<T>(o.z * inv, o.w * inv));
+  // the outputs carry CK_V_FACTOR, and so do the sums
+  if (A.lse && col == 0) A.lse[(size_t)tok * H + h] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
 
 struct CallRange {
@@ -1192,7 +1297,16 @@ hs_status launch_chunk(hs_pool* p, const ChunkArgs& a, cudaStream_t st) {
   if (regs.load(std::memory_order_relaxed) < CK_REGS) return HS_ERR_CUDA;
   const hs_status s = launch_pdl(chunk_attention_kernel<T>, dim3(2 * a.pairs), dim3(CK_THREADS), CK_SMEM, st, 2, p->d, a);
   if (s != HS_OK) return s;
-  return launch_pdl(chunk_merge_kernel<T>, dim3(CK_ROWS, CM_GROUPS), dim3(CM_THREADS), 0, st, 0, p->d, a);
+  // a pair has at most one cut, and there are no more cuts than blocks
+  const int tpb = CK_ROWS / p->cfg.n_heads;
+  const long long blocks = (long long)a.n_seg + a.n_tok / tpb;
+  const int cuts = blocks < a.pairs ? (int)blocks : a.pairs;
+  const long long rows = (long long)a.n_tok * p->cfg.n_heads;
+  const int grid_rows = rows < CK_ROWS ? (int)rows : CK_ROWS;
+  if (cuts <= CM_WIDE_CUTS)
+    return launch_pdl(chunk_merge_kernel<T, true>, dim3(grid_rows, cuts), dim3(CM_THREADS), 0, st, 0, p->d, a);
+  return launch_pdl(chunk_merge_kernel<T, false>, dim3(grid_rows, (a.pairs + CM_SLICES - 1) / CM_SLICES), dim3(CM_THREADS), 0,
+                    st, 0, p->d, a);
 }
 
 }  // namespace
