@@ -997,6 +997,25 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
         bool ignore = false;
         lim = clamp_limit(D, __ldg(A.limit + P.tok0() + tk), &ignore);
       }
+      if (((int)rank * CK_HALF + (quad & 1) * 32) >> hs >= P.n_tok()) {
+        // none of these 32 rows is a token's (nor of the other three warps'): their P is 0, and
+        // what the products make of it is not read
+        sts128(p_lo, make_uint4(0, 0, 0, 0));
+        sts128(p_hi, make_uint4(0, 0, 0, 0));
+        fence_proxy_async();
+        for (int pg = P.pg0(); pg < P.pg1(); ++pg, ++it) {
+          const uint32_t st = it & 1;
+          ok &= ck_wait(bar(B_SD + st), (it >> 1) & 1, D.status, dead);
+          __syncwarp();
+          if (lane == 0) {
+            arrive_cluster(sr0);
+            arrive_cluster(pf0 + 8 * st);
+          }
+          if (!__all_sync(0xffffffffu, ok)) break;
+        }
+        if (it > 0) ok &= ck_wait(bar(B_PD + ((it - 1) & 1)), ((it - 1) >> 1) & 1, D.status, dead);
+        continue;
+      }
       float m = -INFINITY, l = 0.f;   // the row's reference (its four threads alike), this thread's sum
       for (int pg = P.pg0(); pg < P.pg1(); ++pg, ++it) {
         const uint32_t st = it & 1;

@@ -133,20 +133,35 @@ def _host_array(values, ctype):
     return ctypes.cast(arr, _P), arr
 
 
+class _Torch:
+    """What the prefill calls take from torch, looked up once: at a few microseconds of GPU
+    time for a small call, the host's share of each call counts."""
+    codes: dict = {}
+    int32 = None
+    raw_stream = None
+
+    @classmethod
+    def load(cls) -> None:
+        import torch
+        cls.int32 = torch.int32
+        cls.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        cls.codes = {torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32}
+
+
 def _dtype(t) -> int:
-    import torch
-    code = {torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32}.get(t.dtype)
+    if not _Torch.codes:
+        _Torch.load()
+    code = _Torch.codes.get(t.dtype)
     if code is None:
         raise ValueError(f"element type {t.dtype}: bfloat16, float16 or float32 is wanted")
     return code
 
 
-def _ids(name: str, t, n: int, device: int) -> int:
-    """The address of an int32 array of n elements."""
-    if t.dim() != 1 or t.shape[0] != n or t.element_size() != 4 or t.is_floating_point() or not t.is_contiguous():
-        raise ValueError(f"{name}: a contiguous int32 tensor of {n} elements is wanted")
-    _on(name, t, device)
-    return t.data_ptr()
+def _stream_of(stream, device: int) -> Optional[int]:
+    """_stream() for a pool's device, without building a stream object."""
+    if stream is None and _Torch.raw_stream is not None and device >= 0:
+        return _Torch.raw_stream(device)
+    return _stream(stream)
 
 
 def _on(name: str, t, device: int) -> None:
@@ -154,13 +169,23 @@ def _on(name: str, t, device: int) -> None:
         raise ValueError(f"{name}: on {t.device}, the pool is on cuda:{device}")
 
 
-def _values(name: str, t, n: int, width: int, dtype: int, device: int):
+def _ids(name: str, t, n: int, device: int) -> int:
+    """The address of an int32 array of n elements."""
+    if t.shape != (n,) or t.dtype is not _Torch.int32 or not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous int32 tensor of {n} elements is wanted")
+    if t.get_device() != device:
+        _on(name, t, device)
+    return t.data_ptr()
+
+
+def _values(name: str, t, n: int, width: int, dtype, device: int):
     """Address and row stride of [n, width] values whose last dimension is contiguous."""
     if t is None:
         return None, 0
-    if t.dim() != 2 or t.shape[0] != n or t.shape[1] != width or t.stride(1) != 1 or _dtype(t) != dtype:
+    if t.shape != (n, width) or t.dtype is not dtype or t.stride(1) != 1:
         raise ValueError(f"{name}: a [{n}, {width}] tensor of the call's element type is wanted, last stride 1")
-    _on(name, t, device)
+    if t.get_device() != device:
+        _on(name, t, device)
     return t.data_ptr(), t.stride(0) if n > 1 else width
 
 
@@ -259,11 +284,11 @@ class Pool:
 
     # -- prefill and dense decode, one layer at a time ---------------------------------
     def _cache_args(self, req, pos, latent, rope, keys):
-        first = next((t for t in (latent, rope, keys) if t is not None), None)
+        first = latent if latent is not None else rope if rope is not None else keys
         if first is None:
             raise ValueError("none of latent, rope and keys is given")
-        n, dtype, dev = req.shape[0], _dtype(first), self.device
-        return (n, _ids("req", req, n, dev), _ids("pos", pos, n, dev), dtype,
+        code, dtype, n, dev = _dtype(first), first.dtype, req.shape[0], self.device
+        return (n, _ids("req", req, n, dev), _ids("pos", pos, n, dev), code,
                 *_values("latent", latent, n, 512, dtype, dev), *_values("rope", rope, n, 64, dtype, dev),
                 *_values("keys", keys, n, 128, dtype, dev))
 
@@ -273,14 +298,16 @@ class Pool:
         (both or neither), index keys [n, 128]; bf16, fp16 or fp32, rows may be strided.
         key_scale: the step of int8 index keys."""
         _check("hs_append_quantized", lib.hs_append_quantized(
-            self.handle, layer, *self._cache_args(req, pos, latent, rope, keys), key_scale, _stream(stream)))
+            self.handle, layer, *self._cache_args(req, pos, latent, rope, keys), key_scale,
+            _stream_of(stream, self.device)))
 
     def read_rows(self, layer: int, req, pos, latent=None, rope=None, keys=None, key_scale: float = 1.0,
                   stream=None) -> None:
         """Read cached positions of one layer back into latent [n, 512], rope [n, 64] and
         keys [n, 128] (any of them), in their element type."""
         _check("hs_read_rows", lib.hs_read_rows(
-            self.handle, layer, *self._cache_args(req, pos, latent, rope, keys), key_scale, _stream(stream)))
+            self.handle, layer, *self._cache_args(req, pos, latent, rope, keys), key_scale,
+            _stream_of(stream, self.device)))
 
     def chunk_workspace_bytes(self) -> int:
         """Bytes of device workspace that chunk_attention needs, whatever the call's sizes."""
@@ -294,21 +321,24 @@ class Pool:
         tokens [seg_start[i], seg_start[i + 1]) of request seg_req[i]; limit [n]; q [n, H, 576]
         and out [n, H, 512] bf16 or fp16, the last dimension contiguous; lse [n, H] fp32;
         work: chunk_workspace_bytes() bytes that no overlapping call uses."""
-        n, segs, heads, dtype, dev = limit.shape[0], seg_req.shape[0], self.cfg.n_heads, _dtype(q), self.device
-        if q.shape != (n, heads, 576) or out.shape != (n, heads, 512) or out.dtype != q.dtype or \
-                q.stride(2) != 1 or out.stride(2) != 1:
-            raise ValueError(f"q [{n}, {heads}, 576] and out [{n}, {heads}, 512] of one type are wanted, last stride 1")
+        code, n, segs, heads, dev = _dtype(q), limit.shape[0], seg_req.shape[0], self.cfg.n_heads, self.device
+        if q.shape != (n, heads, 576) or out.shape != (n, heads, 512) or out.dtype is not q.dtype:
+            raise ValueError(f"q [{n}, {heads}, 576] and out [{n}, {heads}, 512] of one type are wanted")
+        qs, os = q.stride(), out.stride()
+        if qs[2] != 1 or os[2] != 1:
+            raise ValueError("q and out: a contiguous last dimension is wanted")
         if lse is not None and (lse.shape != (n, heads) or _dtype(lse) != FP32 or not lse.is_contiguous()):
             raise ValueError(f"lse: a contiguous fp32 [{n}, {heads}] tensor is wanted")
         if not work.is_contiguous():
             raise ValueError("work: a contiguous tensor is wanted")
-        for name, t in (("q", q), ("out", out), ("work", work)) + ((("lse", lse),) if lse is not None else ()):
-            _on(name, t, dev)
+        if q.get_device() != dev or out.get_device() != dev or work.get_device() != dev or \
+                (lse is not None and lse.get_device() != dev):
+            raise ValueError(f"q, out, lse or work is not on the pool's device, cuda:{dev}")
         _check("hs_chunk_attention", lib.hs_chunk_attention(
             self.handle, layer, segs, _ids("seg_req", seg_req, segs, dev), _ids("seg_start", seg_start, segs + 1, dev),
-            n, _ids("limit", limit, n, dev), dtype, q.data_ptr(), q.stride(0) if n > 1 else heads * 576, q.stride(1),
-            sm_scale, out.data_ptr(), out.stride(0) if n > 1 else heads * 512, out.stride(1), _ptr(lse),
-            work.data_ptr(), work.numel() * work.element_size(), _stream(stream)))
+            n, _ids("limit", limit, n, dev), code, q.data_ptr(), qs[0] if n > 1 else heads * 576, qs[1], sm_scale,
+            out.data_ptr(), os[0] if n > 1 else heads * 512, os[1], None if lse is None else lse.data_ptr(),
+            work.data_ptr(), work.numel() * work.element_size(), _stream_of(stream, dev)))
 
     # -- status --------------------------------------------------------------------
     def get_error(self, stream=None) -> int:
