@@ -9,10 +9,11 @@
 // Both divisions are the correctly rounded fp32 ones: a code can differ from the one of
 // unrounded arithmetic only where x / scale lies within 2^-23 of a rounding border.
 //
-// One warp per token. Lane l holds latent values 256 j + 8 l .. + 7 (j = 0, 1), so that
-// every load and store of a warp is one contiguous run, and the 16 lanes of a half warp
-// hold exactly one 128-value group.
+// A warp takes a token (two when reading) at a time. Lane l holds latent values
+// 256 j + 8 l .. + 7 (j = 0, 1), so that every load and store of a warp is one contiguous
+// run, and the 16 lanes of a half warp hold exactly one 128-value group.
 #include <cuda_fp8.h>
+#include <float.h>
 #include <math.h>
 #include <nvtx3/nvToolsExt.h>
 
@@ -22,7 +23,9 @@ namespace hs {
 
 namespace {
 
-constexpr int CA_WARPS = 8;          // warps per CTA
+constexpr int CA_WARPS = 4;          // warps per CTA
+constexpr int CA_TOK = 2;            // tokens a warp reads back at a time
+constexpr int CA_CTAS = 40;          // CTAs per SM that share the tokens
 constexpr float E4M3_MAX = 448.f;
 constexpr float MIN_SCALE = 1.17549435e-38f;   // the smallest normal fp32: x / scale stays finite and below 448
 constexpr float BF16_MAX = 3.38953139e38f;
@@ -70,31 +73,79 @@ __device__ __forceinline__ void store_f32(T* p, const float (&v)[N]) {
   }
 }
 
-// The largest finite magnitude of v; a NaN becomes 0 and an infinity counts as no
-// magnitude (it saturates later); either sets *bad.
+// The largest magnitude of v: NaN when one is NaN, else infinite when one is infinite.
 template <int N>
-__device__ __forceinline__ float finite_amax(float (&v)[N], bool* bad) {
-  float a = 0.f;
+__device__ __forceinline__ float amax_of(const float (&v)[N]) {
+  float a = max_nan(fabsf(v[0]), fabsf(v[1]));
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const float x = fabsf(v[i]);
-    const bool fin = x <= 3.402823466e38f;   // false for NaN and infinity
-    *bad |= !fin;
-    a = fmaxf(a, fin ? x : 0.f);
-    if (x != x) v[i] = 0.f;
-  }
+  for (int i = 2; i < N; i += 2) a = max3_nan(a, fabsf(v[i]), fabsf(v[i + 1]));
   return a;
 }
-__device__ __forceinline__ float scale_of(float amax) {
-  return amax > 0.f ? fmaxf(__fdiv_rn(amax, E4M3_MAX), MIN_SCALE) : 1.f;
+template <int LANES>
+__device__ __forceinline__ float lanes_amax(float a) {
+#pragma unroll
+  for (int o = LANES / 2; o >= 1; o >>= 1) a = max_nan(a, __shfl_xor_sync(0xffffffffu, a, o));
+  return a;
 }
-// Four values over a scale as four e4m3 codes.
-__device__ __forceinline__ uint32_t codes4(const float* v, float scale) {
-  const __nv_fp8x2_storage_t lo = __nv_cvt_float2_to_fp8x2(
-      make_float2(__fdiv_rn(v[0], scale), __fdiv_rn(v[1], scale)), __NV_SATFINITE, __NV_E4M3);
-  const __nv_fp8x2_storage_t hi = __nv_cvt_float2_to_fp8x2(
-      make_float2(__fdiv_rn(v[2], scale), __fdiv_rn(v[3], scale)), __NV_SATFINITE, __NV_E4M3);
-  return (uint32_t)lo | ((uint32_t)hi << 16);
+// x / scale, correctly rounded, for the many x of one scale: with r the correctly rounded
+// reciprocal and q within one unit of the quotient, q + r (x - q scale) rounds to it
+// (P. Markstein, IBM J. Res. Dev. 34(1), 1990, theorem 2), in three operations each. It
+// needs x - q scale to be exact, which holds far from the smallest normal numbers: smaller
+// amax go through the division itself.
+__device__ __forceinline__ float over(float x, float scale, float r) {
+  const float q = x * r;
+  return fmaf(fmaf(-q, scale, x), r, q);
+}
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3) |
+         (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3) << 16;
+}
+// The rare groups (a value that is not finite, or an amax below 2^-60), out of line: a NaN
+// becomes 0, an infinity takes the group's largest finite magnitude, which is the largest code.
+__device__ __noinline__ float rare_value(float x, float amax) {
+  const float a = fabsf(x);
+  return a <= FLT_MAX ? x : x != x ? 0.f : copysignf(amax > 0.f ? amax : E4M3_MAX, x);
+}
+__device__ __noinline__ float rare_quotient(float x, float scale) { return __fdiv_rn(x, scale); }
+// The N values that each of LANES lanes holds of one group, as N / 4 words of e4m3 codes;
+// returns the group's scale. *bad: a value was not finite.
+template <int N, int LANES>
+__device__ __forceinline__ float quantise(float (&v)[N], uint32_t (&code)[N / 4], bool* bad) {
+  float a = lanes_amax<LANES>(amax_of(v));
+  if ((a >= 8.6736174e-19f && a <= FLT_MAX) || a == 0.f) {   // 2^-60
+    const float scale = a > 0.f ? over(a, E4M3_MAX, 1.f / E4M3_MAX) : 1.f;
+    const float rs = __frcp_rn(scale);
+    const F2 r = f2(rs), minus = f2(-scale);
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      float q[4];
+#pragma unroll
+      for (int k = 0; k < 4; k += 2) {
+        const F2 x = f2(__float_as_uint(v[i + k]), __float_as_uint(v[i + k + 1])), q0 = mul2(x, r);
+        unpack(fma2(fma2(q0, minus, x), r, q0), q[k], q[k + 1]);
+      }
+      code[i / 4] = e4m3x4(q[0], q[1], q[2], q[3]);
+    }
+    return scale;
+  }
+  if (!(a <= FLT_MAX)) {   // the same in all lanes of the group
+    *bad = true;
+    a = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (fabsf(v[i]) <= FLT_MAX) a = fmaxf(a, fabsf(v[i]));
+    const unsigned group = LANES == 32 ? 0xffffffffu : 0xffffu << (threadIdx.x & 16);
+#pragma unroll
+    for (int o = LANES / 2; o >= 1; o >>= 1) a = fmaxf(a, __shfl_xor_sync(group, a, o));
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = rare_value(v[i], a);
+  }
+  const float scale = a > 0.f ? fmaxf(rare_quotient(a, E4M3_MAX), MIN_SCALE) : 1.f;
+#pragma unroll
+  for (int i = 0; i < N; i += 4)
+    code[i / 4] = e4m3x4(rare_quotient(v[i], scale), rare_quotient(v[i + 1], scale), rare_quotient(v[i + 2], scale),
+                         rare_quotient(v[i + 3], scale));
+  return scale;
 }
 __device__ __forceinline__ void values4(uint32_t w, float scale, float* v) {
   const float2 a = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xFFFFu), __NV_E4M3)));
@@ -102,138 +153,169 @@ __device__ __forceinline__ void values4(uint32_t w, float scale, float* v) {
   v[0] = a.x * scale, v[1] = a.y * scale, v[2] = b.x * scale, v[3] = b.y * scale;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(CA_WARPS * 32)
-append_quantized_kernel(Dev D, int layer, int n, const int32_t* __restrict__ req_of, const int32_t* __restrict__ pos_of,
-                        const T* __restrict__ latent, long long ld_latent, const T* __restrict__ rope,
-                        long long ld_rope, const T* __restrict__ keys, long long ld_keys, float key_scale) {
-  griddep_wait();
-  const int lane = threadIdx.x & 31;
-  const int t = blockIdx.x * CA_WARPS + (threadIdx.x >> 5);
-  if (t >= n) return;
-  const int r = req_of[t], pos = pos_of[t];
-  if (r == -1) return;   // padding
-  if (r < 0 || r >= D.max_requests || pos < 0 || pos >= D.max_ctx) {
-    if (lane == 0) set_status(D.status, HS_ERR_BAD_ID);
-    return;
+// Where one token goes or comes from: its block-table entry's index, or -1 (padding, a bad id).
+struct Place {
+  int r, pos;
+  long long at;
+};
+__device__ __forceinline__ Place place_of(const Dev& D, const int32_t* req_of, const int32_t* pos_of, int t, int n) {
+  Place p = {-1, 0, -1};
+  if (t >= n) return p;
+  p.r = req_of[t], p.pos = pos_of[t];
+  if (p.r == -1) return p;
+  if (p.r < 0 || p.r >= D.max_requests || p.pos < 0 || p.pos >= D.max_ctx) {
+    if ((threadIdx.x & 31) == 0) set_status(D.status, HS_ERR_BAD_ID);
+    return p;
   }
-  // the same position again in the next token: that one is written
-  if (t + 1 < n && req_of[t + 1] == r && pos_of[t + 1] == pos) return;
-  const size_t at = (size_t)r * D.max_pages + (pos >> 6);
-  bool bad = false;
-  if (latent) {
-    const int pg = D.bt[at];
-    if (pg < 0 || pg >= D.num_pages) {
-      if (lane == 0) set_status(D.status, HS_ERR_BAD_ID);
-    } else {
-      uint8_t* row = D.kv[layer] + ((size_t)pg * PAGE + (pos & 63)) * ROW;
-      float v[2][8], rp[2], sc[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) load_f32<T, 8>(latent + t * ld_latent + j * 256 + lane * 8, v[j]);
-      load_f32<T, 2>(rope + t * ld_rope + lane * 2, rp);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        float a = finite_amax(v[j], &bad);
-#pragma unroll
-        for (int o = 8; o >= 1; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-        sc[j] = scale_of(a);
-        *reinterpret_cast<uint2*>(row + j * 256 + lane * 8) = make_uint2(codes4(v[j], sc[j]), codes4(v[j] + 4, sc[j]));
-      }
-      const float s1 = __shfl_sync(0xffffffffu, sc[0], 16), s3 = __shfl_sync(0xffffffffu, sc[1], 16);
-      if (lane == 0) *reinterpret_cast<float4*>(row + LATENT) = make_float4(sc[0], s1, sc[1], s3);
-      finite_amax(rp, &bad);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) rp[i] = fminf(fmaxf(rp[i], -BF16_MAX), BF16_MAX);
-      store_f32<__nv_bfloat16, 2>(reinterpret_cast<__nv_bfloat16*>(row + LATENT + 16) + lane * 2, rp);
-    }
-  }
-  if (keys) {
-    const int ip = D.idx_bt[at];
-    if (ip < 0 || ip >= D.num_idx_pages) {
-      if (lane == 0) set_status(D.status, HS_ERR_BAD_ID);
-    } else {
-      uint8_t* page = reinterpret_cast<uint8_t*>(D.idx[layer / D.lpi]) + (size_t)ip * D.idx_page_bytes;
-      uint32_t* code = reinterpret_cast<uint32_t*>(page + (pos & 63) * IDX_DIM) + lane;
-      float v[4];
-      load_f32<T, 4>(keys + t * ld_keys + lane * 4, v);
-      float a = finite_amax(v, &bad);
-      if (D.idx_fmt == HS_IDX_FP8) {
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-        const float s = scale_of(a);
-        *code = codes4(v, s);
-        if (lane == 0) *reinterpret_cast<float*>(page + PAGE * IDX_DIM + (pos & 63) * 4) = s;
-      } else {
-        uint32_t w = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float q = fminf(fmaxf(rintf(__fdiv_rn(v[i], key_scale)), -127.f), 127.f);
-          w |= ((uint32_t)(int)q & 0xFFu) << (8 * i);
-        }
-        *code = w;
-      }
-    }
-  }
-  if (__any_sync(0xffffffffu, bad) && lane == 0) set_status(D.status, HS_ERR_RANGE);
+  p.at = (long long)p.r * D.max_pages + (p.pos >> 6);
+  return p;
 }
 
 template <typename T>
 __global__ void __launch_bounds__(CA_WARPS * 32)
-read_rows_kernel(Dev D, int layer, int n, const int32_t* __restrict__ req_of, const int32_t* __restrict__ pos_of,
+append_quantized_kernel(const Dev D, int layer, int group, int n, const int32_t* __restrict__ req_of,
+                        const int32_t* __restrict__ pos_of, const T* __restrict__ latent, long long ld_latent,
+                        const T* __restrict__ rope, long long ld_rope, const T* __restrict__ keys, long long ld_keys,
+                        float key_scale) {
+  griddep_wait();
+  const int lane = threadIdx.x & 31, stride = gridDim.x * CA_WARPS;
+  uint8_t* const kv_rows = D.kv[layer];
+  uint8_t* const idx = reinterpret_cast<uint8_t*>(D.idx[group]);
+  bool bad = false;
+  int t = blockIdx.x * CA_WARPS + (threadIdx.x >> 5);
+  Place next = place_of(D, req_of, pos_of, t, n);
+  for (; t < n; t += stride) {
+    Place p = next;
+    float v[2][8], rp[2], kv[4];
+    if (latent) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) load_f32<T, 8>(latent + t * ld_latent + j * 256 + lane * 8, v[j]);
+      load_f32<T, 2>(rope + t * ld_rope + lane * 2, rp);
+    }
+    if (keys) load_f32<T, 4>(keys + t * ld_keys + lane * 4, kv);
+    const int pg = latent && p.at >= 0 ? D.bt[p.at] : 0, ip = keys && p.at >= 0 ? D.idx_bt[p.at] : 0;
+    next = place_of(D, req_of, pos_of, t + stride, n);
+    if (t + 1 < n && p.at >= 0 && req_of[t + 1] == p.r && pos_of[t + 1] == p.pos)
+      p.at = -1;   // the same position again in the next token: that one is written
+    if (p.at < 0) continue;
+    const int off = p.pos & 63;
+    if ((pg < 0 || pg >= D.num_pages || ip < 0 || ip >= D.num_idx_pages) && lane == 0) set_status(D.status, HS_ERR_BAD_ID);
+    if (latent && pg >= 0 && pg < D.num_pages) {
+      uint8_t* row = kv_rows + ((size_t)pg * PAGE + off) * ROW;
+      float sc[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        uint32_t code[2];
+        sc[j] = quantise<8, 16>(v[j], code, &bad);
+        *reinterpret_cast<uint2*>(row + j * 256 + lane * 8) = make_uint2(code[0], code[1]);
+      }
+      const float s1 = __shfl_sync(0xffffffffu, sc[0], 16), s3 = __shfl_sync(0xffffffffu, sc[1], 16);
+      if (lane == 0) *reinterpret_cast<float4*>(row + LATENT) = make_float4(sc[0], s1, sc[1], s3);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float x = fminf(fmaxf(rp[i], -BF16_MAX), BF16_MAX);
+        bad |= !(fabsf(rp[i]) <= FLT_MAX);
+        rp[i] = rp[i] != rp[i] ? 0.f : x;
+      }
+      store_f32<__nv_bfloat16, 2>(reinterpret_cast<__nv_bfloat16*>(row + LATENT + 16) + lane * 2, rp);
+    }
+    if (keys && ip >= 0 && ip < D.num_idx_pages) {
+      uint8_t* page = idx + (size_t)ip * D.idx_page_bytes;
+      uint32_t w[1] = {0};
+      if (D.idx_fmt == HS_IDX_FP8) {
+        const float scale = quantise<4, 32>(kv, w, &bad);
+        if (lane == 0) *reinterpret_cast<float*>(page + PAGE * IDX_DIM + off * 4) = scale;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          bad |= !(fabsf(kv[i]) <= FLT_MAX);
+          const float q = kv[i] != kv[i] ? 0.f : fminf(fmaxf(rintf(__fdiv_rn(kv[i], key_scale)), -127.f), 127.f);
+          w[0] |= ((uint32_t)(int)q & 0xFFu) << (8 * i);
+        }
+      }
+      *(reinterpret_cast<uint32_t*>(page + off * IDX_DIM) + lane) = w[0];
+    }
+  }
+  if (bad) set_status(D.status, HS_ERR_RANGE);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(CA_WARPS * 32)
+read_rows_kernel(const Dev D, int layer, int group, int n, const int32_t* __restrict__ req_of, const int32_t* __restrict__ pos_of,
                  T* __restrict__ latent, long long ld_latent, T* __restrict__ rope, long long ld_rope,
                  T* __restrict__ keys, long long ld_keys, float key_scale) {
   griddep_wait();
   const int lane = threadIdx.x & 31;
-  const int t = blockIdx.x * CA_WARPS + (threadIdx.x >> 5);
-  if (t >= n) return;
-  const int r = req_of[t], pos = pos_of[t];
-  if (r == -1) return;   // padding
-  if (r < 0 || r >= D.max_requests || pos < 0 || pos >= D.max_ctx) {
-    if (lane == 0) set_status(D.status, HS_ERR_BAD_ID);
-    return;
-  }
-  if (latent || rope) {
+  const uint8_t* const idx = reinterpret_cast<const uint8_t*>(D.idx[group]);
+  for (int t0 = (blockIdx.x * CA_WARPS + (threadIdx.x >> 5)) * CA_TOK; t0 < n; t0 += gridDim.x * CA_WARPS * CA_TOK) {
+  const uint8_t *row[CA_TOK], *page[CA_TOK];   // the token's row and index-key page, or null
+  int off[CA_TOK];
+#pragma unroll
+  for (int u = 0; u < CA_TOK; ++u) {
+    const Place p = place_of(D, req_of, pos_of, t0 + u, n);
+    row[u] = page[u] = nullptr;
+    off[u] = p.pos & 63;
+    if (p.at < 0) continue;
     int err = HS_OK;
-    const uint8_t* page = page_rows(D, layer, r, pos >> 6, &err);
-    if (!page) {
-      if (lane == 0) set_status(D.status, err);
-    } else {
-      const uint8_t* row = page + (size_t)(pos & 63) * ROW;
+    if (latent || rope) {
+      row[u] = page_rows(D, layer, p.r, p.pos >> 6, &err);
+      if (row[u]) row[u] += (size_t)off[u] * ROW;
+    }
+    if (keys) {
+      const int ip = D.idx_bt[p.at];
+      if (ip >= 0 && ip < D.num_idx_pages)
+        page[u] = idx + (size_t)ip * D.idx_page_bytes;
+      else
+        err = HS_ERR_BAD_ID;
+    }
+    if (err != HS_OK && lane == 0) set_status(D.status, err);
+  }
+  uint2 w[CA_TOK][2];
+  float4 s4[CA_TOK];
+  float rv[CA_TOK][2], ks[CA_TOK];
+  uint32_t kw[CA_TOK];
+#pragma unroll
+  for (int u = 0; u < CA_TOK; ++u) {
+    if (row[u]) {
       if (latent) {
-        const float4 s4 = *reinterpret_cast<const float4*>(row + LATENT);
+        s4[u] = *reinterpret_cast<const float4*>(row[u] + LATENT);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) w[u][j] = *reinterpret_cast<const uint2*>(row[u] + j * 256 + lane * 8);
+      }
+      if (rope) load_f32<__nv_bfloat16, 2>(reinterpret_cast<const __nv_bfloat16*>(row[u] + LATENT + 16) + lane * 2, rv[u]);
+    }
+    if (page[u]) {
+      kw[u] = *(reinterpret_cast<const uint32_t*>(page[u] + off[u] * IDX_DIM) + lane);
+      ks[u] = D.idx_fmt == HS_IDX_FP8 ? *reinterpret_cast<const float*>(page[u] + PAGE * IDX_DIM + off[u] * 4) : key_scale;
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < CA_TOK; ++u) {
+    const long long t = t0 + u;
+    if (row[u]) {
+      if (latent) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const uint2 w = *reinterpret_cast<const uint2*>(row + j * 256 + lane * 8);
-          const float s = j == 0 ? (lane < 16 ? s4.x : s4.y) : (lane < 16 ? s4.z : s4.w);
+          const float s = j == 0 ? (lane < 16 ? s4[u].x : s4[u].y) : (lane < 16 ? s4[u].z : s4[u].w);
           float v[8];
-          values4(w.x, s, v);
-          values4(w.y, s, v + 4);
+          values4(w[u][j].x, s, v);
+          values4(w[u][j].y, s, v + 4);
           store_f32<T, 8>(latent + t * ld_latent + j * 256 + lane * 8, v);
         }
       }
-      if (rope) {
-        float v[2];
-        load_f32<__nv_bfloat16, 2>(reinterpret_cast<const __nv_bfloat16*>(row + LATENT + 16) + lane * 2, v);
-        store_f32<T, 2>(rope + t * ld_rope + lane * 2, v);
-      }
+      if (rope) store_f32<T, 2>(rope + t * ld_rope + lane * 2, rv[u]);
     }
-  }
-  if (keys) {
-    const int ip = D.idx_bt[(size_t)r * D.max_pages + (pos >> 6)];
-    if (ip < 0 || ip >= D.num_idx_pages) {
-      if (lane == 0) set_status(D.status, HS_ERR_BAD_ID);
-    } else {
-      const uint8_t* page = reinterpret_cast<const uint8_t*>(D.idx[layer / D.lpi]) + (size_t)ip * D.idx_page_bytes;
-      const uint32_t w = *(reinterpret_cast<const uint32_t*>(page + (pos & 63) * IDX_DIM) + lane);
+    if (page[u]) {
       float v[4];
       if (D.idx_fmt == HS_IDX_FP8) {
-        values4(w, *reinterpret_cast<const float*>(page + PAGE * IDX_DIM + (pos & 63) * 4), v);
+        values4(kw[u], ks[u], v);
       } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = (float)(int8_t)(w >> (8 * i)) * key_scale;
+        for (int i = 0; i < 4; ++i) v[i] = (float)(int8_t)(kw[u] >> (8 * i)) * ks[u];
       }
       store_f32<T, 4>(keys + t * ld_keys + lane * 4, v);
     }
+  }
   }
 }
 
@@ -267,6 +349,12 @@ CallArgs check_call(hs_pool* p, int32_t layer, int32_t n, const int32_t* d_req, 
   return a;
 }
 
+// Up to CA_CTAS CTAs per SM, which take the rest of the tokens in turn.
+int cache_grid(int n, int per_warp) {
+  const long long need = ((long long)n + CA_WARPS * per_warp - 1) / (CA_WARPS * per_warp), wave = (long long)num_sms() * CA_CTAS;
+  return (int)(need < wave ? need : wave);
+}
+
 struct CallRange {
   explicit CallRange(const char* name) { nvtxRangePushA(name); }
   ~CallRange() { nvtxRangePop(); }
@@ -276,8 +364,8 @@ template <typename T>
 hs_status launch_append_quantized(hs_pool* p, int layer, int n, const int32_t* d_req, const int32_t* d_pos,
                                   const void* d_latent, int64_t ld_latent, const void* d_rope, int64_t ld_rope,
                                   const void* d_keys, int64_t ld_keys, float key_scale, cudaStream_t st) {
-  return launch_pdl(append_quantized_kernel<T>, dim3((n + CA_WARPS - 1) / CA_WARPS), dim3(CA_WARPS * 32), 0, st, 0,
-                    p->d, layer, n, d_req, d_pos, static_cast<const T*>(d_latent), (long long)ld_latent,
+  return launch_pdl(append_quantized_kernel<T>, dim3(cache_grid(n, 1)), dim3(CA_WARPS * 32), 0, st, 0,
+                    p->d, layer, layer / p->d.lpi, n, d_req, d_pos, static_cast<const T*>(d_latent), (long long)ld_latent,
                     static_cast<const T*>(d_rope), (long long)ld_rope, static_cast<const T*>(d_keys),
                     (long long)ld_keys, key_scale);
 }
@@ -285,8 +373,8 @@ template <typename T>
 hs_status launch_read_rows(hs_pool* p, int layer, int n, const int32_t* d_req, const int32_t* d_pos, void* d_latent,
                            int64_t ld_latent, void* d_rope, int64_t ld_rope, void* d_keys, int64_t ld_keys,
                            float key_scale, cudaStream_t st) {
-  return launch_pdl(read_rows_kernel<T>, dim3((n + CA_WARPS - 1) / CA_WARPS), dim3(CA_WARPS * 32), 0, st, 0, p->d,
-                    layer, n, d_req, d_pos, static_cast<T*>(d_latent), (long long)ld_latent, static_cast<T*>(d_rope),
+  return launch_pdl(read_rows_kernel<T>, dim3(cache_grid(n, CA_TOK)), dim3(CA_WARPS * 32), 0, st, 0, p->d,
+                    layer, layer / p->d.lpi, n, d_req, d_pos, static_cast<T*>(d_latent), (long long)ld_latent, static_cast<T*>(d_rope),
                     (long long)ld_rope, static_cast<T*>(d_keys), (long long)ld_keys, key_scale);
 }
 
