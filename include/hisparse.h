@@ -319,6 +319,9 @@ hs_status hs_offload_pages(hs_pool* pool, int32_t n, const int32_t* d_pool_pages
 #define HS_FP16 1
 #define HS_FP32 2
 
+/* Most tokens of one hs_append_quantized or hs_read_rows call. */
+#define HS_CACHE_MAX_TOKENS 16777216
+
 /* Quantise the new rows of one layer as they are written: n_tokens KV rows of `layer`
  * and index keys of its indexer group (layer / layers_per_indexer).
  *  d_req, d_pos  [n] request slot and position of each token. req -1 skips the token
@@ -337,7 +340,7 @@ hs_status hs_offload_pages(hs_pool* pool, int32_t n, const int32_t* d_pool_pages
  * The page holding each position must be resident (HS_ERR_BAD_ID otherwise, and that part
  * of that token is not written). A NaN is written as 0 and an infinity as the largest value
  * of its format with the group's scale taken from its finite values; both set
- * HS_ERR_RANGE. */
+ * HS_ERR_RANGE. n_tokens at most HS_CACHE_MAX_TOKENS. */
 hs_status hs_append_quantized(hs_pool* pool, int32_t layer, int32_t n_tokens, const int32_t* d_req,
                               const int32_t* d_pos, int32_t dtype, const void* d_latent, int64_t ld_latent,
                               const void* d_rope, int64_t ld_rope, const void* d_keys, int64_t ld_keys,
@@ -384,12 +387,13 @@ hs_status hs_chunk_workspace(const hs_pool* pool, int64_t* bytes);
  * Rows of placeholder pages are read from the host copy through the mapping, once for every
  * 128 / H tokens that see them; a page with neither sets HS_ERR_HOST_MISSING and counts as
  * not seen. The cache may hold anything at positions that no token of the call sees.
- * Precision: z from exact products of the codes in fp32 (q rounded to fp16 where it is
- * bf16: exact from 2^-14 to 65504), softmax statistics fp32, P fp16 with 11 significant
- * bits down to 2^-21 of its row's largest, v = code * scale rounded once to fp16 (an
- * absolute 2^-25 below 2^-14). Limits: |scale| below 146, rope and q below 65504 in
- * magnitude, no e4m3 NaN code. Beyond them HS_ERR_RANGE is set; such a cached value counts
- * as 0 for every token that sees its row. */
+ * Precision: z from products of the exact codes, summed in fp32 (q rounded to fp16 where it
+ * is bf16: exact from 2^-14 to 65504 in magnitude), softmax statistics fp32, P fp16 with 11
+ * significant bits down to 2^-21 of its row's largest, v = code * scale rounded once to fp16
+ * (an absolute 2^-27 below 2^-16), sums fp32. Limits: |scale| below 36.5 (latents below
+ * 16,352), rope and q below 65504 in magnitude, no e4m3 NaN code, and finite. Beyond them
+ * HS_ERR_RANGE is set; such a scale counts as 0, a row with another such value as not seen,
+ * and a query row with one sees nothing (out 0, lse -inf). */
 hs_status hs_chunk_attention(hs_pool* pool, int32_t layer, int32_t n_segments, const int32_t* d_seg_req,
                              const int32_t* d_seg_start, int32_t n_tokens, const int32_t* d_limit, int32_t dtype,
                              const void* d_q, int64_t q_stride_token, int64_t q_stride_head, float sm_scale,

@@ -333,7 +333,7 @@ CallArgs check_call(hs_pool* p, int32_t layer, int32_t n, const int32_t* d_req, 
                     const void* d_latent, int64_t ld_latent, const void* d_rope, int64_t ld_rope, const void* d_keys,
                     int64_t ld_keys, float key_scale) {
   CallArgs a;
-  if (!p || layer < 0 || layer >= p->cfg.n_layers || n < 0) return a;
+  if (!p || layer < 0 || layer >= p->cfg.n_layers || n < 0 || n > HS_CACHE_MAX_TOKENS) return a;
   const int size = dtype_size(dtype);
   if (size == 0 || !on_pool_device(p)) return a;
   if (n > 0) {

@@ -61,7 +61,10 @@ constexpr int CK_MMA_WARP = 16, CK_PLAN_WARP = 17;
 // Registers per thread: 96 at the launch (five warpgroups), then shifted between warpgroups,
 // whose sum stays within the launch's.
 constexpr int CK_REGS = 96, CK_SM_REGS = 96, CK_CONV_REGS = 104, CK_MISC_REGS = 80;
-static_assert(2 * CK_SM_REGS + 2 * CK_CONV_REGS + CK_MISC_REGS <= CK_THREADS / 128 * CK_REGS, "register shares");
+// The softmax keeps what it was launched with; asking for more than the others free would wait
+// without end.
+static_assert(CK_SM_REGS == CK_REGS && 2 * CK_SM_REGS + 2 * CK_CONV_REGS + CK_MISC_REGS <= CK_THREADS / 128 * CK_REGS,
+              "register shares");
 constexpr int CK_ROWS = 128;       // rows of a block
 constexpr int CK_HALF = 64;        // rows of a block per CTA
 constexpr int CK_BLOCK_COST = 3;   // what a block costs besides its pages, in pages
@@ -133,6 +136,7 @@ __host__ __device__ inline ChunkWork work_at(void* base, int pairs) {
 
 struct ChunkArgs {
   int layer, n_seg, n_tok, pairs;
+  int small;         // at most 32 segments and blocks: one warp plans
   const int32_t *seg_req, *seg_start, *limit;
   const void* q;
   long long q_tok, q_head;
@@ -514,6 +518,63 @@ __device__ Range plan_range(const Dev& D, const ChunkArgs& A, int pair, int tpb,
   return r;
 }
 
+// The same for at most 32 segments and 32 blocks, by one warp without a barrier (3 us of a
+// short call); lane b keeps block b.
+struct WarpPlan {
+  int tok0, tok1, req, limit;   // of this lane's block
+};
+__device__ Range plan_range_warp(const Dev& D, const ChunkArgs& A, int pair, int tpb, WarpPlan& mine) {
+  const int lane = threadIdx.x & 31;
+  auto all_max = [&](int v) {   // inclusive
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v = max(v, u);
+    }
+    return v;
+  };
+  auto all_sum = [&](int v) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += u;
+    }
+    return v;
+  };
+  bool bad = false;
+  int s = 0, e = 0, req = -1;
+  if (lane < A.n_seg) {
+    const int s0 = __ldg(A.seg_start + lane), e0 = __ldg(A.seg_start + lane + 1);
+    req = __ldg(A.seg_req + lane);
+    s = min(max(s0, 0), A.n_tok);
+    e = min(max(e0, 0), A.n_tok);
+    bad = s != s0 || e != e0 || e < s;
+  }
+  const int start = all_max(s), end = max(start, e);
+  const int before_seg = __shfl_up_sync(0xffffffffu, start, 1);
+  bad |= lane > 0 && lane < A.n_seg && s < before_seg;
+  const int nb = lane < A.n_seg ? (end - start + tpb - 1) / tpb : 0;
+  const int upto = all_sum(nb), blk = upto - nb, n_blocks = __shfl_sync(0xffffffffu, upto, 31);
+  int seg = 0;
+  for (int i = 1; i < A.n_seg; ++i)
+    if (__shfl_sync(0xffffffffu, blk, i) <= lane) seg = i;
+  mine.tok0 = __shfl_sync(0xffffffffu, start, seg) + (lane - __shfl_sync(0xffffffffu, blk, seg)) * tpb;
+  mine.tok1 = min(mine.tok0 + tpb, __shfl_sync(0xffffffffu, end, seg));
+  mine.req = __shfl_sync(0xffffffffu, req, seg);
+  mine.limit = lane < n_blocks ? block_limit(D, A.limit, mine.tok0, mine.tok1, &bad) : 0;
+  if (bad) set_status(D.status, HS_ERR_BAD_ID);
+  const int cost = lane < n_blocks ? CK_BLOCK_COST + pages_of(mine.limit) : 0;
+  const int cost_end = all_sum(cost), all = __shfl_sync(0xffffffffu, cost_end, 31);
+  Range r = {};
+  r.per_pair = max((all + A.pairs - 1) / A.pairs, CK_MIN_COST);
+  r.at = pair * r.per_pair;
+  r.n = max(0, min(r.per_pair, all - r.at));
+  const unsigned after = __ballot_sync(0xffffffffu, cost_end > r.at);
+  r.seg = after ? __ffs(after) - 1 : 0;   // here the block
+  r.into = r.at - __shfl_sync(0xffffffffu, cost_end - cost, r.seg);
+  return r;
+}
+
 template <typename T>
 __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const Dev D, const ChunkArgs A) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -565,26 +626,41 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
   griddep_wait();
   griddep_launch();   // only the merge of this call depends on it, and waits for its end
 
-  const Range R = plan_range(D, A, pair, tpb, smem, found);
-  __syncthreads();   // the plan's arrays are done with
+  Range R = {};
+  if (!A.small) {
+    R = plan_range(D, A, pair, tpb, smem, found);
+    __syncthreads();   // the plan's arrays are done with
+  }
 
   if (warp >= CK_MMA_WARP) {
     regs_dec<CK_MISC_REGS>();
    if (warp == CK_PLAN_WARP) {
     // ------------------------------- pieces of the range -------------------------------
+    const uint8_t* const kv = D.kv[A.layer];
+    WarpPlan mine = {};
+    if (A.small) R = plan_range_warp(D, A, pair, tpb, mine);
     int seg = R.seg, t0 = R.tok0, seg_end = R.seg_t1, into = R.into, left = R.n, at = R.at;
     uint32_t k = 0, t = 0;
     int entries = -1;
-    const uint8_t* const kv = D.kv[A.layer];
     ChunkCut cut = {0, 0, 0, 0};
     bool ok = true;
     for (;; ++k) {
       int4 pa = make_int4(0, -1, -1, 0), pb = make_int4(0, 0, -1, 0);
       while (left > 0 && pa.y < 0) {   // the range's next pages: none of a block whose fixed cost it ends in
-        const int t1 = min(t0 + tpb, seg_end);
-        const int r = __ldg(A.seg_req + seg);
-        bool bad = r < 0 || r >= D.max_requests, ignore = false;
-        const int lim = block_limit(D, A.limit, t0, t1, &ignore), n_pages = pages_of(lim);
+        int t1, r, lim;
+        if (A.small) {
+          t0 = __shfl_sync(0xffffffffu, mine.tok0, seg);
+          t1 = __shfl_sync(0xffffffffu, mine.tok1, seg);
+          r = __shfl_sync(0xffffffffu, mine.req, seg);
+          lim = __shfl_sync(0xffffffffu, mine.limit, seg);
+        } else {
+          bool ignore = false;
+          t1 = min(t0 + tpb, seg_end);
+          r = __ldg(A.seg_req + seg);
+          lim = block_limit(D, A.limit, t0, t1, &ignore);
+        }
+        const bool bad = r < 0 || r >= D.max_requests;
+        const int n_pages = pages_of(lim);
         if (bad && lane == 0) set_status(D.status, HS_ERR_BAD_ID);
         const int end = min(CK_BLOCK_COST + n_pages, into + left), used = end - into;
         const int p0 = max(into - CK_BLOCK_COST, 0), p1 = max(end - CK_BLOCK_COST, 0);
@@ -598,13 +674,14 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
         at += used;
         into = 0;
         t0 = t1;
-        while (left > 0 && t0 >= seg_end) {   // the next segment with tokens
+        if (A.small) ++seg;
+        while (!A.small && left > 0 && t0 >= seg_end) {   // the next segment with tokens
           ++seg;
           t0 = seg_end;
           seg_end = max(seg_end, min(max(__ldg(A.seg_start + seg + 1), 0), A.n_tok));
         }
       }
-      if (pa.y > 0) {   // Q's rows on their way to L2
+      if (pa.y > 0 && k > 0) {   // the queries of the next pieces on their way to L2
         for (int c = lane; c < CK_HALF * 9; c += 32) {
           const int r = c / 9, gr = (int)rank * CK_HALF + r, tk = gr >> hs;
           if (tk < pa.y)
@@ -773,36 +850,42 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
       return 0.f;
     };
     // Q's rows, once the products of the previous piece have read theirs: copied as they are, then
-    // each thread converts what it copied.
-    auto load_q = [&]() {
+    // each thread converts what it copied. Of 256 threads, a thread's next chunk is 3 rows and
+    // 40 chunks on.
+    int qr, qc;
+    auto q_first = [&]() { qr = ct / 72, qc = ct % 72; };
+    auto q_next = [&]() {
+      qr += 3;
+      qc += 40;
+      if (qc >= 72) qc -= 72, ++qr;
+    };
+    auto q_at = [&]() { return sbase + CK_OFF_Q + (qc >> 3) * CK_QATOM + sw128_chunk(qr, qc & 7); };
+    auto copy_q = [&]() {
       if (it > 0 && !ck_wait(bar(B_SD + ((it - 1) & 1)), ((it - 1) >> 1) & 1, D.status, dead)) return false;
       const T* q = static_cast<const T*>(A.q) + (long long)tok0 * A.q_tok;
-      int r = ct / 72, ch = ct % 72;        // row and 16-byte chunk: 256 chunks on are 3 rows and 40 chunks
-      auto next = [&]() {
-        r += 3;
-        ch += 40;
-        if (ch >= 72) ch -= 72, ++r;
-      };
-#pragma unroll 3
-      for (int k = 0; k < 18; ++k, next()) {
-        const int gr = (int)rank * CK_HALF + r, tk = gr >> hs, h = gr & (H - 1);
-        const uint32_t dst = sbase + CK_OFF_Q + (ch >> 3) * CK_QATOM + sw128_chunk(r, ch & 7);
+      q_first();
+#pragma unroll 1
+      for (int k = 0; k < 18; ++k, q_next()) {
+        const int gr = (int)rank * CK_HALF + qr, tk = gr >> hs, h = gr & (H - 1);
         if (tk < n_tok) {
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(q + tk * A.q_tok + h * A.q_head + ch * 8)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(q_at()), "l"(q + tk * A.q_tok + h * A.q_head + qc * 8)
                        : "memory");
         } else {
-          sts128(dst, make_uint4(0, 0, 0, 0));
+          sts128(q_at(), make_uint4(0, 0, 0, 0));
         }
       }
+      return true;
+    };
+    auto convert_q = [&]() {
       asm volatile("cp.async.wait_all;" ::: "memory");
-      r = ct / 72, ch = ct % 72;
+      q_first();
 #pragma unroll 1
       for (int k = 0; k < 18; k += 3) {
         uint32_t dst[3];
         uint4 v[3];
 #pragma unroll
-        for (int i = 0; i < 3; ++i, next()) {
-          dst[i] = sbase + CK_OFF_Q + (ch >> 3) * CK_QATOM + sw128_chunk(r, ch & 7);
+        for (int i = 0; i < 3; ++i, q_next()) {
+          dst[i] = q_at();
           v[i] = lds128(dst[i]);
         }
 #pragma unroll
@@ -811,7 +894,6 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
           if constexpr (!__is_same(T, __half)) sts128(dst[i], f);
         }
       }
-      return true;
     };
     // K: 16-byte parts (16 codes) of this CTA's 32 rows: a warp reads 16 parts of two rows at a
     // time, 128 contiguous bytes for every 8 threads, of 8 rows in all. A part is two 16-byte
@@ -862,6 +944,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
     if (more) {
       load_k();
       load_v();
+      copy_q();   // nothing to wait for: on its way while K is converted
     }
     while (more) {
       const uint32_t st = it & 1;
@@ -892,9 +975,15 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           o[i] = h2_bits(__floats2half2_rn(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u)));
+        // bf16 magnitudes of 0x4780 = 65,536 and above, infinities and NaN carry into bit 15
+        const uint32_t m = 0x7FFF7FFFu, c = 0x38803880u;
+        bad_range |= ((((w[0] & m) + c) | ((w[1] & m) + c) | ((w[2] & m) + c) | ((w[3] & m) + c)) & 0x80008000u) != 0;
         sts128(kt + rope_at, make_uint4(o[0], o[1], o[2], o[3]));
       }
-      if (first && !load_q()) break;
+      if (first) {
+        if (it > 0 && !copy_q()) break;
+        convert_q();
+      }
       fence_proxy_async();
       __syncwarp();
       if (lane == 0) arrive_cluster(kf0 + 8 * st);
@@ -1322,7 +1411,8 @@ extern "C" hs_status hs_chunk_attention(hs_pool* p, int32_t layer, int32_t n_seg
   }
   p->settled_rows = nullptr;
   if (n == 0 || n_seg == 0) return HS_OK;
-  const ChunkArgs a = {layer, n_seg, n, pairs, d_seg_req, d_seg_start, d_limit, d_q, q_tok, q_head, sm_scale * CK_LOG2E,
+  const int small = n_seg + n / (CK_ROWS / p->cfg.n_heads) <= 32;
+  const ChunkArgs a = {layer, n_seg, n, pairs, small, d_seg_req, d_seg_start, d_limit, d_q, q_tok, q_head, sm_scale * CK_LOG2E,
                        d_out, o_tok, o_head, d_lse, d_work};
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   return dtype == HS_BF16 ? launch_chunk<__nv_bfloat16>(p, a, st) : launch_chunk<__half>(p, a, st);

@@ -49,6 +49,7 @@ class Counters(ctypes.Structure):
 
 
 BF16, FP16, FP32 = 0, 1, 2   # HS_BF16, HS_FP16, HS_FP32
+CACHE_MAX_TOKENS = 1 << 24   # HS_CACHE_MAX_TOKENS
 CHUNK_MAX_SEGMENTS = 4096    # HS_CHUNK_MAX_SEGMENTS
 CHUNK_MAX_TOKENS = 65536     # HS_CHUNK_MAX_TOKENS
 

@@ -42,6 +42,7 @@ def test_constants_match_the_header(H):
     import re
     text = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "hisparse.h")).read()
     for name, want in [("HS_BF16", H.BF16), ("HS_FP16", H.FP16), ("HS_FP32", H.FP32),
+                       ("HS_CACHE_MAX_TOKENS", H.CACHE_MAX_TOKENS),
                        ("HS_CHUNK_MAX_SEGMENTS", H.CHUNK_MAX_SEGMENTS), ("HS_CHUNK_MAX_TOKENS", H.CHUNK_MAX_TOKENS)]:
         assert int(re.search(rf"#define {name} (\d+)", text).group(1)) == want
 

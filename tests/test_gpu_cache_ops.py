@@ -376,6 +376,70 @@ def test_chunk_prompt_from_its_first_token(heads, new):
         check_chunk(c, kv, [0], [0, new], limit, q, 1 / 24, out, lse, "bf16", some)
 
 
+def test_chunk_more_blocks_than_threads():
+    """A prompt of 1,450 blocks, planned in three rounds of the CTA's threads, behind 700 single
+    tokens and with empty segments between."""
+    rng = np.random.default_rng(13)
+    with Cache(heads=64, n_layers=1, lpi=1, pages=(46, 4)) as c:
+        kv = fill(c, rng, 0, [2900, 256])
+        seg_req = [1, 1] * 700 + [0, 1]
+        start = np.r_[0, np.repeat(np.arange(1, 701), 2), 700 + 2900, 700 + 2900]
+        limit = np.r_[rng.integers(0, 257, 700), np.arange(1, 2901)]
+        q = make_q(rng, 3600, 64, "bf16")
+        out, lse = run_chunk(c, 0, seg_req, start, limit, q, 1 / 24)
+        assert c.pool.get_error() == 0
+        some = set(range(0, 700, 60)) | set(range(700, 3600, 290)) | {3599}
+        check_chunk(c, kv, seg_req, start, limit, q, 1 / 24, out, lse, "bf16", some)
+
+
+def test_chunk_most_segments_and_tokens_of_a_call():
+    """4,096 segments of 16 tokens, 65,536 tokens in all, over short contexts."""
+    rng = np.random.default_rng(14)
+    with Cache(heads=16, n_layers=1, lpi=1, pages=(2, 1)) as c:
+        kv = fill(c, rng, 0, [100, 64])
+        n, segs = 65536, 4096
+        q = make_q(rng, 64, 16, "bf16").repeat(n // 64, 1, 1)
+        limit = np.tile(np.r_[np.arange(85, 101), np.arange(49, 65)], n // 32)
+        seg_req = np.tile([0, 1], segs // 2)
+        start = np.arange(segs + 1) * 16
+        out, lse = run_chunk(c, 0, seg_req, start, limit, q, 1 / 24)
+        assert c.pool.get_error() == 0
+        few = [slice(0, 64), slice(n // 2, n // 2 + 64), slice(n - 64, n)]
+        for s in few:      # the same inputs: the same bits, wherever a pair's range was cut or not
+            o, l = out[s].float().cpu().numpy(), lse[s].cpu().numpy()
+            for j in range(0, 64, 5):
+                wo, wl, a, sz = CP.attend(q[j].float().cpu().numpy().astype(np.float64),
+                                          kv[int(seg_req[j // 16])][:limit[j]], 1 / 24)
+                assert np.all(np.abs(o[j] - wo) <= CP.out_bound(wo, a, sz, HALF_STEP["bf16"], limit[j]))
+                assert np.all(np.abs(l[j] - wl) <= CP.lse_bound(wl, sz))
+        assert torch.isfinite(out.float()).all() and torch.isfinite(lse).all()
+
+
+def test_two_calls_at_once_on_two_streams():
+    """Two pools' caches, two streams, a workspace each: the calls overlap as they like."""
+    rng = np.random.default_rng(15)
+    with Cache(heads=64, n_layers=1, lpi=1, pages=(40,), seed=1) as c, Cache(heads=16, n_layers=1, lpi=1, pages=(40,)) as d:
+        s = [torch.cuda.Stream(), torch.cuda.Stream()]
+        sides = []
+        for x in (c, d):
+            kv = fill(x, rng, 0, [2500])
+            q = make_q(rng, 40, x.heads, "bf16")
+            limit = np.arange(2461, 2501)
+            args = (i32([0]), i32([0, 40]), i32(limit))
+            sides.append((kv, q, limit, args, [torch.full((40, x.heads, 512), 0.25, dtype=torch.bfloat16, device="cuda") for _ in range(4)],
+                          [torch.full((40, x.heads), 0.25, device="cuda") for _ in range(4)]))
+        torch.cuda.synchronize()
+        for rep in range(4):
+            for x, st, (kv, q, limit, args, outs, lses) in zip((c, d), s, sides):
+                x.pool.chunk_attention(0, *args, q, 1 / 24, outs[rep], x.work, lse=lses[rep], stream=st)
+        torch.cuda.synchronize()
+        for x, (kv, q, limit, args, outs, lses) in zip((c, d), sides):
+            assert x.pool.get_error() == 0
+            check_chunk(x, kv, [0], [0, 40], limit, q, 1 / 24, outs[0], lses[0], "bf16", {0, 17, 39})
+            for o, l in zip(outs[1:], lses[1:]):
+                assert torch.equal(o, outs[0]) and torch.equal(l, lses[0])
+
+
 def test_chunk_many_single_token_segments():
     """More segments than thread-block pairs on the GPU, lengths from nothing to 700 rows."""
     rng = np.random.default_rng(12)
@@ -464,7 +528,7 @@ def test_chunk_ignores_what_no_token_sees():
         check_chunk(c, kv, [0], [0, 3], limit, q, 1 / 24, out, lse, "bf16")
 
 
-def test_chunk_values_out_of_range_are_reported_and_count_as_zero():
+def test_chunk_values_out_of_range_are_reported_and_not_seen():
     rng = np.random.default_rng(24)
     with Cache(heads=16, n_layers=1, lpi=1, pages=(4,)) as c:
         n = 200
@@ -480,31 +544,46 @@ def test_chunk_values_out_of_range_are_reported_and_count_as_zero():
         out, lse = run_chunk(c, 0, [0], [0, 4], limit, q, 1 / 24)
         assert c.pool.get_error() == RANGE
         assert torch.isfinite(out.float()).all() and torch.isfinite(lse).all()
+        rows = good.copy()
+        rows[50, 530:532] = [0x80, 0xFF]               # minus infinity at a rope value that every query
+        q1 = q.clone()                                 # has positive: its score is -inf everywhere
+        q1[:, :, 513] = 1.0
+        c.put_rows(0, 0, np.arange(n), rows)
+        out, lse = run_chunk(c, 0, [0], [0, 4], limit, q1, 1 / 24)
+        assert c.pool.get_error() == RANGE
+        kv = CP.row_values(good)
+        rest = np.r_[0:50, 51:n]                       # the row counts as not seen
+        check_chunk(c, [kv[rest]], [0], [0, 4], limit - 1, q1, 1 / 24, out, lse, "bf16")
         c.put_rows(0, 0, np.arange(n), good)
         q[2, 3, 100] = 70000.0                         # beyond fp16
         out, lse = run_chunk(c, 0, [0], [0, 4], limit, q, 1 / 24)
         assert c.pool.get_error() == RANGE
-        kv = [CP.row_values(good)]
+        assert torch.all(out[2, 3] == 0) and lse[2, 3] == float("-inf")     # that query row sees nothing
         q0 = q.clone()
         q0[2, 3, 100] = 0
         keep = [0, 1, 3]
-        check_chunk(c, kv, [0], [0, 4], limit, q0, 1 / 24, torch.where(torch.isfinite(out.float()), out, 0), lse, "bf16", set(keep))
+        check_chunk(c, [CP.row_values(good)], [0], [0, 4], limit, q0, 1 / 24, out, lse, "bf16", set(keep))
 
 
-def test_chunk_bad_ids_leave_the_other_segments_right():
+@pytest.mark.parametrize("more", [0, 60])
+def test_chunk_bad_ids_leave_the_other_segments_right(more):
+    """With `more` empty segments behind, the call is planned by the whole CTA instead of a warp."""
     rng = np.random.default_rng(25)
     with Cache(heads=16, n_layers=1, lpi=1, pages=(3, 3)) as c:
         kv = fill(c, rng, 0, [150, 150])
         q = make_q(rng, 8, 16, "bf16")
+
+        def run(seg_req, start, limit):
+            return run_chunk(c, 0, list(seg_req) + [0] * more, list(start) + [start[-1]] * more, limit, q, 1 / 24)
         for seg_req, start, limit in [([0, 9, 1], [0, 2, 5, 8], [100] * 8), ([0, -1, 1], [0, 2, 5, 8], [100] * 8),
                                       ([0, 0, 1], [0, 2, 5, 8], [100, 100, c.max_ctx + 1, -3, 1 << 30, 100, 100, 100])]:
-            out, lse = run_chunk(c, 0, seg_req, start, limit, q, 1 / 24)
+            out, lse = run(seg_req, start, limit)
             assert c.pool.get_error() == BAD_ID
             check_chunk(c, kv, [0, 0, 1], [0, 2, 5, 8], limit, q, 1 / 24, out, lse, "bf16", {0, 1, 5, 6, 7})
             assert torch.all(out[2:5] == 0) and torch.all(lse[2:5] == float("-inf"))
         # starts out of order or range: clamped, reported
         for start in ([0, 6, 3, 8], [0, 2, 5, 9], [-4, 2, 5, 8]):
-            out, lse = run_chunk(c, 0, [0, 0, 1], start, [100] * 8, q, 1 / 24)
+            out, lse = run([0, 0, 1], start, [100] * 8)
             assert c.pool.get_error() == BAD_ID
 
 
@@ -596,7 +675,7 @@ def test_refusals_launch_nothing():
                      lat=lat.data_ptr(), ldl=512, rope=rope.data_ptr(), ldr=64, keys=keys.data_ptr(), ldk=128, ks=1.0)
             a.update(kw)
             return fn(*a.values(), torch.cuda.current_stream().cuda_stream)
-        bad = [dict(pool=None), dict(layer=-1), dict(layer=2), dict(n=-1), dict(req=None), dict(pos=None), dict(dtype=3),
+        bad = [dict(pool=None), dict(layer=-1), dict(layer=2), dict(n=-1), dict(n=H.CACHE_MAX_TOKENS + 1), dict(req=None), dict(pos=None), dict(dtype=3),
                dict(dtype=-1), dict(lat=lat.data_ptr() + 2), dict(rope=rope.data_ptr() + 8), dict(keys=keys.data_ptr() + 4),
                dict(ldl=511), dict(ldl=513), dict(ldr=63), dict(ldk=127), dict(ldk=1 << 40),
                dict(lat=None, rope=None, keys=None)]
