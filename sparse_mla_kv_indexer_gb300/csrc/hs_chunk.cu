@@ -16,7 +16,7 @@
 //
 // Split of a block over a pair. The output of 128 rows is 128 x 512 fp32, all of one SM's
 // tensor memory, with no room for scores; so two CTAs form a pair (tcgen05.mma of
-// cta_group::2, M = 128): each holds 64 rows, 256 columns of tensor memory for their
+// cta_group::2, M = 128): each holds every other row, 256 columns of tensor memory for their
 // output, and supplies half of each B operand: the keys of half the page for QK, half the
 // output dims for PV. The full rate of M = 128 then needs one copy of Q (64 rows, 72 KB),
 // and shared memory holds two stages of everything else.
@@ -691,7 +691,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
       }
       if (pa.y > 0 && k > 0) {   // the queries of the next pieces on their way to L2
         for (int c = lane; c < CK_HALF * 9; c += 32) {
-          const int r = c / 9, gr = (int)rank * CK_HALF + r, tk = gr >> hs;
+          const int r = c / 9, gr = 2 * r + (int)rank, tk = gr >> hs;
           if (tk < pa.y)
             asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const T*>(A.q) + (pa.x + tk) * A.q_tok +
                                                           (gr & (H - 1)) * A.q_head + (c - r * 9) * 64));
@@ -871,7 +871,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
       q_first();
 #pragma unroll 1
       for (int k = 0; k < 18; ++k, q_next()) {
-        const int gr = (int)rank * CK_HALF + qr, tk = gr >> hs, h = gr & (H - 1);
+        const int gr = 2 * qr + (int)rank, tk = gr >> hs, h = gr & (H - 1);
         if (tk < n_tok) {
           asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(q_at()), "l"(q + tk * A.q_tok + h * A.q_head + qc * 8)
                        : "memory");
@@ -1030,7 +1030,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
     const uint32_t pf0 = mapa(bar(B_PF), 0), sr0 = mapa(bar(B_SR), 0);
     const uint32_t p_lo = sbase + CK_OFF_P + sw128_chunk(row, key0 >> 3),
                    p_hi = sbase + CK_OFF_P + sw128_chunk(row, (key0 >> 3) + 1);
-    const int gr = (int)rank * CK_HALF + row, tk = gr >> hs, h = gr & (H - 1);
+    const int gr = 2 * row + (int)rank, tk = gr >> hs, h = gr & (H - 1);
     const uint32_t red_row = sbase + CK_OFF_RED + row * 4, red_mine = red_row + (half * 2 + sub) * 256;
     auto red_at = [&](uint32_t at) { return __uint_as_float(lds32(at)); };
     uint32_t it = 0;
@@ -1053,7 +1053,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
         bool ignore = false;
         lim = clamp_limit(D, __ldg(A.limit + P.tok0() + tk), &ignore);
       }
-      if (((int)rank * CK_HALF + (quad & 1) * 32) >> hs >= P.n_tok()) {
+      if ((2 * (quad & 1) * 32 + (int)rank) >> hs >= P.n_tok()) {
         // none of these 32 rows is a token's (nor of the other three warps'): their P is 0, and
         // what the products make of it is not read
         sts128(p_lo, make_uint4(0, 0, 0, 0));
@@ -1218,7 +1218,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
           __syncwarp();
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const int r = (lane >> 1) + 16 * i, g = (int)rank * CK_HALF + (quad & 1) * 32 + r, k = g >> hs;
+            const int r = (lane >> 1) + 16 * i, g = 2 * ((quad & 1) * 32 + r) + (int)rank, k = g >> hs;
             const uint4 v = lds128(stage + r * 32 + (((lane & 1) ^ ((r >> 2) & 1)) * 16));
             if (k < P.n_tok())
               *reinterpret_cast<uint4*>(out0 + (P.tok0() + (long long)k) * A.o_tok + (g & (H - 1)) * A.o_head + c) = v;
