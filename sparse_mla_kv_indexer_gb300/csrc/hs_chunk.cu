@@ -900,28 +900,26 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
         }
       }
     };
-    // K: 16-byte parts (16 codes) of this CTA's 32 rows: a warp reads 16 parts of two rows at a
-    // time, 128 contiguous bytes for every 8 threads, of 8 rows in all. A part is two 16-byte
-    // chunks of fp16; of 8 neighbouring threads, 4 store the second chunk first, so that the 8
-    // chunks of one store lie on 8 different bank groups under the swizzle.
+    // K: 16-byte parts (16 codes) of this CTA's 32 rows: a warp has 16 parts of 8 rows, two rows at
+    // a time, and 8 neighbouring threads 4 parts of two rows, whose chunks of fp16 (a part is two)
+    // the swizzle puts on 8 different bank groups. (128 contiguous bytes per 8 threads read with a
+    // third fewer L1 wavefronts, but need the chunks of half the threads exchanged: 1 % slower.)
     // V: the 16 parts of the groups 2 rank and 2 rank + 1 of all 64 rows: the warps that have
     // them for this CTA's rows take them again, the others read the other half page's.
     const uint32_t kf0 = mapa(bar(B_KF), 0), vf0 = mapa(bar(B_VF), 0);   // the first CTA's
-    const int cw = ct >> 5, pv = lane & 15, row0 = 8 * (cw >> 1) + (lane >> 4);   // rows row0 + 2 k
+    const int cw = ct >> 5, pv = 4 * (lane >> 3) + (lane & 3), row0 = 8 * (cw >> 1) + ((lane >> 2) & 1);   // rows row0 + 2 k
     const bool own_v = (cw & 1) == (int)rank;
     const int part = 16 * (cw & 1) + pv, base_row = (int)rank * 32, rope_row = ct >> 3;
     const int row_v = (own_v ? base_row : 32 - base_row) + row0;
-    const bool flip = (pv >> 2) & 1;
-    const uint32_t k_at = (part >> 2) * CK_KATOM + sw128_chunk(row0, (pv & 3) * 2 + flip),
+    const uint32_t k_at = (part >> 2) * CK_KATOM + sw128_chunk(row0, (pv & 3) * 2),
                    rope_at = 8 * CK_KATOM + sw128_chunk(rope_row, ct & 7),
-                   v_at = (pv >> 2) * CK_VATOM + sw128_chunk(row_v, (pv & 3) * 2 + flip);
+                   v_at = (pv >> 2) * CK_VATOM + sw128_chunk(row_v, (pv & 3) * 2);
     const uint32_t src = (base_row + row0) * ROW + part * 16, src_v = row_v * ROW + (16 * (int)rank + pv) * 16,
                    src_rope = (base_row + rope_row) * ROW + (33 + (ct & 7)) * 16, src_sc = (ct & 63) * ROW + LATENT;
     const uint32_t sc_v = sbase + CK_OFF_SCL + (2 * (int)rank + (pv >> 3)) * CK_SCL_G + row_v * 4;
     const uint4 z = make_uint4(0, 0, 0, 0);
     uint4 own[4], val[4], rope = z, sc = z;
     auto ld16 = [&](uint32_t at) { return __ldg(reinterpret_cast<const uint4*>(rows + at)); };
-    auto flipped = [&](uint4 v) { return flip ? make_uint4(v.z, v.w, v.x, v.y) : v; };
     auto load_k = [&]() {
       if (n_rows == PAGE) {
 #pragma unroll
@@ -968,7 +966,6 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         uint4 lo, hi;
-        own[k] = flipped(own[k]);
         codes_to_f16(own[k], lo, hi);
         const uint32_t d = (kt + k_at + k * 256) ^ (k * 32);
         sts128(d, lo);
@@ -1007,7 +1004,6 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         uint4 lo, hi;
-        if (!own_v) val[k] = flipped(val[k]);
         codes_to_scaled_f16(val[k], v_scale(__uint_as_float(sv[k]) * sign), lo, hi);
         const uint32_t d = (vt + k * 256) ^ (k * 32);
         sts128(d, lo);
