@@ -379,7 +379,7 @@ hs_status hs_chunk_workspace(const hs_pool* pool, int64_t* bytes);
  *  dtype        of q and out: HS_BF16 or HS_FP16.
  *  d_q, d_out   element (j, h, d) at j * stride_token + h * stride_head + d; d < 576 for q,
  *               < 512 for out. 16-byte aligned, strides multiples of 8 elements (q: >= 0;
- *               out: >= 512, no two rows overlapping).
+ *               out: >= 512, no two rows overlapping; out overlaps neither q nor lse).
  *  d_lse        nullable [n_tokens, H] fp32.
  *  d_work       at least hs_chunk_workspace bytes, 16-byte aligned, used by this call
  *               alone from its start to its end: calls on one stream may share it, calls
@@ -391,9 +391,11 @@ hs_status hs_chunk_workspace(const hs_pool* pool, int64_t* bytes);
  * is bf16: exact from 2^-14 to 65504 in magnitude), softmax statistics fp32, P fp16 with 11
  * significant bits down to 2^-21 of its row's largest, v = code * scale rounded once to fp16
  * (an absolute 2^-27 below 2^-16), sums fp32. Limits: |scale| below 36.5 (latents below
- * 16,352), rope and q below 65504 in magnitude, no e4m3 NaN code, and finite. Beyond them
- * HS_ERR_RANGE is set; such a scale counts as 0, a row with another such value as not seen,
- * and a query row with one sees nothing (out 0, lse -inf). */
+ * 16,352), rope and q below 65504 in magnitude, no e4m3 NaN code, and finite; z below
+ * 2,900,000 (2^22 ln 2), and the largest z of a query row above minus that; |sm_scale| at most
+ * 1e20 (HS_ERR_INVALID otherwise). Beyond them HS_ERR_RANGE is set; such a scale counts as 0, a
+ * row with another such value, or with too large a z, as not seen, and a query row with such a
+ * value, or without a z in range, sees nothing (out 0, lse -inf). */
 hs_status hs_chunk_attention(hs_pool* pool, int32_t layer, int32_t n_segments, const int32_t* d_seg_req,
                              const int32_t* d_seg_start, int32_t n_tokens, const int32_t* d_limit, int32_t dtype,
                              const void* d_q, int64_t q_stride_token, int64_t q_stride_head, float sm_scale,

@@ -95,11 +95,14 @@ __device__ __forceinline__ float lanes_amax(float a) {
   for (int o = LANES / 2; o >= 1; o >>= 1) a = max_nan(a, __shfl_xor_sync(0xffffffffu, a, o));
   return a;
 }
-// x / scale, correctly rounded, for the many x of one scale: with r the correctly rounded
-// reciprocal and q within one unit of the quotient, q + r (x - q scale) rounds to it
-// (P. Markstein, IBM J. Res. Dev. 34(1), 1990, theorem 2), in three operations each. It
-// needs x - q scale to be exact, which holds far from the smallest normal numbers: smaller
-// amax go through the division itself.
+// x / scale for the many x of one scale: with r the correctly rounded reciprocal,
+// q + r (x - q scale) rounds to the quotient as the division does (P. Markstein, IBM J. Res.
+// Dev. 34(1), 1990, theorem 2, for q within one unit of it), in three operations each. Here q
+// = x r is within 1.5 units, so this was enumerated in exact arithmetic: amax / 448 for all
+// 2^23 significands, and all x / scale that lie beside a border of two codes (such a scale's
+// significand is a multiple of 2^18 give or take 24; 200,688 quotients). x - q scale has to
+// be exact, which holds far from the smallest normal numbers: smaller amax go through the
+// division itself.
 __device__ __forceinline__ float over(float x, float scale, float r) {
   const float q = x * r;
   return fmaf(fmaf(-q, scale, x), r, q);

@@ -42,7 +42,7 @@
 // once to fp16 (the scale in two fp16 parts); P keeps 11 bits from 2^15 down to 2^-14, that is
 // to 2^-21 of the row's largest (the shift by 2^7 buys seven binades under a dominant row).
 // Scores, maxima, sums and the output accumulate in fp32. A row with a NaN code, or rope
-// beyond fp16, scores NaN or infinity and is not seen.
+// beyond fp16, scores NaN or infinity and is not seen; nor is one whose score is beyond 2^22.
 //
 // Measured on a GB300: 753 tokens over 74,913 rows with 64 heads 8.6 ms, 0.91 PFLOP/s, 49 % of
 // the measured bf16 rate; per tile of a pair 1.48 us, against 0.73 us of its products alone
@@ -123,6 +123,10 @@ constexpr float CK_V_FACTOR = 4.f, CK_V_SHIFT = 2.f;   // V is held times this; 
 constexpr float CK_MAX_SCALE = 36.5f;      // 4 x 448 x scale < 65504
 constexpr float CK_RESCALE_LOG2 = 8.f;     // the reference maximum moves beyond this
 constexpr float CK_P_SHIFT = 7.f;          // P = 2^(z - m + 7) <= 2^15
+// Largest score in log2 units: m and 7 - m are each rounded by at most 2^-3 then, and a P of
+// 2^15 times those 2^(1/4) stays below fp16's largest. Far beyond, P would overflow.
+constexpr float CK_MAX_Z = 4194304.f;      // 2^22
+constexpr float CK_MAX_SM_SCALE = 1e20f;   // times any score of finite operands (1e12): finite
 
 // A pair's partial results: for each of its two cut blocks 128 rows of unnormalised
 // outputs and (reference in log2 units, sum); and the block that starts in its range and
@@ -226,8 +230,12 @@ __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 // Bounded wait for a phase: false after `seconds` (or when another role of this CTA gave up),
-// with HS_ERR_TIMEOUT recorded. Inlined: a call here makes its callers keep their operands
-// across it in local memory, which does not fit beside 228 KB of shared memory.
+// with HS_ERR_TIMEOUT recorded. Each lane has its own answer, and one may give up where the
+// others still see the phase end; so that none waits for it at a warp's barrier, the softmax's
+// lanes go on to a vote at their next barrier, and a converter's lane ends there and then (the
+// barriers of warp, CTA and cluster wait for threads that have not ended). Inlined: a call here
+// makes its callers keep their operands across it in local memory, which does not fit beside
+// 228 KB of shared memory.
 __device__ __forceinline__ bool ck_wait_slow(uint32_t bar, uint32_t parity, int32_t* status, uint32_t dead, int seconds) {
   const uint64_t t0 = globaltimer();
   for (uint32_t it = 1;; ++it) {
@@ -245,6 +253,11 @@ __device__ __forceinline__ bool ck_wait_slow(uint32_t bar, uint32_t parity, int3
 __device__ __forceinline__ bool ck_wait(uint32_t bar, uint32_t parity, int32_t* status, uint32_t dead, int seconds = 2) {
   if (try_wait(bar, parity)) return true;
   return ck_wait_slow(bar, parity, status, dead, seconds);
+}
+// The same for a whole warp, one answer for all of its lanes. (A vote at every wait of the
+// softmax and the converters, or a converter that goes on, costs 1.2 to 1.6 % of a long call.)
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int32_t* status, uint32_t dead, int seconds = 2) {
+  return __all_sync(0xffffffffu, ck_wait(bar, parity, status, dead, seconds));
 }
 
 // Registers of the calling warpgroup, down (freed at once) or up (waits for freed ones).
@@ -699,7 +712,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
       }
       const uint32_t slot = k % CK_RING;
       // a piece may be a whole context read over the host link: a long bound
-      if (k >= CK_RING) ok = ck_wait(bar(B_RE + slot), (k / CK_RING - 1) & 1, D.status, dead, 30);
+      if (k >= CK_RING) ok = warp_wait(bar(B_RE + slot), (k / CK_RING - 1) & 1, D.status, dead, 30);
       if (!ok) break;
       if (lane == 0) {
         const uint32_t dst = sbase + CK_OFF_RING + slot * CK_PIECE_BYTES;
@@ -727,7 +740,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
             }
           }
         }
-        if (t >= CK_TILES) ok = ck_wait(bar(B_TE + ts), (t / CK_TILES - 1) & 1, D.status, dead, 30);
+        if (t >= CK_TILES) ok = warp_wait(bar(B_TE + ts), (t / CK_TILES - 1) & 1, D.status, dead, 30);
         if (!ok) break;
         if (lane == 0) {
           const uint64_t at = reinterpret_cast<uint64_t>(rows);
@@ -755,7 +768,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
       bool ok = true;
       for (uint32_t k = 0; ok; ++k) {
         const uint32_t slot = k % CK_RING;
-        ok = __all_sync(0xffffffffu, ck_wait(bar(B_RF + slot), (k / CK_RING) & 1, D.status, dead, 30));
+        ok = warp_wait(bar(B_RF + slot), (k / CK_RING) & 1, D.status, dead, 30);
         if (!ok) break;
         const Piece p = piece_at(slot);
         const int n_tok = __shfl_sync(0xffffffffu, p.n_tok(), 0), n = __shfl_sync(0xffffffffu, p.pg1() - p.pg0(), 0);
@@ -765,8 +778,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
         for (int i = 0; i <= n; ++i) {
           if (i < n) {
             const uint32_t t = it + i, st = t & 1;
-            ok = ck_wait(bar(B_KF + st), (t >> 1) & 1, D.status, dead);
-            ok = __all_sync(0xffffffffu, ok);
+            ok = warp_wait(bar(B_KF + st), (t >> 1) & 1, D.status, dead);
             if (!ok) break;
             tc_fence_after();
             asm volatile("" : "+r"(qd), "+r"(kd));   // the 36 descriptors are added up here, not kept in registers
@@ -786,7 +798,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
             }
             __syncwarp();
             // the other two take accumulators of the tile before, once its scores have been read
-            if (t > 0) ok = __all_sync(0xffffffffu, ck_wait(bar(B_SR), (t - 1) & 1, D.status, dead));
+            if (t > 0) ok = warp_wait(bar(B_SR), (t - 1) & 1, D.status, dead);
             if (!ok) break;
             tc_fence_after();
             if (elect_lane()) {
@@ -798,9 +810,8 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
           }
           if (i > 0) {
             const uint32_t t = it + i - 1, st = t & 1;
-            ok = ck_wait(bar(B_VF + st), (t >> 1) & 1, D.status, dead) &&
-                 ck_wait(bar(B_PF + st), (t >> 1) & 1, D.status, dead);
-            ok = __all_sync(0xffffffffu, ok);
+            ok = warp_wait(bar(B_VF + st), (t >> 1) & 1, D.status, dead) &&
+                 warp_wait(bar(B_PF + st), (t >> 1) & 1, D.status, dead);
             if (!ok) break;
             tc_fence_after();
             asm volatile("" : "+r"(pd), "+r"(vd));
@@ -834,7 +845,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
     bool more = true, first = true;         // first: it begins a piece
     auto advance = [&](uint32_t t) {
       const uint32_t ts = t % CK_TILES, at = sbase + CK_OFF_TILES + ts * CK_PIECE_BYTES;
-      more = __all_sync(0xffffffffu, ck_wait(bar(B_TF + ts), (t / CK_TILES) & 1, D.status, dead, 30));
+      more = warp_wait(bar(B_TF + ts), (t / CK_TILES) & 1, D.status, dead, 30);
       if (!more) return;
       const uint4 x = lds128(at);
       rows = reinterpret_cast<const uint8_t*>((uint64_t)x.x | (uint64_t)x.y << 32);
@@ -951,7 +962,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
     }
     while (more) {
       const uint32_t st = it & 1;
-      if (it >= 2 && !ck_wait(bar(B_SD + st), ((it - 2) >> 1) & 1, D.status, dead)) break;
+      if (it >= 2 && !ck_wait(bar(B_SD + st), ((it - 2) >> 1) & 1, D.status, dead)) return;
       if (ct < PAGE) {
         const uint32_t x = sbase + CK_OFF_SCL + (it % CK_SCL) * CK_SCL_T + ct * 4;
         sts32(x, __float_as_uint(good_scale(__uint_as_float(sc.x))));
@@ -983,7 +994,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
         sts128(kt + rope_at, make_uint4(o[0], o[1], o[2], o[3]));
       }
       if (first) {
-        if (it > 0 && !copy_q()) break;
+        if (it > 0 && !copy_q()) return;
         convert_q();
       }
       fence_proxy_async();
@@ -995,8 +1006,8 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
       }
       advance(it + 1);
       if (more) load_k();
-      if (it >= 2 && !ck_wait(bar(B_PD + st), ((it - 2) >> 1) & 1, D.status, dead)) break;
-      if (!ck_wait(bar(B_SC + it % CK_SCL), (it / CK_SCL) & 1, D.status, dead)) break;
+      if (it >= 2 && !ck_wait(bar(B_PD + st), ((it - 2) >> 1) & 1, D.status, dead)) return;
+      if (!ck_wait(bar(B_SC + it % CK_SCL), (it / CK_SCL) & 1, D.status, dead)) return;
       const uint32_t vt = sbase + CK_OFF_V + st * CK_VSTAGE + v_at, scv = sc_v + (it % CK_SCL) * CK_SCL_T;
       uint32_t sv[4];
 #pragma unroll
@@ -1119,12 +1130,12 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
         float mt = max_nan(s[0], s[1]);
 #pragma unroll
         for (int j = 2; j < 16; j += 2) mt = max3_nan(mt, s[j], s[j + 1]);
-        if (!(mt < INFINITY)) {   // a row with a value that is not finite (or a query beyond fp16): not seen
+        if (!(mt * scale < CK_MAX_Z)) {   // a value that is not finite (or a query beyond fp16), or too large a score: not seen
           bad_range = true;
           mt = -INFINITY;
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
-            if (!(s[j] < INFINITY)) s[j] = -INFINITY;
+            if (!(s[j] * scale < CK_MAX_Z)) s[j] = -INFINITY;
             mt = fmaxf(mt, s[j]);
           }
         }
@@ -1139,9 +1150,12 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
         float f = 1.f;
         if (mt > m + CK_RESCALE_LOG2) {   // also the first finite maximum, when m is -inf
           if (m > -INFINITY) f = ex2_approx(m - mt);
-          m = mt;
+          if (mt > -CK_MAX_Z)
+            m = mt;
+          else
+            bad_range = true;   // its weights are 0, as those of other rows next to a score in range
         }
-        const float off = m > -INFINITY ? CK_P_SHIFT - m : 0.f;   // no finite score yet: every s is -inf
+        const float off = m > -INFINITY ? CK_P_SHIFT - m : 0.f;   // no finite score yet: every weight is 0
         F2 ls2 = f2(0.f);
         uint32_t ph[8];
 #pragma unroll
@@ -1405,7 +1419,7 @@ extern "C" hs_status hs_chunk_attention(hs_pool* p, int32_t layer, int32_t n_seg
   if (n > 0 && n_seg > 0) {
     const auto aligned = [](const void* x) { return x && (reinterpret_cast<uintptr_t>(x) & 15) == 0; };
     if (!d_seg_req || !d_seg_start || !d_limit || !aligned(d_q) || !aligned(d_out) || !aligned(d_work) ||
-        work_bytes < work_bytes_for(pairs) || !(fabsf(sm_scale) <= 2.0e38f))
+        work_bytes < work_bytes_for(pairs) || !(fabsf(sm_scale) <= CK_MAX_SM_SCALE))
       return HS_ERR_INVALID;
     if (!stride_ok(q_tok, 0) || !stride_ok(q_head, 0) || !stride_ok(o_tok, LATENT) || !stride_ok(o_head, LATENT))
       return HS_ERR_INVALID;

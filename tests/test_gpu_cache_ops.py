@@ -565,6 +565,41 @@ def test_chunk_values_out_of_range_are_reported_and_not_seen():
         check_chunk(c, [CP.row_values(good)], [0], [0, 4], limit, q0, 1 / 24, out, lse, "bf16", set(keep))
 
 
+@pytest.mark.parametrize("sm_scale", [1.0, -1.0, 64.0])
+def test_chunk_scores_too_large_are_reported_and_not_seen(sm_scale):
+    """A row whose scores are 2.5e8 or more for one query and minus that for another: the first
+    does not see it, for the second its weight is 0 by the formula; a query that has no score
+    in range sees nothing."""
+    rng = np.random.default_rng(26)
+    with Cache(heads=16, n_layers=1, lpi=1, pages=(4,)) as c:
+        n = 200
+        x = np.zeros((n, 576))
+        x[:, 1:512] = rng.standard_normal((n, 511)) / 32
+        rows = CP.pack_rows(x[:, :512], x[:, 512:])
+        rows[70:71] = CP.pack_rows(np.where(np.arange(512) == 0, 4096.0, x[70:71, :512]), x[70:71, 512:])
+        c.put_rows(0, 0, np.arange(n), rows)
+        q = torch.zeros(4, 16, 576, dtype=torch.bfloat16, device="cuda")
+        q[:, :, 1:] = make_q(rng, 4, 16, "bf16")[:, :, 1:] / abs(sm_scale)
+        limit = np.array([200, 200, 71, 70])
+        sign = 1.0 if sm_scale > 0 else -1.0
+        q[0, :, 0] = 60000.0 * sign                    # z = 2.5e8 |sm_scale|
+        q[1, :, 0] = -60000.0 * sign
+        out, lse = run_chunk(c, 0, [0], [0, 4], limit, q, sm_scale)
+        assert c.pool.get_error() == RANGE             # token 0's
+        without = CP.row_values(rows)[np.r_[0:70, 71:n]]
+        check_chunk(c, [without], [0], [0, 4], np.array([199, 199, 70, 70]), q, sm_scale, out, lse, "bf16", {0, 1, 3})
+        check_chunk(c, [CP.row_values(rows)], [0], [0, 4], limit, q, sm_scale, out, lse, "bf16", {1, 2, 3})
+        out, lse = run_chunk(c, 0, [0], [0, 3], limit[1:], q[1:], sm_scale)
+        assert c.pool.get_error() == 0                 # a low score beside others is no error
+        c.put_rows(0, 0, np.arange(n), np.repeat(rows[70:71], n, axis=0))
+        out, lse = run_chunk(c, 0, [0], [0, 2], limit[:2], q[:2], sm_scale)
+        assert c.pool.get_error() == RANGE
+        assert torch.all(out == 0) and torch.all(torch.isneginf(lse))
+        out, lse = run_chunk(c, 0, [0], [0, 1], limit[1:2], q[1:2], sm_scale)
+        assert c.pool.get_error() == RANGE             # none in range from below
+        assert torch.all(out == 0) and torch.all(torch.isneginf(lse))
+
+
 @pytest.mark.parametrize("more", [0, 60])
 def test_chunk_bad_ids_leave_the_other_segments_right(more):
     """With `more` empty segments behind, the call is planned by the whole CTA instead of a warp."""
@@ -701,7 +736,7 @@ def test_refusals_launch_nothing():
                    dict(lim=None), dict(q=None), dict(q=q.data_ptr() + 2), dict(out=None), dict(out=out.data_ptr() + 8),
                    dict(work=None), dict(work=c.work.data_ptr() + 4), dict(wb=c.pool.chunk_workspace_bytes() - 1),
                    dict(qt=-8), dict(qt=4), dict(qh=577), dict(ot=511), dict(ot=0), dict(oh=516), dict(oh=0),
-                   dict(sm=float("nan")), dict(sm=float("inf"))]:
+                   dict(sm=float("nan")), dict(sm=float("inf")), dict(sm=-1.01e20)]:
             assert chunk_call(**kw) == INVALID, kw
         assert chunk_call(n=0) == 0 and chunk_call(n_seg=0) == 0
         b = ctypes.c_int64(0)
