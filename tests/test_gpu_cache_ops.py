@@ -269,6 +269,80 @@ def test_append_then_read_round_trip_and_a_fork_between_requests():
         assert np.array_equal(CP.row_values(a), CP.row_values(b))
 
 
+@pytest.mark.parametrize("n", [9729, 20011, 170001])
+def test_a_large_call_equals_its_pieces(n):
+    """Warps that take runs of several tokens, up to the longest run, the last one cut short:
+    padding and positions given twice at odd places, two thirds of the padding in one stretch."""
+    rng = np.random.default_rng(n)
+    pages = -(-n // 64) + 1
+    with Cache(n_layers=1, lpi=1, pages=(pages, pages)) as c:
+        lat, _ = values(rng, n, 512, "bf16")
+        rope, _ = values(rng, n, 64, "bf16")
+        keys, _ = values(rng, n, 128, "bf16")
+        pos = rng.permutation(pages * 64)[:n]
+        twice = rng.choice(np.arange(1, n), n // 20, replace=False)
+        twice = np.r_[twice, [31, 32, 33, 64, n - 1]]
+        for j in np.sort(twice):
+            pos[j] = pos[j - 1]
+        req = np.zeros(n, np.int32)
+        req[rng.choice(n, n // 50, replace=False)] = -1
+        req[n // 3:n // 3 + n // 25] = -1
+        live = np.flatnonzero(req >= 0)                # a position again behind padding is not adjacent: not allowed
+        again = np.flatnonzero((pos[live[1:]] == pos[live[:-1]]) & (np.diff(live) > 1)) + 1
+        req[live[again]] = -1
+        c.pool.append_quantized(0, i32(req), i32(pos), lat, rope, keys)
+        cut = [0]
+        while cut[-1] < n:                              # never between the two of one position
+            e = min(cut[-1] + 4000, n)
+            while e < n and pos[e] == pos[e - 1]:
+                e += 1
+            cut.append(e)
+        for a, b in zip(cut, cut[1:]):
+            c.pool.append_quantized(0, i32(np.where(req[a:b] < 0, -1, 1)), i32(pos[a:b]), lat[a:b], rope[a:b], keys[a:b])
+        assert c.pool.get_error() == 0
+        every = np.arange(pages * 64)
+        assert np.array_equal(c.get_rows(0, 0, every), c.get_rows(0, 1, every))
+        for a, b in zip(c.get_keys(0, 0, every), c.get_keys(0, 1, every)):
+            assert np.array_equal(a.view(np.uint8), b.view(np.uint8))
+        got, want = (torch.full((n, 704), 5.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        c.pool.read_rows(0, i32(req), i32(pos), got[:, :512], got[:, 512:576], got[:, 576:])
+        for a in range(0, n, 4000):
+            w = want[a:a + 4000]
+            c.pool.read_rows(0, i32(req[a:a + 4000]), i32(pos[a:a + 4000]), w[:, :512], w[:, 512:576], w[:, 576:])
+        assert c.pool.get_error() == 0
+        assert torch.equal(got, want) and not torch.isnan(got.float()).any()
+
+
+def test_the_most_tokens_of_a_call():
+    """Values whose offsets pass 2^31 elements."""
+    rng = np.random.default_rng(11)
+    with Cache(n_layers=1, lpi=1, pages=(8,)) as c:
+        n, H = c.H.CACHE_MAX_TOKENS, c.H
+        some, _ = values(rng, 500, 128, "fp16")
+        keys = torch.zeros(n, 128, dtype=torch.float16, device="cuda")
+        at = torch.from_numpy(np.sort(rng.choice(n - 1, 499, replace=False))).cuda()
+        at = torch.cat([at, torch.tensor([n - 1], device="cuda")])
+        req, pos = torch.full((n,), -1, dtype=torch.int32, device="cuda"), torch.zeros(n, dtype=torch.int32, device="cuda")
+        req[at], pos[at], keys[at] = 0, torch.arange(500, dtype=torch.int32, device="cuda"), some
+        c.pool.append_quantized(0, req, pos, keys=keys)
+        assert c.pool.get_error() == 0
+        codes, scales = c.get_keys(0, 0, np.arange(500))
+        wc, ws = CP.quantise(some.float().cpu().numpy())
+        assert np.array_equal(codes, wc) and np.array_equal(scales, ws[:, 0])
+        table = torch.empty(500, 128, dtype=torch.float16, device="cuda")
+        every = i32(np.arange(500))
+        c.pool.read_rows(0, i32(np.zeros(500)), every, keys=table)
+        pos = torch.randint(0, 500, (n,), dtype=torch.int32, device="cuda")
+        keys.fill_(9.0)
+        c.pool.read_rows(0, torch.zeros_like(pos), pos, keys=keys)
+        assert c.pool.get_error() == 0
+        for a in range(0, n, 1 << 21):
+            assert torch.equal(keys[a:a + (1 << 21)], table[pos[a:a + (1 << 21)].long()]), a
+        with pytest.raises(H.HisparseError):
+            more = torch.zeros(n + 1, dtype=torch.int32, device="cuda")
+            c.pool.read_rows(0, more, more, keys=torch.empty(n + 1, 128, dtype=torch.float16, device="cuda"))
+
+
 # ---- chunk attention ---------------------------------------------------------------
 
 
@@ -489,6 +563,24 @@ def test_chunk_dominant_row_and_a_long_faint_tail():
         out, lse = run_chunk(c, 0, [0], [0, 3], limit, q, 1.0)
         assert c.pool.get_error() == 0
         check_chunk(c, kv, [0], [0, 3], limit, q, 1.0, out, lse, "bf16")
+
+
+@pytest.mark.parametrize("heads", [16, 64])
+def test_chunk_up_to_the_longest_context(heads):
+    """Limits of max_ctx itself, for one token and for many; one more is refused by the kernel."""
+    rng = np.random.default_rng(30)
+    with Cache(heads=heads, n_layers=1, lpi=1, pages=(4, 4), max_ctx=256) as c:
+        kv = fill(c, rng, 0, [256, 256])
+        q = make_q(rng, 21, heads, "bf16")
+        limit = np.r_[np.full(20, 256), 256]
+        out, lse = run_chunk(c, 0, [0, 1], [0, 20, 21], limit, q, 1 / 24)
+        assert c.pool.get_error() == 0
+        check_chunk(c, kv, [0, 1], [0, 20, 21], limit, q, 1 / 24, out, lse, "bf16")
+        limit[3] = 257
+        out, lse = run_chunk(c, 0, [0, 1], [0, 20, 21], limit, q, 1 / 24)
+        assert c.pool.get_error() == BAD_ID
+        assert torch.all(out[3] == 0) and torch.all(torch.isneginf(lse[3]))
+        check_chunk(c, kv, [0, 1], [0, 20, 21], limit, q, 1 / 24, out, lse, "bf16", set(range(21)) - {3})
 
 
 def test_chunk_strides_and_no_lse():
