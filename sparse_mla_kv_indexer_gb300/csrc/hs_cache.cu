@@ -10,16 +10,19 @@
 // unrounded arithmetic only where x / scale lies within 2^-23 of a rounding border.
 //
 // A warp has a run of up to 32 tokens, whose places (request -> page -> row, a chain of three
-// loads) its lanes look up side by side; then it takes CA_APPEND or CA_READ tokens at a time,
-// all of their loads in flight. Lane l holds latent values 256 j + 8 l .. + 7 (j = 0, 1), so
+// loads) its lanes look up side by side. Then it appends token by token, the next one's values on
+// their way, or reads CA_READ tokens at a time, all of their loads in flight. The runs are dealt
+// so that all warps are resident at once. Lane l holds latent values 256 j + 8 l .. + 7 (j = 0, 1), so
 // that every load and store of a warp is one contiguous run, and the 16 lanes of a half warp
 // hold exactly one 128-value group.
 //
-// Measured on a GB300 (163 MB moved for 74,160 tokens of bf16, 24.5 us at the copy rate): append
-// 35.7 us, read back 34.2 us, against 46 and 37 us when every token's places are looked up by the
-// warp that takes it, one chain after another. Two tokens at a time when appending take 46 us
-// (the arithmetic of one already fills the issue slots), three and four when reading 46 and
-// 43 us; 16, 64 and 128 warps per SM 50, 37 and 39 us (append), 45, 35 and 37 us (read).
+// Measured on a GB300 (163 MB moved for 74,160 tokens of bf16, 24.5 us at the copy rate, 25.2 us
+// for a plain elementwise pass over as many bytes): append 33.4 us, read back 30.9 us, against 46
+// and 37 us when every token's places are looked up by the warp that takes it, one chain after
+// another. The append is bound by its instructions (0.6 a cycle and scheduler), the read by the
+// latency between a warp's loads; one token at a time with the next one on its way reads in 34.6
+// us, three or four at a time in 43 us and more. 28, 36, 48 and 64 warps per SM append in 41 (two
+// tokens more per warp), 39, 39 and 39 us (two waves).
 #include <cuda_fp8.h>
 #include <float.h>
 #include <math.h>
@@ -32,30 +35,38 @@ namespace hs {
 namespace {
 
 constexpr int CA_WARPS = 4;          // warps per CTA
-constexpr int CA_APPEND = 1, CA_READ = 2;   // tokens of a warp at a time
+constexpr int CA_READ = 2;           // tokens of a warp at a time when reading
 constexpr int CA_SM_WARPS = 32;      // warps per SM among which the tokens are dealt, up to 32 each
 constexpr float E4M3_MAX = 448.f;
 constexpr float MIN_SCALE = 1.17549435e-38f;   // the smallest normal fp32: x / scale stays finite and below 448
 constexpr float BF16_MAX = 3.38953139e38f;
 
-// N consecutive values of type T (16-byte or smaller aligned accesses) as fp32, and back.
+// N consecutive values of type T (16-byte or smaller aligned accesses) as they are stored, as
+// fp32, and back.
 template <typename T, int N>
-__device__ __forceinline__ void load_f32(const T* p, float (&v)[N]) {
-  constexpr int BYTES = N * (int)sizeof(T);
+struct Raw {
   union {
-    uint4 q[BYTES >= 16 ? BYTES / 16 : 1];
-    uint2 d[BYTES >= 8 ? BYTES / 8 : 1];
-    uint32_t w[BYTES / 4];
+    uint4 q[N * (int)sizeof(T) >= 16 ? N * (int)sizeof(T) / 16 : 1];
+    uint2 d;
+    uint32_t w;
     T t[N];
-  } u;
+  };
+  __device__ Raw() {}
+};
+template <typename T, int N>
+__device__ __forceinline__ void load_raw(const T* p, Raw<T, N>& u) {
+  constexpr int BYTES = N * (int)sizeof(T);
   if constexpr (BYTES >= 16) {
 #pragma unroll
     for (int i = 0; i < BYTES / 16; ++i) u.q[i] = reinterpret_cast<const uint4*>(p)[i];
   } else if constexpr (BYTES == 8) {
-    u.d[0] = *reinterpret_cast<const uint2*>(p);
+    u.d = *reinterpret_cast<const uint2*>(p);
   } else {
-    u.w[0] = *reinterpret_cast<const uint32_t*>(p);
+    u.w = *reinterpret_cast<const uint32_t*>(p);
   }
+}
+template <typename T, int N>
+__device__ __forceinline__ void raw_f32(const Raw<T, N>& u, float (&v)[N]) {
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = to_f32(u.t[i]);
 }
@@ -192,7 +203,7 @@ __device__ __forceinline__ P* shfl_ptr(P* p, int lane) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(CA_WARPS * 32)
+__global__ void __launch_bounds__(CA_WARPS * 32, CA_SM_WARPS / CA_WARPS)
 append_quantized_kernel(const Dev D, int layer, int group, int n, int per_warp, const int32_t* __restrict__ req_of,
                         const int32_t* __restrict__ pos_of, const T* __restrict__ latent, long long ld_latent,
                         const T* __restrict__ rope, long long ld_rope, const T* __restrict__ keys, long long ld_keys,
@@ -218,65 +229,85 @@ append_quantized_kernel(const Dev D, int layer, int group, int n, int per_warp, 
       if ((latent && !row_mine) || (keys && !page_mine)) set_status(D.status, HS_ERR_BAD_ID);
     }
   }
-  for (int k0 = 0; k0 < count; k0 += CA_APPEND) {
-    float v[CA_APPEND][2][8], rp[CA_APPEND][2], kv[CA_APPEND][4];
+  struct In {
+    Raw<T, 8> v[2];
+    Raw<T, 2> rope;
+    Raw<T, 4> key;
+  } in[2];
+  auto fetch = [&](int k, In& x) {
+    if (k >= count) return;
+    const long long t = base + k;
+    if (latent) {
 #pragma unroll
-    for (int u = 0; u < CA_APPEND; ++u) {
-      const long long t = min(base + k0 + u, n - 1);
-      if (latent) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) load_f32<T, 8>(latent + t * ld_latent + j * 256 + lane * 8, v[u][j]);
-        load_f32<T, 2>(rope + t * ld_rope + lane * 2, rp[u]);
-      }
-      if (keys) load_f32<T, 4>(keys + t * ld_keys + lane * 4, kv[u]);
+      for (int j = 0; j < 2; ++j) load_raw<T, 8>(latent + t * ld_latent + j * 256 + lane * 8, x.v[j]);
+      load_raw<T, 2>(rope + t * ld_rope + lane * 2, x.rope);
     }
+    if (keys) load_raw<T, 4>(keys + t * ld_keys + lane * 4, x.key);
+  };
+  auto put = [&](int k, const In& x) {
+    if (k >= count) return;
+    uint8_t* const row = shfl_ptr(row_mine, k);
+    uint8_t* const page = shfl_ptr(page_mine, k);
+    const int off = __shfl_sync(0xffffffffu, off_mine, k);
+    if (row) {
+      float sc[2];
 #pragma unroll
-    for (int u = 0; u < CA_APPEND; ++u) {
-      const int from = (k0 + u) & 31;
-      uint8_t* const row = shfl_ptr(row_mine, from);
-      uint8_t* const page = shfl_ptr(page_mine, from);
-      const int off = __shfl_sync(0xffffffffu, off_mine, from);
-      if (k0 + u >= count) break;
-      if (row) {
-        float sc[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          uint32_t code[2];
-          sc[j] = quantise<8, 16>(v[u][j], code, &bad);
-          *reinterpret_cast<uint2*>(row + j * 256 + lane * 8) = make_uint2(code[0], code[1]);
-        }
-        const float s1 = __shfl_sync(0xffffffffu, sc[0], 16), s3 = __shfl_sync(0xffffffffu, sc[1], 16);
-        if (lane == 0) *reinterpret_cast<float4*>(row + LATENT) = make_float4(sc[0], s1, sc[1], s3);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float x = fminf(fmaxf(rp[u][i], -BF16_MAX), BF16_MAX);
-          bad |= !(fabsf(rp[u][i]) <= FLT_MAX);
-          rp[u][i] = rp[u][i] != rp[u][i] ? 0.f : x;
-        }
-        store_f32<__nv_bfloat16, 2>(reinterpret_cast<__nv_bfloat16*>(row + LATENT + 16) + lane * 2, rp[u]);
+      for (int j = 0; j < 2; ++j) {
+        float v[8];
+        raw_f32(x.v[j], v);
+        uint32_t code[2];
+        sc[j] = quantise<8, 16>(v, code, &bad);
+        *reinterpret_cast<uint2*>(row + j * 256 + lane * 8) = make_uint2(code[0], code[1]);
       }
-      if (page) {
-        uint32_t w[1] = {0};
-        if (D.idx_fmt == HS_IDX_FP8) {
-          const float scale = quantise<4, 32>(kv[u], w, &bad);
-          if (lane == 0) *reinterpret_cast<float*>(page + PAGE * IDX_DIM + off * 4) = scale;
-        } else {
+      const float s1 = __shfl_sync(0xffffffffu, sc[0], 16), s3 = __shfl_sync(0xffffffffu, sc[1], 16);
+      if (lane == 0) *reinterpret_cast<float4*>(row + LATENT) = make_float4(sc[0], s1, sc[1], s3);
+      float rp[2];
+      raw_f32(x.rope, rp);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            bad |= !(fabsf(kv[u][i]) <= FLT_MAX);
-            const float q = kv[u][i] != kv[u][i] ? 0.f : fminf(fmaxf(rintf(__fdiv_rn(kv[u][i], key_scale)), -127.f), 127.f);
-            w[0] |= ((uint32_t)(int)q & 0xFFu) << (8 * i);
-          }
-        }
-        *(reinterpret_cast<uint32_t*>(page + off * IDX_DIM) + lane) = w[0];
+      for (int i = 0; i < 2; ++i) {
+        const float r = fminf(fmaxf(rp[i], -BF16_MAX), BF16_MAX);
+        bad |= !(fabsf(rp[i]) <= FLT_MAX);
+        rp[i] = rp[i] != rp[i] ? 0.f : r;
       }
+      store_f32<__nv_bfloat16, 2>(reinterpret_cast<__nv_bfloat16*>(row + LATENT + 16) + lane * 2, rp);
+    }
+    if (page) {
+      float kv[4];
+      raw_f32(x.key, kv);
+      uint32_t w[1] = {0};
+      if (D.idx_fmt == HS_IDX_FP8) {
+        const float scale = quantise<4, 32>(kv, w, &bad);
+        if (lane == 0) *reinterpret_cast<float*>(page + PAGE * IDX_DIM + off * 4) = scale;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          bad |= !(fabsf(kv[i]) <= FLT_MAX);
+          const float q = kv[i] != kv[i] ? 0.f : fminf(fmaxf(rintf(__fdiv_rn(kv[i], key_scale)), -127.f), 127.f);
+          w[0] |= ((uint32_t)(int)q & 0xFFu) << (8 * i);
+        }
+      }
+      *(reinterpret_cast<uint32_t*>(page + off * IDX_DIM) + lane) = w[0];
+    }
+  };
+  if constexpr (sizeof(T) == 2) {   // the next token's values on their way while one is quantised
+    fetch(0, in[0]);
+    for (int k = 0; k < count; k += 2) {
+      fetch(k + 1, in[1]);
+      put(k, in[0]);
+      fetch(k + 2, in[0]);
+      put(k + 1, in[1]);
+    }
+  } else {   // twice the registers: they would spill
+    for (int k = 0; k < count; ++k) {
+      fetch(k, in[0]);
+      put(k, in[0]);
     }
   }
   if (bad) set_status(D.status, HS_ERR_RANGE);
 }
 
 template <typename T>
-__global__ void __launch_bounds__(CA_WARPS * 32)
+__global__ void __launch_bounds__(CA_WARPS * 32, CA_SM_WARPS / CA_WARPS)
 read_rows_kernel(const Dev D, int layer, int group, int n, int per_warp, const int32_t* __restrict__ req_of,
                  const int32_t* __restrict__ pos_of, T* __restrict__ latent, long long ld_latent, T* __restrict__ rope,
                  long long ld_rope, T* __restrict__ keys, long long ld_keys, float key_scale) {
@@ -310,8 +341,8 @@ read_rows_kernel(const Dev D, int layer, int group, int n, int per_warp, const i
     const uint8_t *row[CA_READ], *page[CA_READ];
     uint2 w[CA_READ][2];
     float4 s4[CA_READ];
-    float rv[CA_READ][2], ks[CA_READ];
-    uint32_t kw[CA_READ];
+    float ks[CA_READ];
+    uint32_t rw[CA_READ], kw[CA_READ];
 #pragma unroll
     for (int u = 0; u < CA_READ; ++u) {
       const int from = (k0 + u) & 31;
@@ -325,7 +356,7 @@ read_rows_kernel(const Dev D, int layer, int group, int n, int per_warp, const i
 #pragma unroll
           for (int j = 0; j < 2; ++j) w[u][j] = *reinterpret_cast<const uint2*>(row[u] + j * 256 + lane * 8);
         }
-        if (rope) load_f32<__nv_bfloat16, 2>(reinterpret_cast<const __nv_bfloat16*>(row[u] + LATENT + 16) + lane * 2, rv[u]);
+        if (rope) rw[u] = *(reinterpret_cast<const uint32_t*>(row[u] + LATENT + 16) + lane);
       }
       if (page[u]) {
         kw[u] = *(reinterpret_cast<const uint32_t*>(page[u] + off * IDX_DIM) + lane);
@@ -346,7 +377,10 @@ read_rows_kernel(const Dev D, int layer, int group, int n, int per_warp, const i
             store_f32<T, 8>(latent + t * ld_latent + j * 256 + lane * 8, v);
           }
         }
-        if (rope) store_f32<T, 2>(rope + t * ld_rope + lane * 2, rv[u]);
+        if (rope) {
+          const float v[2] = {__uint_as_float(rw[u] << 16), __uint_as_float(rw[u] & 0xFFFF0000u)};
+          store_f32<T, 2>(rope + t * ld_rope + lane * 2, v);
+        }
       }
       if (page[u]) {
         float v[4];
@@ -408,7 +442,7 @@ template <typename T>
 hs_status launch_append_quantized(hs_pool* p, int layer, int n, const int32_t* d_req, const int32_t* d_pos,
                                   const void* d_latent, int64_t ld_latent, const void* d_rope, int64_t ld_rope,
                                   const void* d_keys, int64_t ld_keys, float key_scale, cudaStream_t st) {
-  const int per = tokens_per_warp(n, CA_APPEND);
+  const int per = tokens_per_warp(n, 1);
   return launch_pdl(append_quantized_kernel<T>, dim3(cache_grid(n, per)), dim3(CA_WARPS * 32), 0, st, 0,
                     p->d, layer, layer / p->d.lpi, n, per, d_req, d_pos, static_cast<const T*>(d_latent), (long long)ld_latent,
                     static_cast<const T*>(d_rope), (long long)ld_rope, static_cast<const T*>(d_keys),
