@@ -997,6 +997,9 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
         if (it > 0 && !copy_q()) return;
         convert_q();
       }
+      // the stores complete behind the wait for the next tile's place, and V's behind the next loads:
+      // the fences then wait 200 cycles less each (3 % of a long call)
+      advance(it + 1);
       fence_proxy_async();
       __syncwarp();
       if (lane == 0) arrive_cluster(kf0 + 8 * st);
@@ -1004,7 +1007,6 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
 #pragma unroll
         for (int k = 0; k < 4; ++k) val[k] = own[k];
       }
-      advance(it + 1);
       if (more) load_k();
       if (it >= 2 && !ck_wait(bar(B_PD + st), ((it - 2) >> 1) & 1, D.status, dead)) return;
       if (!ck_wait(bar(B_SC + it % CK_SCL), (it / CK_SCL) & 1, D.status, dead)) return;
@@ -1020,11 +1022,11 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
         sts128(d, lo);
         sts128(d ^ 16, hi);
       }
+      if (more) load_v();
       fence_proxy_async();
       __syncwarp();
       if (lane == 0) arrive_cluster(vf0 + 8 * st);
       ++it;
-      if (more) load_v();
     }
     if (bad_range) set_status(D.status, HS_ERR_RANGE);
   } else {
