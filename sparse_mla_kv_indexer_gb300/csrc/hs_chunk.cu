@@ -102,7 +102,8 @@ constexpr int CK_PIECE_BYTES = 32;
 constexpr int CK_OFF_TILES = CK_OFF_RING + CK_RING * CK_PIECE_BYTES;   // Tile [CK_TILES]
 constexpr int CK_OFF_BAR = CK_OFF_TILES + CK_TILES * CK_PIECE_BYTES;
 enum Bar { B_KF = 0, B_VF = 2, B_PF = 4, B_SD = 6, B_PD = 8, B_SR = 10, B_FIN = 11, B_RF = 12, B_RE = 12 + CK_RING,
-           B_TF = 12 + 2 * CK_RING, B_TE = B_TF + CK_TILES, B_SC = B_TE + CK_TILES, B_N = B_SC + CK_SCL };
+           B_TF = 12 + 2 * CK_RING, B_TE = B_TF + CK_TILES, B_SC = B_TE + CK_TILES, B_SE = B_SC + CK_SCL,
+           B_N = B_SE + CK_SCL };
 constexpr int CK_OFF_MISC = CK_OFF_BAR + B_N * 8;   // tensor-memory slot, dead flag, plan scalars
 constexpr int CK_SMEM = CK_OFF_MISC + 64 + 1024;
 static_assert(CK_SMEM <= 232448, "shared memory budget");
@@ -195,11 +196,13 @@ __device__ __forceinline__ bool bar_any(int id, int n, bool flag) {
 __device__ __forceinline__ void arrive_local(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// Arrive on a barrier of either CTA of the pair (cluster address). What the arrival announces
-// (operands, scores read) lies in the arriving CTA's own shared or tensor memory, made visible
-// there by the proxy and tcgen05 fences before it, and is read there by the tensor core: no
-// data crosses the pair through this barrier, and the default scope is enough. A release at
-// cluster scope measured 1,400 cycles per arrival (four per tile).
+// Arrive on a barrier of either CTA of the pair (cluster address). What the arrival announces to
+// the issue of the products (operands, scores read) lies in the arriving CTA's own shared or
+// tensor memory, behind the proxy and tcgen05 fences before it, and is read there by the tensor
+// core: no data crosses the pair through this barrier, and its scope is the default one. Words
+// that threads of a CTA hand to one another (pieces, tiles, scales) go through barriers of that
+// CTA alone: the way round over the other CTA would not order them. A release at cluster scope
+// measured 1,400 cycles per arrival (four per tile).
 __device__ __forceinline__ void arrive_cluster(uint32_t cbar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cbar) : "memory");
 }
@@ -626,7 +629,10 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
       mbar_init(bar(B_SD + i), 1);
       mbar_init(bar(B_PD + i), 1);
     }
-    for (int i = 0; i < CK_SCL; ++i) mbar_init(bar(B_SC + i), 2);
+    for (int i = 0; i < CK_SCL; ++i) {
+      mbar_init(bar(B_SC + i), 2);
+      mbar_init(bar(B_SE + i), CK_SM_WARPS);
+    }
     mbar_init(bar(B_SR), 2 * CK_SM_WARPS);
     mbar_init(bar(B_FIN), 1);
     for (int i = 0; i < CK_RING; ++i) {
@@ -964,6 +970,8 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
       const uint32_t st = it & 1;
       if (it >= 2 && !ck_wait(bar(B_SD + st), ((it - 2) >> 1) & 1, D.status, dead)) return;
       if (ct < PAGE) {
+        // the softmax has read the scales of four tiles before
+        if (it >= CK_SCL && !ck_wait(bar(B_SE + it % CK_SCL), (it / CK_SCL - 1) & 1, D.status, dead)) return;
         const uint32_t x = sbase + CK_OFF_SCL + (it % CK_SCL) * CK_SCL_T + ct * 4;
         sts32(x, __float_as_uint(good_scale(__uint_as_float(sc.x))));
         sts32(x + CK_SCL_G, __float_as_uint(good_scale(__uint_as_float(sc.y))));
@@ -971,7 +979,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
         sts32(x + 3 * CK_SCL_G, __float_as_uint(good_scale(__uint_as_float(sc.w))));
         if (ct == 0) sts32(there + (it % CK_SCL) * 4, n_rows > 0);
         __syncwarp();
-        if (lane == 0) arrive_local(bar(B_SC + it % CK_SCL));   // for V
+        if (lane == 0) arrive_local(bar(B_SC + it % CK_SCL));
       }
       const uint32_t kt = sbase + CK_OFF_K + st * CK_KSTAGE;
 #pragma unroll
@@ -1074,6 +1082,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
           __syncwarp();
           if (lane == 0) {
             arrive_cluster(sr0);
+            arrive_local(bar(B_SE + it % CK_SCL));
             arrive_cluster(pf0 + 8 * st);
           }
           if (!__all_sync(0xffffffffu, ok)) break;
@@ -1085,6 +1094,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
       for (int pg = P.pg0(); pg < P.pg1(); ++pg, ++it) {
         const uint32_t st = it & 1;
         ok &= ck_wait(bar(B_SD + st), (it >> 1) & 1, D.status, dead);
+        ok &= ck_wait(bar(B_SC + it % CK_SCL), (it / CK_SCL) & 1, D.status, dead);   // long past, by this CTA's own barrier
         tc_fence_after();
         const uint32_t sc = sbase + CK_OFF_SCL + (it % CK_SCL) * CK_SCL_T + key0 * 4;
         F2 s2[8];   // scores, times the sign of sm_scale, in pairs of keys
@@ -1121,10 +1131,13 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
             unpack(s2[j / 2], s[j], s[j + 1]);
           }
         }
+        const int seen = lds32(there + (it % CK_SCL) * 4) ? lim - pg * PAGE - key0 : 0;   // of this thread's keys
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_cluster(sr0);   // the score accumulators may be written again
-        const int seen = lds32(there + (it % CK_SCL) * 4) ? lim - pg * PAGE - key0 : 0;   // of this thread's keys
+        if (lane == 0) {   // the score accumulators may be written again, and the scales
+          arrive_cluster(sr0);
+          arrive_local(bar(B_SE + it % CK_SCL));
+        }
         if (seen < 16) {
 #pragma unroll
           for (int j = 0; j < 16; ++j) s[j] = j < seen ? s[j] : -INFINITY;
