@@ -38,8 +38,8 @@
 // QK(t+1) is issued before PV(t), so the softmax of one tile runs under the products of
 // its neighbours.
 //
-// Numbers. K codes and bf16 rope are exact in fp16 (rope to 65504); V is 4 code scale rounded
-// once to fp16 (the scale in two fp16 parts); P keeps 11 bits from 2^15 down to 2^-14, that is
+// Numbers. K codes and bf16 rope are exact in fp16 (rope to 65504); V is 4 code scale, a
+// product in fp32, rounded once to fp16; P keeps 11 bits from 2^15 down to 2^-14, that is
 // to 2^-21 of the row's largest (the shift by 2^7 buys seven binades under a dominant row).
 // Scores, maxima, sums and the output accumulate in fp32. A row with a NaN code, or rope
 // beyond fp16, scores NaN or infinity and is not seen; nor is one whose score is beyond 2^22.
@@ -333,26 +333,20 @@ __device__ __forceinline__ void codes_to_f16(uint4 v, uint4& lo, uint4& hi) {
   hi = make_uint4(h2_bits(e4m3x2_to_h2(v.z & 0xFFFFu)), h2_bits(e4m3x2_to_h2(v.z >> 16)),
                   h2_bits(e4m3x2_to_h2(v.w & 0xFFFFu)), h2_bits(e4m3x2_to_h2(v.w >> 16)));
 }
-// 4 x code x scale in fp16, rounded once: 4 x scale in two fp16 parts (the factor keeps the
-// second part's bits down to scales of 2^-16; it leaves the output again with the sum). A NaN
-// code becomes a finite value: its row's scores are NaN, so it is not seen, and 0 x it has to
-// be 0.
-struct VScale {
-  __half2 hi, lo;
-};
-__device__ __forceinline__ VScale v_scale(float s) {
-  VScale r;
-  const float s4 = CK_V_FACTOR * s;
-  const __half h = __float2half_rn(s4);
-  r.hi = __half2half2(h);
-  r.lo = __half2half2(__float2half_rn(s4 - __half2float(h)));
-  return r;
+// 4 x code x scale in fp16: the product in fp32, rounded once (the factor keeps two more bits of
+// the smallest; it leaves the output again with the sum). Products of fp16 parts of the scale are
+// not exact enough: the second part of a small scale is lost under fp16's smallest step, times a
+// code of up to 448. (Those products took 4 % less of a long call; with 2^-8 code and 2^10 scale, also
+// fp16, nearly exact, they take 1 % more; a branch on the scales to choose between them 0 to 20 % more.)
+// A NaN code becomes a finite value: its row's scores are NaN, so it is not seen, and 0 x it has to be 0.
+__device__ __forceinline__ uint32_t scaled2(uint32_t two, float scale4) {
+  const float2 c = __half22float2(e4m3x2_to_h2(two));
+  float a, b;
+  unpack(mul2(f2(__float_as_uint(c.x), __float_as_uint(c.y)), f2(scale4)), a, b);
+  return h2_bits(__hmin2(__floats2half2_rn(a, b), __half2half2(__ushort_as_half(0x7BFF))));
 }
-__device__ __forceinline__ uint32_t scaled2(uint32_t two, const VScale& v) {
-  const __half2 c = e4m3x2_to_h2(two);
-  return h2_bits(__hmin2(__hfma2(c, v.hi, __hmul2(c, v.lo)), __half2half2(__ushort_as_half(0x7BFF))));
-}
-__device__ __forceinline__ void codes_to_scaled_f16(uint4 v, const VScale& s, uint4& lo, uint4& hi) {
+__device__ __forceinline__ void codes_to_scaled_f16(uint4 v, float scale, uint4& lo, uint4& hi) {
+  const float s = CK_V_FACTOR * scale;
   lo = make_uint4(scaled2(v.x & 0xFFFFu, s), scaled2(v.x >> 16, s), scaled2(v.y & 0xFFFFu, s), scaled2(v.y >> 16, s));
   hi = make_uint4(scaled2(v.z & 0xFFFFu, s), scaled2(v.z >> 16, s), scaled2(v.w & 0xFFFFu, s), scaled2(v.w >> 16, s));
 }
@@ -1025,7 +1019,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         uint4 lo, hi;
-        codes_to_scaled_f16(val[k], v_scale(__uint_as_float(sv[k]) * sign), lo, hi);
+        codes_to_scaled_f16(val[k], __uint_as_float(sv[k]) * sign, lo, hi);
         const uint32_t d = (vt + k * 256) ^ (k * 32);
         sts128(d, lo);
         sts128(d ^ 16, hi);

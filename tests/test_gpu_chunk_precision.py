@@ -1,0 +1,67 @@
+"""The dense attention's documented precision: values of small scales, weights and values of 11
+significant bits."""
+import numpy as np
+import pytest
+
+import cache_plain as CP
+from test_gpu_cache_ops import HALF_STEP, Cache, check_chunk, make_q, run_chunk, torch
+
+pytestmark = pytest.mark.gpu
+
+
+def value_bound(kv, out, half_step):
+    """Equal weights (sm_scale 0: every weight is the same power of two): a value is rounded once to
+    fp16 after a product in fp32, at 4 times its size (2^-11 of it, 2^-27 at least, and 2^-24 of it);
+    n sums in fp32; a quotient rounded to the output type (fp16: 2^-25 at least)."""
+    v = np.abs(kv[:, :512])
+    each = np.maximum(2.0 ** -11 * v, 2.0 ** -27) + 2.0 ** -24 * v
+    return each.mean(0) + (v.shape[0] + 8) * 2.0 ** -23 * v.mean(0) + \
+        np.maximum(half_step * 1.01 * np.abs(out), 2.0 ** -25)
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("n", [1, 3, 40])
+@pytest.mark.parametrize("sizes", [(1e-2, 1e-3, 1e-4, 1e-6), (1.0, 1e-3, 1e-5, 1e-7), (1e-4, 3e-5, 1e-5, 1e-6),
+                                   (3e-3, 7e-4, 1e-30, 16000.0)])
+def test_values_of_small_scales(dtype, n, sizes):
+    """Groups of normal and of tiny values, largest codes and small ones, in one row and in all rows."""
+    rng = np.random.default_rng(n)
+    with Cache(heads=16, n_layers=1, lpi=1, pages=(1,)) as c:
+        x = rng.uniform(-1, 1, (n, 4, 128)) * np.array(sizes)[None, :, None]
+        x[:, :, ::7] /= 60.0
+        x[:, :, 5] = np.array(sizes)                   # a code of 448
+        rows = CP.pack_rows(x.reshape(n, 512), rng.standard_normal((n, 64)))
+        c.put_rows(0, 0, np.arange(n), rows)
+        kv = CP.row_values(rows)
+        q = make_q(rng, 2, 16, dtype)
+        out, lse = run_chunk(c, 0, [0], [0, 2], [n, n], q, 0.0)
+        assert c.pool.get_error() == 0
+        want = kv[:, :512].mean(0)
+        b = value_bound(kv, want, HALF_STEP[dtype])
+        err = np.abs(out.double().cpu().numpy() - want)
+        assert np.all(err <= b), ((err / b).max(axis=(0, 1)).reshape(4, 128).max(1), err.max())
+        assert np.all(np.abs(lse.cpu().numpy() - np.log(n)) <= 2.0 ** -19)
+
+
+@pytest.mark.parametrize("heads", [16, 64])
+def test_a_cache_of_tiny_and_normal_groups(heads):
+    """Rows whose groups differ by 10^7 in size, over several pages, within the bounds of any other."""
+    rng = np.random.default_rng(heads)
+    n = 700
+    with Cache(heads=heads, n_layers=1, lpi=1, pages=(11,)) as c:
+        x = rng.standard_normal((n, 4, 128)) * np.array([1e-3, 1.0, 1e-5, 1e-4])[None, :, None]
+        x[::3] *= 0.01
+        rows = CP.pack_rows(x.reshape(n, 512), rng.standard_normal((n, 64)))
+        c.put_rows(0, 0, np.arange(n), rows)
+        kv = [CP.row_values(rows)]
+        q = make_q(rng, 5, heads, "fp16")
+        limit = np.arange(n - 4, n + 1)
+        out, lse = run_chunk(c, 0, [0], [0, 5], limit, q, 1 / 24)
+        assert c.pool.get_error() == 0
+        check_chunk(c, kv, [0], [0, 5], limit, q, 1 / 24, out, lse, "fp16")
+        # the groups of small values by themselves, with no absolute allowance but fp16's own steps
+        for j in range(5):
+            wo, _, a, s = CP.attend(q[j].double().cpu().numpy(), kv[0][:limit[j]], 1 / 24)
+            b = 2.0 ** -11 * np.abs(wo) + (2 * CP.DZ * s[:, None] + 3 * 2.0 ** -11) * a + 2.0 ** -25 + 2.0 ** -27
+            err = np.abs(out[j].double().cpu().numpy() - wo)
+            assert np.all(err <= b), (j, (err / b).reshape(heads, 4, 128).max((0, 2)))
