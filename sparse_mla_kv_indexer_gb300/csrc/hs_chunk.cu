@@ -127,7 +127,15 @@ constexpr float CK_P_SHIFT = 7.f;          // P = 2^(z - m + 7) <= 2^15
 // Largest score in log2 units: m and 7 - m are each rounded by at most 2^-3 then, and a P of
 // 2^15 times those 2^(1/4) stays below fp16's largest. Far beyond, P would overflow.
 constexpr float CK_MAX_Z = 4194304.f;      // 2^22
+// A row's reference may lie as far below, and further until its end: scores next to the border keep
+// their weights (P at most 2^15 times 2^(1/2) there), and those below -2^23, whose reference is
+// CK_LOW, have the weight 0 that they have next to any score in range. A row that ends with a
+// reference below -2^22 is reported.
+constexpr float CK_LOW_Z = -8388608.f;     // -2^23
+constexpr float CK_LOW = -3.0e38f;
 constexpr float CK_MAX_SM_SCALE = 1e20f;   // times any score of finite operands (1e12): finite
+
+__device__ __forceinline__ bool only_low(float m) { return m > -INFINITY && m < -CK_MAX_Z; }
 
 // A pair's partial results: for each of its two cut blocks 128 rows of unnormalised
 // outputs and (reference in log2 units, sum); and the block that starts in its range and
@@ -962,10 +970,10 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
     }
     while (more) {
       const uint32_t st = it & 1;
+      // the softmax has read the scales of four tiles before
+      if (ct < PAGE && it >= CK_SCL && !ck_wait(bar(B_SE + it % CK_SCL), (it / CK_SCL - 1) & 1, D.status, dead)) return;
       if (it >= 2 && !ck_wait(bar(B_SD + st), ((it - 2) >> 1) & 1, D.status, dead)) return;
       if (ct < PAGE) {
-        // the softmax has read the scales of four tiles before
-        if (it >= CK_SCL && !ck_wait(bar(B_SE + it % CK_SCL), (it / CK_SCL - 1) & 1, D.status, dead)) return;
         const uint32_t x = sbase + CK_OFF_SCL + (it % CK_SCL) * CK_SCL_T + ct * 4;
         sts32(x, __float_as_uint(good_scale(__uint_as_float(sc.x))));
         sts32(x + CK_SCL_G, __float_as_uint(good_scale(__uint_as_float(sc.y))));
@@ -1087,8 +1095,8 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
       float m = -INFINITY, l = 0.f;   // the row's reference (its four threads alike), this thread's sum
       for (int pg = P.pg0(); pg < P.pg1(); ++pg, ++it) {
         const uint32_t st = it & 1;
+        ok &= ck_wait(bar(B_SC + it % CK_SCL), (it / CK_SCL) & 1, D.status, dead);   // over long before the products are
         ok &= ck_wait(bar(B_SD + st), (it >> 1) & 1, D.status, dead);
-        ok &= ck_wait(bar(B_SC + it % CK_SCL), (it / CK_SCL) & 1, D.status, dead);   // long past, by this CTA's own barrier
         tc_fence_after();
         const uint32_t sc = sbase + CK_OFF_SCL + (it % CK_SCL) * CK_SCL_T + key0 * 4;
         F2 s2[8];   // scores, times the sign of sm_scale, in pairs of keys
@@ -1158,13 +1166,10 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
         mt *= scale;
         float f = 1.f;
         if (mt > m + CK_RESCALE_LOG2) {   // also the first finite maximum, when m is -inf
-          if (m > -INFINITY) f = ex2_approx(m - mt);
-          if (mt > -CK_MAX_Z)
-            m = mt;
-          else
-            bad_range = true;   // its weights are 0, as those of other rows next to a score in range
+          f = ex2_approx(m - mt);
+          m = mt > CK_LOW_Z ? mt : CK_LOW;
         }
-        const float off = m > -INFINITY ? CK_P_SHIFT - m : 0.f;   // no finite score yet: every weight is 0
+        const float off = m > CK_LOW_Z ? CK_P_SHIFT - m : 0.f;   // no score beside which one counts: every weight is 0
         F2 ls2 = f2(0.f);
         uint32_t ph[8];
 #pragma unroll
@@ -1214,6 +1219,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
       m -= CK_P_SHIFT + CK_V_SHIFT;
       const int dim = (2 * half + sub) * 128;      // this thread's output dims
       if (P.slot() < 0) {
+        if (only_low(m)) l = 0.f, bad_range = true;
         const float inv = l > 0.f ? 1.f / l : 0.f;
         // 16 columns at a time through this warp's quarter of its rows' P (free until the next
         // exchange of maxima), so that two lanes store 32 bytes of one row
@@ -1360,6 +1366,10 @@ __global__ void __launch_bounds__(CM_THREADS) chunk_merge_kernel(const Dev D, co
         o.x += w * v.x, o.y += w * v.y, o.z += w * v.z, o.w += w * v.w;
       }
     }
+  }
+  if (only_low(m)) {
+    l = 0.f;
+    if (col == 0) set_status(D.status, HS_ERR_RANGE);
   }
   const float inv = l > 0.f ? 1.f / l : 0.f;
   const int tok = cut.tok0 + row / H, h = row % H;
