@@ -325,8 +325,9 @@ hs_status hs_offload_pages(hs_pool* pool, int32_t n, const int32_t* d_pool_pages
 /* Quantise the new rows of one layer as they are written: n_tokens KV rows of `layer`
  * and index keys of its indexer group (layer / layers_per_indexer).
  *  d_req, d_pos  [n] request slot and position of each token. req -1 skips the token
- *                (padding). A position given twice in adjacent tokens is written once, from
- *                the later one; otherwise a position may occur once per call.
+ *                (padding). A position given again in the next token that is not padding, at
+ *                most 32 tokens on, is written once, from the later one; otherwise a position
+ *                may occur once per call.
  *  dtype         element type of the three inputs: HS_BF16, HS_FP16 or HS_FP32.
  *  d_latent, d_rope  [n, 512] and [n, 64], both or neither (NULL). Per 128 latent values:
  *                scale = amax / 448 (1 when all are zero), code = the e4m3 value nearest to

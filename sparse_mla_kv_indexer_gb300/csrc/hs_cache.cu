@@ -195,6 +195,22 @@ __device__ __forceinline__ Place place_of(const Dev& D, const int32_t* req_of, c
   p.at = (long long)p.r * D.max_pages + (p.pos >> 6);
   return p;
 }
+// Whether the next token that is not padding, of the 32 behind this lane's t = base + lane, gives
+// the same position again (which then is the one to be written). All lanes take part: they hold
+// the 64 tokens from base on, two each.
+constexpr int CA_AGAIN = 32;
+__device__ __forceinline__ bool given_again(const int32_t* req_of, const int32_t* pos_of, int base, int n) {
+  const int lane = threadIdx.x & 31, t = base + lane;
+  const bool in0 = t < n, in1 = n - t > CA_AGAIN;
+  const int r0 = in0 ? req_of[t] : -1, r1 = in1 ? req_of[t + CA_AGAIN] : -1;
+  const int p0 = in0 ? pos_of[t] : 0, p1 = in1 ? pos_of[t + CA_AGAIN] : 0;
+  const uint64_t live = (uint64_t)__ballot_sync(0xffffffffu, r1 != -1) << 32 | __ballot_sync(0xffffffffu, r0 != -1);
+  const int ahead = __ffs((unsigned)(live >> (lane + 1))), at = (lane + ahead) & 31;   // 0: none
+  const int ra0 = __shfl_sync(0xffffffffu, r0, at), ra1 = __shfl_sync(0xffffffffu, r1, at);
+  const int pa0 = __shfl_sync(0xffffffffu, p0, at), pa1 = __shfl_sync(0xffffffffu, p1, at);
+  const bool first = lane + ahead < 32;
+  return ahead > 0 && (first ? ra0 : ra1) == r0 && (first ? pa0 : pa1) == p0;
+}
 template <typename P>
 __device__ __forceinline__ P* shfl_ptr(P* p, int lane) {
   const uint64_t v = reinterpret_cast<uint64_t>(p);
@@ -217,10 +233,8 @@ append_quantized_kernel(const Dev D, int layer, int group, int n, int per_warp, 
   uint8_t *row_mine = nullptr, *page_mine = nullptr;
   int off_mine = 0;
   {
-    const int t = base + lane;
-    Place p = place_of(D, req_of, pos_of, t, lane < count);
-    // the same position again in the next token: that one is written
-    if (p.at >= 0 && t + 1 < n && req_of[t + 1] == p.r && pos_of[t + 1] == p.pos) p.at = -1;
+    Place p = place_of(D, req_of, pos_of, base + lane, lane < count);
+    if (given_again(req_of, pos_of, base, n)) p.at = -1;
     if (p.at >= 0) {
       off_mine = p.pos & 63;
       const int pg = latent ? D.bt[p.at] : -1, ip = keys ? D.idx_bt[p.at] : -1;

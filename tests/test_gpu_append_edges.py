@@ -1,0 +1,64 @@
+"""Edges of the quantised append on the GPU: positions given more than once."""
+import numpy as np
+import pytest
+
+import cache_plain as CP
+from test_gpu_cache_ops import Cache, i32, values
+
+pytestmark = pytest.mark.gpu
+
+
+def chains(rng, n, pages, longest):
+    """Positions that occur in up to four tokens, with up to `longest` padding tokens between one
+    and the next; returns req, pos and the token that each position is written from."""
+    req, pos, last = [], [], {}
+    free = iter(rng.permutation(pages * 64))
+    while len(req) < n:
+        p = int(next(free))
+        for k in range(int(rng.integers(1, 5))):
+            if k:
+                gap = int(rng.integers(0, longest + 1))
+                req += [-1] * gap
+                pos += rng.integers(0, pages * 64, gap).tolist()
+            last[p] = len(req)
+            req.append(0)
+            pos.append(p)
+    return np.array(req, np.int32), np.array(pos, np.int32), last
+
+
+@pytest.mark.parametrize("n,longest", [(40, 0), (300, 2), (3000, 31), (3000, 3), (9000, 5), (40000, 31), (200000, 2)])
+def test_a_position_given_again_behind_padding_is_written_from_the_later_token(n, longest):
+    rng = np.random.default_rng(n + longest)
+    pages = -(-n // 64)
+    req, pos, last = chains(rng, n, pages, longest)
+    n = len(req)
+    with Cache(n_layers=1, lpi=1, pages=(pages,)) as c:
+        lat, lf = values(rng, n, 512, "bf16")
+        rope, rf = values(rng, n, 64, "bf16")
+        keys, kf = values(rng, n, 128, "bf16")
+        c.pool.append_quantized(0, i32(req), i32(pos), lat, rope, keys)
+        assert c.pool.get_error() == 0
+        at, tok = np.array(list(last)), np.array(list(last.values()))
+        some = np.sort(rng.permutation(len(at))[:20000])
+        at, tok = at[some], tok[some]
+        assert np.array_equal(c.get_rows(0, 0, at), CP.pack_rows(lf[tok], rf[tok]))
+        codes, scales = c.get_keys(0, 0, at)
+        wc, ws = CP.quantise(kf[tok])
+        assert np.array_equal(codes, wc) and np.array_equal(scales, ws[:, 0])
+
+
+def test_the_last_of_32_padding_tokens_apart():
+    """31 padding tokens between: one write; a chain over a warp's and a call's end."""
+    rng = np.random.default_rng(1)
+    with Cache(n_layers=1, lpi=1, pages=(4,)) as c:
+        for lead in (0, 1, 30, 31, 32, 33):
+            n = lead + 33
+            req, pos = np.full(n, -1, np.int32), np.arange(n, dtype=np.int32)
+            req[:lead + 1] = 0
+            req[-1], pos[-1] = 0, lead
+            lat, lf = values(rng, n, 512, "bf16")
+            rope, rf = values(rng, n, 64, "bf16")
+            c.pool.append_quantized(0, i32(req), i32(pos), lat, rope)
+            assert c.pool.get_error() == 0
+            tok = np.r_[np.arange(lead), n - 1]
+            assert np.array_equal(c.get_rows(0, 0, np.arange(lead + 1)), CP.pack_rows(lf[tok], rf[tok]))
