@@ -376,7 +376,7 @@ hs_status hs_chunk_workspace(const hs_pool* pool, int64_t* bytes);
  *               left alone. A start out of order or range sets HS_ERR_BAD_ID and is clamped.
  *  d_limit      [n_tokens] int32, 0 <= limit <= max_ctx, in any order. A token of limit 0
  *               gets out 0 and lse -inf, and so does one of a bad request or limit
- *               (HS_ERR_BAD_ID).
+ *               (HS_ERR_BAD_ID). The q of a token of limit 0 may hold anything.
  *  dtype        of q and out: HS_BF16 or HS_FP16.
  *  d_q, d_out   element (j, h, d) at j * stride_token + h * stride_head + d; d < 576 for q,
  *               < 512 for out. 16-byte aligned, strides multiples of 8 elements (q: >= 0;

@@ -902,6 +902,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
     };
     auto convert_q = [&]() {
       asm volatile("cp.async.wait_all;" ::: "memory");
+      bool bad = false;
       q_first();
 #pragma unroll 1
       for (int k = 0; k < 18; k += 3) {
@@ -914,8 +915,17 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
         }
 #pragma unroll
         for (int i = 0; i < 3; ++i) {
-          const uint4 f = q_to_f16<T>(v[i], &bad_range);
+          const uint4 f = q_to_f16<T>(v[i], &bad);
           if constexpr (!__is_same(T, __half)) sts128(dst[i], f);
+        }
+      }
+      if (bad) {   // rare: which tokens' they are, for it is no error in one that sees nothing
+        q_first();
+#pragma unroll 1
+        for (int k = 0; k < 18; ++k, q_next()) {
+          bool here = false, ignore = false;
+          q_to_f16<__half>(lds128(q_at()), &here);
+          if (here) bad_range |= clamp_limit(D, __ldg(A.limit + tok0 + ((2 * qr + (int)rank) >> hs)), &ignore) > 0;
         }
       }
     };

@@ -70,3 +70,36 @@ def test_scores_next_to_the_lower_border():
         # units are held to 2^-2 of one, their reference as well
         assert np.all(np.abs(out[0].double().cpu().numpy() - wo) <= 1.01 * 2.0 ** -10 * np.abs(wo))
         assert np.all(np.abs(lse[0].cpu().numpy() - wl) <= 1.0)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("heads", [16, 64])
+def test_queries_of_tokens_that_see_nothing(heads, dtype):
+    """Padding tokens inside a segment (limit 0) may hold anything, NaN and infinities too: their
+    output is 0 and nothing is reported, until one of them sees a row."""
+    rng = np.random.default_rng(heads)
+    with Cache(heads=heads, n_layers=1, lpi=1, pages=(3,)) as c:
+        x = rng.standard_normal((150, 576))
+        rows = CP.pack_rows(x[:, :512], x[:, 512:])
+        c.put_rows(0, 0, np.arange(150), rows)
+        q = make_q(rng, 30, heads, "bf16").to(dtype)
+        limit = 150 - np.arange(30)
+        blind = [1, 8, 9, 10, 15, 29]
+        limit[blind] = 0
+        q[1], q[8, 3, 575], q[9, :, 0], q[10] = float("nan"), float("inf"), float("-inf"), float("nan")
+        q[15, heads - 1, 64:128] = float("nan")
+        q[29] = float("inf")
+        name = "bf16" if dtype is torch.bfloat16 else "fp16"
+        clean = q.clone()
+        clean[blind] = 0
+        for start in ([0, 30], [0, 9, 11, 30]):
+            segs = len(start) - 1
+            out, lse = run_chunk(c, 0, [0] * segs, start, limit, q, 1 / 24)
+            assert c.pool.get_error() == 0
+            check_chunk(c, [CP.row_values(rows)], [0] * segs, start, limit, clean, 1 / 24, out, lse, name)
+        for j in blind:                                # one row seen: reported, and that query alone
+            one = limit.copy()
+            one[j] = 1
+            out, lse = run_chunk(c, 0, [0], [0, 30], one, q, 1 / 24)
+            assert c.pool.get_error() == RANGE, j
+            check_chunk(c, [CP.row_values(rows)], [0], [0, 30], limit, clean, 1 / 24, out, lse, name, set(range(30)) - {j})
