@@ -345,10 +345,13 @@ read_rows_kernel(const Dev D, int layer, int group, int n, int per_warp, const i
         const int ip = D.idx_bt[p.at];
         if (ip >= 0 && ip < D.num_idx_pages)
           page_mine = reinterpret_cast<const uint8_t*>(D.idx[group]) + (size_t)ip * D.idx_page_bytes;
-        else
+        else if (err == HS_OK)
           err = HS_ERR_BAD_ID;
       }
-      if (err != HS_OK) set_status(D.status, err);
+      if (err != HS_OK) {   // nothing of this token is written
+        set_status(D.status, err);
+        row_mine = page_mine = nullptr;
+      }
     }
   }
   for (int k0 = 0; k0 < count; k0 += CA_READ) {
