@@ -136,17 +136,18 @@ __device__ __forceinline__ float quantise(float (&v)[N], uint32_t (&code)[N / 4]
   float a = lanes_amax<LANES>(amax_of(v));
   if ((a >= 8.6736174e-19f && a <= FLT_MAX) || a == 0.f) {   // 2^-60
     const float scale = a > 0.f ? over(a, E4M3_MAX, 1.f / E4M3_MAX) : 1.f;
-    const float rs = __frcp_rn(scale);
-    const F2 r = f2(rs), minus = f2(-scale);
+    // minus the quotients, and the signs of the codes turned: so that -0 keeps its sign (q + r (x - q
+    // scale) would add +0 to it)
+    const F2 r = f2(-__frcp_rn(scale)), s = f2(scale);
 #pragma unroll
     for (int i = 0; i < N; i += 4) {
       float q[4];
 #pragma unroll
       for (int k = 0; k < 4; k += 2) {
         const F2 x = f2(__float_as_uint(v[i + k]), __float_as_uint(v[i + k + 1])), q0 = mul2(x, r);
-        unpack(fma2(fma2(q0, minus, x), r, q0), q[k], q[k + 1]);
+        unpack(fma2(fma2(q0, s, x), r, q0), q[k], q[k + 1]);
       }
-      code[i / 4] = e4m3x4(q[0], q[1], q[2], q[3]);
+      code[i / 4] = e4m3x4(q[0], q[1], q[2], q[3]) ^ 0x80808080u;
     }
     return scale;
   }

@@ -3,7 +3,7 @@ import numpy as np
 import pytest
 
 import cache_plain as CP
-from test_gpu_cache_ops import Cache, i32, values
+from test_gpu_cache_ops import RANGE, Cache, dt, i32, torch, values
 
 pytestmark = pytest.mark.gpu
 
@@ -62,3 +62,24 @@ def test_the_last_of_32_padding_tokens_apart():
             assert c.pool.get_error() == 0
             tok = np.r_[np.arange(lead), n - 1]
             assert np.array_equal(c.get_rows(0, 0, np.arange(lead + 1)), CP.pack_rows(lf[tok], rf[tok]))
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+def test_minus_zero_keeps_its_sign(dtype):
+    """The e4m3 value nearest to -0 / scale is -0, in groups of zeros and beside other values."""
+    rng = np.random.default_rng(6)
+    with Cache(pages=(1,)) as c:
+        x = rng.standard_normal((2, 640)).astype(np.float32)
+        x[:, 128:256] = 0
+        x[1, 512:] = 0
+        x[rng.random((2, 640)) < 0.3] = 0
+        x = np.where((x == 0) & (rng.random((2, 640)) < 0.5), np.float32(-0.0), x)
+        t = torch.from_numpy(x).to(dt(dtype)).cuda()
+        rope = torch.zeros(2, 64, dtype=dt(dtype), device="cuda")
+        c.pool.append_quantized(0, i32([0, 0]), i32([3, 4]), t[:, :512], rope, t[:, 512:])
+        assert c.pool.get_error() == 0
+        f = t.float().cpu().numpy()
+        assert np.array_equal(c.get_rows(0, 0, [3, 4]), CP.pack_rows(f[:, :512], np.zeros((2, 64))))
+        codes, scales = c.get_keys(0, 0, [3, 4])
+        wc, ws = CP.quantise(f[:, 512:])
+        assert np.array_equal(codes, wc) and np.array_equal(scales, ws[:, 0])
