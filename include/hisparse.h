@@ -330,8 +330,8 @@ hs_status hs_offload_pages(hs_pool* pool, int32_t n, const int32_t* d_pool_pages
  *                may occur once per call.
  *  dtype         element type of the three inputs: HS_BF16, HS_FP16 or HS_FP32.
  *  d_latent, d_rope  [n, 512] and [n, 64], both or neither (NULL). Per 128 latent values:
- *                scale = amax / 448 (1 when all are zero), code = the e4m3 value nearest to
- *                x / scale, ties to even; rope is rounded to bf16.
+ *                scale = amax / 448, at least 2^-126 (1 when all are zero), code = the e4m3
+ *                value nearest to x / scale, ties to even; rope is rounded to bf16.
  *  d_keys        nullable [n, 128]. HS_IDX_FP8: the same with one scale per key.
  *                HS_IDX_INT8: x / key_scale rounded to the nearest integer, ties to even,
  *                clamped to +-127; key_scale (a normal positive fp32) is used for this

@@ -4,7 +4,7 @@
 // and 3: a cached KV row is 512 FP8 latent values with four fp32 scales and 64 bf16
 // rope values (656 bytes); an index key is 128 FP8 values with one fp32 scale. The
 // pages give the formats only; the quantisation is
-//   scale = amax / 448 over the 128 values of a group (1 when they are all zero),
+//   scale = amax / 448 over the 128 values of a group, 2^-126 at least (1 when they are all zero),
 //   code  = x / scale rounded to the nearest e4m3 value, ties to even.
 // Both divisions are the correctly rounded fp32 ones: a code can differ from the one of
 // unrounded arithmetic only where x / scale lies within 2^-23 of a rounding border.
@@ -38,7 +38,7 @@ constexpr int CA_WARPS = 4;          // warps per CTA
 constexpr int CA_READ = 2;           // tokens of a warp at a time when reading
 constexpr int CA_SM_WARPS = 32;      // warps per SM among which the tokens are dealt, up to 32 each
 constexpr float E4M3_MAX = 448.f;
-constexpr float MIN_SCALE = 1.17549435e-38f;   // the smallest normal fp32: x / scale stays finite and below 448
+constexpr float MIN_SCALE = 1.17549435e-38f;   // 2^-126, the smallest normal fp32: below it amax / 448 has too few bits, or none
 constexpr float BF16_MAX = 3.38953139e38f;
 
 // N consecutive values of type T (16-byte or smaller aligned accesses) as they are stored, as
@@ -123,10 +123,11 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
          (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3) << 16;
 }
 // The rare groups (a value that is not finite, or an amax below 2^-60), out of line: a NaN
-// becomes 0, an infinity takes the group's largest finite magnitude, which is the largest code.
+// becomes 0, an infinity what the group's scale makes the largest code: its largest finite
+// magnitude, or 448 times the least scale, or times that of zeros.
 __device__ __noinline__ float rare_value(float x, float amax) {
   const float a = fabsf(x);
-  return a <= FLT_MAX ? x : x != x ? 0.f : copysignf(amax > 0.f ? amax : E4M3_MAX, x);
+  return a <= FLT_MAX ? x : x != x ? 0.f : copysignf(amax > 0.f ? fmaxf(amax, E4M3_MAX * MIN_SCALE) : E4M3_MAX, x);
 }
 __device__ __noinline__ float rare_quotient(float x, float scale) { return __fdiv_rn(x, scale); }
 // The N values that each of LANES lanes holds of one group, as N / 4 words of e4m3 codes;

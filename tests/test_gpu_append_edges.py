@@ -64,6 +64,32 @@ def test_the_last_of_32_padding_tokens_apart():
             assert np.array_equal(c.get_rows(0, 0, np.arange(lead + 1)), CP.pack_rows(lf[tok], rf[tok]))
 
 
+@pytest.mark.parametrize("magnitude", [0.0, 1e-45, 1e-40, 1e-37, 5e-36, 1e-20, 1.0, 3.3e38])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_an_infinity_is_the_largest_code_whatever_the_group(dtype, magnitude):
+    """In groups whose scale is held at 2^-126 too; the finite values beside it keep the group's
+    scale, which is 1 where they are all zero."""
+    rng = np.random.default_rng(5)
+    with Cache(pages=(2,)) as c:
+        x = rng.uniform(-1, 1, (3, 512)) * magnitude
+        x[:, ::128] = magnitude
+        x[1, 7], x[1, 200], x[2, 300], x[2, 301] = np.inf, -np.inf, np.inf, np.nan
+        k = rng.uniform(-1, 1, (3, 128)) * magnitude
+        k[2, 100] = -np.inf
+        lat, keys = (torch.from_numpy(v.astype(np.float32)).to(dt(dtype)).cuda() for v in (x, k))
+        rope = torch.zeros(3, 64, dtype=dt(dtype), device="cuda")
+        c.pool.append_quantized(0, i32([0, 0, 0]), i32([0, 1, 64]), lat, rope, keys)
+        assert c.pool.get_error() == RANGE
+        lf, kf = lat.float().cpu().numpy(), keys.float().cpu().numpy()
+        want = CP.pack_rows(np.where(np.isfinite(lf), lf, 0), np.zeros((3, 64)))
+        want[1, 7], want[1, 200], want[2, 300], want[2, 301] = 0x7E, 0xFE, 0x7E, 0
+        assert np.array_equal(c.get_rows(0, 0, [0, 1, 64]), want)
+        codes, scales = c.get_keys(0, 0, [0, 1, 64])
+        wc, ws = CP.quantise(np.where(np.isfinite(kf), kf, 0))
+        wc[2, 100] = 0xFE
+        assert np.array_equal(codes, wc) and np.array_equal(scales, ws[:, 0])
+
+
 @pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
 def test_minus_zero_keeps_its_sign(dtype):
     """The e4m3 value nearest to -0 / scale is -0, in groups of zeros and beside other values."""
