@@ -340,8 +340,9 @@ hs_status hs_offload_pages(hs_pool* pool, int32_t n, const int32_t* d_pool_pages
  *                16-byte aligned, each stride a multiple of 16 bytes.
  * The page holding each position must be resident (HS_ERR_BAD_ID otherwise, and that part
  * of that token is not written). A NaN is written as 0 and an infinity as the largest value
- * of its format with the group's scale taken from its finite values; both set
- * HS_ERR_RANGE. n_tokens at most HS_CACHE_MAX_TOKENS. */
+ * of its format with the group's scale taken from its finite values, as is finite rope that
+ * bf16 would round to infinity; all of these set HS_ERR_RANGE. n_tokens at most
+ * HS_CACHE_MAX_TOKENS. */
 hs_status hs_append_quantized(hs_pool* pool, int32_t layer, int32_t n_tokens, const int32_t* d_req,
                               const int32_t* d_pos, int32_t dtype, const void* d_latent, int64_t ld_latent,
                               const void* d_rope, int64_t ld_rope, const void* d_keys, int64_t ld_keys,

@@ -40,6 +40,7 @@ constexpr int CA_SM_WARPS = 32;      // warps per SM among which the tokens are 
 constexpr float E4M3_MAX = 448.f;
 constexpr float MIN_SCALE = 1.17549435e-38f;   // 2^-126, the smallest normal fp32: below it amax / 448 has too few bits, or none
 constexpr float BF16_MAX = 3.38953139e38f;
+constexpr float BF16_OVER = 3.39617752e38f;   // BF16_MAX and half a step: from here on bf16 rounds to infinity
 
 // N consecutive values of type T (16-byte or smaller aligned accesses) as they are stored, as
 // fp32, and back.
@@ -282,7 +283,7 @@ append_quantized_kernel(const Dev D, int layer, int group, int n, int per_warp, 
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const float r = fminf(fmaxf(rp[i], -BF16_MAX), BF16_MAX);
-        bad |= !(fabsf(rp[i]) <= FLT_MAX);
+        bad |= !(fabsf(rp[i]) < BF16_OVER);
         rp[i] = rp[i] != rp[i] ? 0.f : r;
       }
       store_f32<__nv_bfloat16, 2>(reinterpret_cast<__nv_bfloat16*>(row + LATENT + 16) + lane * 2, rp);

@@ -90,6 +90,21 @@ def test_an_infinity_is_the_largest_code_whatever_the_group(dtype, magnitude):
         assert np.array_equal(codes, wc) and np.array_equal(scales, ws[:, 0])
 
 
+def test_finite_rope_beyond_bf16_is_the_largest_value_and_reported():
+    """fp32 rope from bf16's largest value and half a step on; the value below it is rounded."""
+    with Cache(pages=(2,)) as c:
+        top = np.array([0x7F7F0000, 0x7F7F7FFF, 0x7F7F8000, 0x7F7FFFFF], np.uint32).view(np.float32)
+        lat = torch.ones(1, 512, device="cuda")
+        for i, v in enumerate(top):
+            for sign in (1.0, -1.0):
+                rope = torch.zeros(1, 64, device="cuda")
+                rope[0, 9] = float(v) * sign
+                c.pool.append_quantized(0, i32([0]), i32([5]), lat, rope)
+                assert c.pool.get_error() == (RANGE if i >= 2 else 0), hex(v.view(np.uint32))
+                got = c.get_rows(0, 0, [5])[0, 528:].view("<u2")
+                assert got[9] == (0x7F7F if sign > 0 else 0xFF7F) and np.all(np.delete(got, 9) == 0)
+
+
 @pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
 def test_minus_zero_keeps_its_sign(dtype):
     """The e4m3 value nearest to -0 / scale is -0, in groups of zeros and beside other values."""
