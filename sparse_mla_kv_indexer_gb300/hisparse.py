@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import sys
 from typing import Optional, Sequence
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libhisparse.so")
@@ -208,7 +209,8 @@ class Pool:
     def __init__(self, cfg: PoolConfig, kv_layers: Sequence, idx_layers: Sequence, host_kv):
         self.cfg = cfg
         self._keep = (list(kv_layers), list(idx_layers), host_kv)
-        self.device = _current_device()
+        # the current device; without torch it is looked up by the first call that takes tensors
+        self.device = _current_device() if sys.modules.get("torch") is not None else None
         kv = (_P * len(kv_layers))(*[_ptr(t) for t in kv_layers])
         ix = (_P * len(idx_layers))(*[_ptr(t) for t in idx_layers])
         handle = _P()
@@ -284,11 +286,17 @@ class Pool:
                                                         _ptr(host_pages), _stream(stream)))
 
     # -- prefill and dense decode, one layer at a time ---------------------------------
+    def _device(self) -> int:
+        if self.device is None:
+            self.chunk_workspace_bytes()     # refused unless the pool's device is the current one
+            self.device = _current_device()
+        return self.device
+
     def _cache_args(self, req, pos, latent, rope, keys):
         first = latent if latent is not None else rope if rope is not None else keys
         if first is None:
             raise ValueError("none of latent, rope and keys is given")
-        code, dtype, n, dev = _dtype(first), first.dtype, req.shape[0], self.device
+        code, dtype, n, dev = _dtype(first), first.dtype, req.shape[0], self._device()
         return (n, _ids("req", req, n, dev), _ids("pos", pos, n, dev), code,
                 *_values("latent", latent, n, 512, dtype, dev), *_values("rope", rope, n, 64, dtype, dev),
                 *_values("keys", keys, n, 128, dtype, dev))
@@ -322,7 +330,7 @@ class Pool:
         tokens [seg_start[i], seg_start[i + 1]) of request seg_req[i]; limit [n]; q [n, H, 576]
         and out [n, H, 512] bf16 or fp16, the last dimension contiguous; lse [n, H] fp32;
         work: chunk_workspace_bytes() bytes that no overlapping call uses."""
-        code, n, segs, heads, dev = _dtype(q), limit.shape[0], seg_req.shape[0], self.cfg.n_heads, self.device
+        code, n, segs, heads, dev = _dtype(q), limit.shape[0], seg_req.shape[0], self.cfg.n_heads, self._device()
         if q.shape != (n, heads, 576) or out.shape != (n, heads, 512) or out.dtype is not q.dtype:
             raise ValueError(f"q [{n}, {heads}, 576] and out [{n}, {heads}, 512] of one type are wanted")
         qs, os = q.stride(), out.stride()
