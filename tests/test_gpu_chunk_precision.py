@@ -4,6 +4,7 @@ import numpy as np
 import pytest
 
 import cache_plain as CP
+import chunk_bits as B
 from test_gpu_cache_ops import HALF_STEP, Cache, check_chunk, make_q, run_chunk, torch
 
 pytestmark = pytest.mark.gpu
@@ -65,3 +66,18 @@ def test_a_cache_of_tiny_and_normal_groups(heads):
             b = 2.0 ** -11 * np.abs(wo) + (2 * CP.DZ * s[:, None] + 3 * 2.0 ** -11) * a + 2.0 ** -25 + 2.0 ** -27
             err = np.abs(out[j].double().cpu().numpy() - wo)
             assert np.all(err <= b), (j, (err / b).reshape(heads, 4, 128).max((0, 2)))
+
+
+@pytest.mark.parametrize("heads", [16, 64])
+@pytest.mark.parametrize("n", [900, 6000])
+def test_weights_and_values_have_11_bits(heads, n):
+    """The errors' root mean square, which a bit less in either would exceed (test_chunk_bits.py)."""
+    x, q, sm = B.data(n, n=n, heads=heads)
+    with Cache(heads=heads, n_layers=1, lpi=1, pages=(-(-n // 64),)) as c:
+        rows = CP.pack_rows(x[:, :512], x[:, 512:])
+        c.put_rows(0, 0, np.arange(n), rows)
+        kv = CP.row_values(rows)
+        out, _ = run_chunk(c, 0, [0], [0, 8], [n] * 8, torch.from_numpy(q).cuda(), sm)
+        assert c.pool.get_error() == 0
+        want = np.array([CP.attend(q[j].astype(np.float64), kv, sm)[0] for j in range(8)])
+        assert B.relative_rms(out.double().cpu().numpy(), want) < B.LIMIT
