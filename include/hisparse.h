@@ -389,15 +389,15 @@ hs_status hs_chunk_workspace(const hs_pool* pool, int64_t* bytes);
  * Rows of placeholder pages are read from the host copy through the mapping, once for every
  * 128 / H tokens that see them; a page with neither sets HS_ERR_HOST_MISSING and counts as
  * not seen. The cache may hold anything at positions that no token of the call sees.
- * Precision: z from products of the exact codes, summed in fp32 (q rounded to fp16 where it
- * is bf16: exact from 2^-14 to 65504 in magnitude), softmax statistics fp32, P fp16 with 11
- * significant bits down to 2^-21 of its row's largest, v = code * scale rounded once to fp16
- * (an absolute 2^-27 below 2^-16), sums fp32. Limits: |scale| below 36.5 (latents below
- * 16,352), rope and q below 65504 in magnitude, no e4m3 NaN code, and finite; z below
- * 2,900,000 (2^22 ln 2), and the largest z of a query row above minus that; |sm_scale| at most
- * 1e20 (HS_ERR_INVALID otherwise). Beyond them HS_ERR_RANGE is set; such a scale counts as 0, a
- * row with another such value, or with too large a z, as not seen, and a query row with such a
- * value, or without a z in range, sees nothing (out 0, lse -inf). */
+ * Precision: z from products of the exact codes, summed in fp32 (rope and bf16 q as fp16: exact
+ * from 2^-17 to 65504 in magnitude, off by 2^-25 at most below), softmax statistics fp32, P
+ * fp16 with 11 significant bits down to 2^-21 of its row's largest, v = code * scale in fp32
+ * rounded once to fp16 (11 significant bits, an absolute 2^-27 below 2^-16), sums fp32. Limits:
+ * |scale| below 36.5 (latents below 16,352), rope and q below 65504 in magnitude, no e4m3 NaN
+ * code, and finite; z below 2,900,000 (2^22 ln 2), and the largest z of a query row above minus
+ * that; |sm_scale| at most 1e20 (HS_ERR_INVALID otherwise). Beyond them HS_ERR_RANGE is set;
+ * such a scale counts as 0, a row with another such value, or with too large a z, as not seen,
+ * and a query row with such a value, or without a z in range, sees nothing (out 0, lse -inf). */
 hs_status hs_chunk_attention(hs_pool* pool, int32_t layer, int32_t n_segments, const int32_t* d_seg_req,
                              const int32_t* d_seg_start, int32_t n_tokens, const int32_t* d_limit, int32_t dtype,
                              const void* d_q, int64_t q_stride_token, int64_t q_stride_head, float sm_scale,

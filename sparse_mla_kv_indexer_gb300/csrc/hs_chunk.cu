@@ -38,7 +38,8 @@
 // QK(t+1) is issued before PV(t), so the softmax of one tile runs under the products of
 // its neighbours.
 //
-// Numbers. K codes and bf16 rope are exact in fp16 (rope to 65504); V is 4 code scale, a
+// Numbers. K codes are exact in fp16, and rope and bf16 queries from 2^-17 to 65504 in magnitude
+// (off by 2^-25 at most below: their last bits, or all, lie under fp16's smallest step); V is 4 code scale, a
 // product in fp32, rounded once to fp16; P keeps 11 bits from 2^15 down to 2^-14, that is
 // to 2^-21 of the row's largest (the shift by 2^7 buys seven binades under a dominant row).
 // Scores, maxima, sums and the output accumulate in fp32. A row with a NaN code, or rope
@@ -358,7 +359,7 @@ __device__ __forceinline__ void codes_to_scaled_f16(uint4 v, float scale, uint4&
   lo = make_uint4(scaled2(v.x & 0xFFFFu, s), scaled2(v.x >> 16, s), scaled2(v.y & 0xFFFFu, s), scaled2(v.y >> 16, s));
   hi = make_uint4(scaled2(v.z & 0xFFFFu, s), scaled2(v.z >> 16, s), scaled2(v.w & 0xFFFFu, s), scaled2(v.w >> 16, s));
 }
-// Eight bf16 -> fp16 (exact inside its normal range); *bad when one is beyond it.
+// Eight bf16 -> fp16 (exact from 2^-17 on); *bad when one is beyond its largest.
 __device__ __forceinline__ uint4 bf16x8_to_f16(uint4 v, bool* bad) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
   uint32_t o[4];

@@ -5,7 +5,7 @@ import pytest
 
 import cache_plain as CP
 import chunk_bits as B
-from test_gpu_cache_ops import HALF_STEP, Cache, check_chunk, make_q, run_chunk, torch
+from test_gpu_cache_ops import HALF_STEP, RANGE, Cache, check_chunk, make_q, run_chunk, torch
 
 pytestmark = pytest.mark.gpu
 
@@ -81,3 +81,29 @@ def test_weights_and_values_have_11_bits(heads, n):
         assert c.pool.get_error() == 0
         want = np.array([CP.attend(q[j].astype(np.float64), kv, sm)[0] for j in range(8)])
         assert B.relative_rms(out.double().cpu().numpy(), want) < B.LIMIT
+
+
+def test_small_rope_and_queries():
+    """In fp16, rope and bf16 queries are exact from 2^-17 to 65504 and off by at most 2^-25 below; of one
+    row seen, lse is the score: one exact product, then seven roundings to fp32 of numbers of its size (the
+    scale, z, the reference, twice shifted, its sum with the logarithm and the factor of that): 2^-21 of it.
+    Scores of 2,900,000 and more are out of range."""
+    r = np.array([2.0 ** -e * m for e in (-15, -8, 0, 9, 14, 16, 17, 18, 20, 23, 25, 26, 40) for m in (1.0, 1.0078125, 1.9921875)])
+    r = r[np.abs(r) <= 65504]
+    with Cache(heads=16, n_layers=1, lpi=1, pages=(1,)) as c:
+        for i, dtype in ((0, "bf16"), (0, "fp16"), (1, "bf16")):     # a small rope value, or a small query
+            big = 49152.0
+            for v in r:
+                x = np.zeros((1, 576))
+                x[0, 512] = v if i == 0 else big
+                c.put_rows(0, 0, [0], CP.pack_rows(x[:, :512], x[:, 512:]))
+                q = torch.zeros(1, 16, 576, dtype=torch.bfloat16 if dtype == "bf16" else torch.float16, device="cuda")
+                q[..., 512] = big if i == 0 else float(v)
+                out, lse = run_chunk(c, 0, [0], [0, 1], [1], q, 2.0 ** -10)
+                z = v * big * 2.0 ** -10
+                assert c.pool.get_error() == (RANGE if z > 2900000 else 0), (i, dtype, v)
+                if z > 2900000:
+                    assert torch.all(out == 0) and torch.all(torch.isneginf(lse))
+                    continue
+                off = 0 if v >= 2.0 ** -17 else 2.0 ** -25 * big * 2.0 ** -10
+                assert np.all(np.abs(lse.double().cpu().numpy() - z) <= 1.01 * off + 2.0 ** -21 * abs(z) + 2.0 ** -19), (i, dtype, v)
