@@ -87,7 +87,7 @@ typedef enum hs_status {
   HS_ERR_BAD_WEIGHT = 8,   /* device: a negative index-head weight */
   HS_ERR_SCRATCH_LIMIT = 9, /* request larger than the fixed scratch of hs_indexer_topk_noalloc */
   HS_ERR_NOT_RESOLVED = 10, /* hs_replay_topk met a token that is neither resident nor hot */
-  HS_ERR_RANGE = 11         /* device: an attention input beyond the fp16 range of the batched path */
+  HS_ERR_RANGE = 11         /* device: a value or a score beyond what a call can represent */
 } hs_status;
 
 /* Index-key formats.

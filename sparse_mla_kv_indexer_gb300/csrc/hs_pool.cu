@@ -219,7 +219,7 @@ const char* hs_status_string(hs_status s) {
     case HS_ERR_BAD_WEIGHT: return "negative index-head weight";
     case HS_ERR_SCRATCH_LIMIT: return "request exceeds the fixed scratch of the no-allocation indexer";
     case HS_ERR_NOT_RESOLVED: return "replayed token is neither resident nor in the hot buffer";
-    case HS_ERR_RANGE: return "attention input beyond the fp16 range of the batched path";
+    case HS_ERR_RANGE: return "a value or a score beyond what the call can represent";
   }
   return "unknown status";
 }
