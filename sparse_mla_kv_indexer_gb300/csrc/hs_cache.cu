@@ -434,7 +434,7 @@ CallArgs check_call(hs_pool* p, int32_t layer, int32_t n, const int32_t* d_req, 
   const int size = dtype_size(dtype);
   if (size == 0 || !on_pool_device(p)) return a;
   if (n > 0) {
-    if (!d_req || !d_pos || (!d_latent && !d_rope && !d_keys)) return a;
+    if (!d_req || !d_pos || !words_ok(d_req) || !words_ok(d_pos) || (!d_latent && !d_rope && !d_keys)) return a;
     if (d_latent && !rows_ok(d_latent, ld_latent, LATENT, size)) return a;
     if (d_rope && !rows_ok(d_rope, ld_rope, ROPE, size)) return a;
     if (d_keys && !rows_ok(d_keys, ld_keys, IDX_DIM, size)) return a;

@@ -1449,6 +1449,7 @@ extern "C" hs_status hs_chunk_attention(hs_pool* p, int32_t layer, int32_t n_seg
   if (n > 0 && n_seg > 0) {
     const auto aligned = [](const void* x) { return x && (reinterpret_cast<uintptr_t>(x) & 15) == 0; };
     if (!d_seg_req || !d_seg_start || !d_limit || !aligned(d_q) || !aligned(d_out) || !aligned(d_work) ||
+        !words_ok(d_seg_req) || !words_ok(d_seg_start) || !words_ok(d_limit) || !words_ok(d_lse) ||
         work_bytes < work_bytes_for(pairs) || !(fabsf(sm_scale) <= CK_MAX_SM_SCALE))
       return HS_ERR_INVALID;
     if (!stride_ok(q_tok, 0) || !stride_ok(q_head, 0) || !stride_ok(o_tok, LATENT) || !stride_ok(o_head, LATENT))

@@ -15,6 +15,9 @@ inline bool on_pool_device(const hs_pool* p) {
   return cudaGetDevice(&dev) == cudaSuccess && dev == p->device;
 }
 
+// An address that 4-byte words may be read from or written to.
+inline bool words_ok(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
+
 __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
