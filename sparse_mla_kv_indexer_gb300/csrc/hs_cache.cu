@@ -26,7 +26,6 @@
 #include <cuda_fp8.h>
 #include <float.h>
 #include <math.h>
-#include <nvtx3/nvToolsExt.h>
 
 #include "hs_chunk.cuh"
 
@@ -452,11 +451,6 @@ int tokens_per_warp(int n, int least) {
   return per < least ? least : per > 32 ? 32 : per;
 }
 int cache_grid(int n, int per_warp) { return (int)(((long long)n + CA_WARPS * per_warp - 1) / (CA_WARPS * per_warp)); }
-
-struct CallRange {
-  explicit CallRange(const char* name) { nvtxRangePushA(name); }
-  ~CallRange() { nvtxRangePop(); }
-};
 
 template <typename T>
 hs_status launch_append_quantized(hs_pool* p, int layer, int n, const int32_t* d_req, const int32_t* d_pos,

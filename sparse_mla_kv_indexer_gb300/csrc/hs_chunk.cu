@@ -56,7 +56,6 @@
 // the copy rate): 27 tiles a pair of 1.5 us, 12 us before the first and 5 us of merge.
 #include <cuda_fp8.h>
 #include <math.h>
-#include <nvtx3/nvToolsExt.h>
 
 #include <atomic>
 
@@ -68,7 +67,7 @@ namespace {
 
 constexpr int CK_THREADS = 640;
 constexpr int CK_SM_WARPS = 8, CK_SM = CK_SM_WARPS * 32;         // softmax
-constexpr int CK_CONV_WARP0 = 8, CK_CONV_WARPS = 8, CK_CONV = CK_CONV_WARPS * 32;
+constexpr int CK_CONV_WARP0 = 8, CK_CONV_WARPS = 8;               // conversion
 constexpr int CK_MMA_WARP = 16, CK_PLAN_WARP = 17;
 // Registers per thread: 96 at the launch (five warpgroups), then shifted between warpgroups,
 // whose sum stays within the launch's.
@@ -181,7 +180,6 @@ struct Piece {
   __device__ int tok0() const { return a.x; }
   __device__ int n_tok() const { return a.y; }
   __device__ int req() const { return a.z; }
-  __device__ int limit() const { return a.w; }
   __device__ int pg0() const { return b.x; }
   __device__ int pg1() const { return b.y; }
   __device__ int slot() const { return b.z; }
@@ -1301,7 +1299,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
 // in pair order. A CTA has four slices of 128 threads. WIDE (few cuts, of many parts each): CTA
 // (row, k) joins that row of the k-th cut, its parts dealt to the slices. Otherwise each slice
 // joins one row of one pair's cut.
-constexpr int CM_SLICES = 4, CM_THREADS = 128 * CM_SLICES, CM_MAX_PAIRS = 128, CM_WIDE_CUTS = 32;
+constexpr int CM_SLICES = 4, CM_THREADS = 128 * CM_SLICES, CM_WIDE_CUTS = 32;
 template <typename T, bool WIDE>
 __global__ void __launch_bounds__(CM_THREADS) chunk_merge_kernel(const Dev D, const ChunkArgs A) {
   __shared__ float4 acc[CM_SLICES][128];
@@ -1389,11 +1387,6 @@ __global__ void __launch_bounds__(CM_THREADS) chunk_merge_kernel(const Dev D, co
   // the outputs carry CK_V_FACTOR, and so do the sums
   if (A.lse && col == 0) A.lse[(size_t)tok * H + h] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
-
-struct CallRange {
-  explicit CallRange(const char* name) { nvtxRangePushA(name); }
-  ~CallRange() { nvtxRangePop(); }
-};
 
 bool stride_ok(int64_t s, int64_t least) { return s >= least && s < (1ll << 40) && s % 8 == 0; }
 

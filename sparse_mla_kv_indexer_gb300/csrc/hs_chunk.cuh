@@ -1,10 +1,18 @@
-// Shared by the cache operators of prefill (hs_cache.cu, hs_chunk.cu): element types and
-// the place of a request's page.
+// Shared by the cache operators of prefill (hs_cache.cu, hs_chunk.cu): element types, checks of
+// arguments and the place of a request's page.
 #pragma once
+
+#include <nvtx3/nvToolsExt.h>
 
 #include "hs_internal.cuh"
 
 namespace hs {
+
+// One NVTX range per ABI call, as for the other calls.
+struct CallRange {
+  explicit CallRange(const char* name) { nvtxRangePushA(name); }
+  ~CallRange() { nvtxRangePop(); }
+};
 
 inline int dtype_size(int32_t dtype) {
   return dtype == HS_BF16 || dtype == HS_FP16 ? 2 : dtype == HS_FP32 ? 4 : 0;
