@@ -45,15 +45,17 @@
 // Scores, maxima, sums and the output accumulate in fp32. A row with a NaN code, or rope
 // beyond fp16, scores NaN or infinity and is not seen; nor is one whose score is beyond 2^22.
 //
-// Measured on a GB300: 753 tokens over 74,913 rows with 64 heads 8.4 ms, 0.93 PFLOP/s, 50 % of
-// the measured bf16 rate; per tile of a pair 1.43 us, against 0.73 us of its products alone
+// Measured on a GB300: 753 tokens over 74,913 rows with 64 heads 8.9 ms, 0.88 PFLOP/s, 47 % of
+// the measured bf16 rate; per tile of a pair 1.52 us, against 0.73 us of its products alone
 // (1,416 cycles: 36 of 25 for QK, which its shared-memory reads bound, and 8 of 64 for PV).
-// What bounds it is the work around them: 6,300 warp instructions per tile and SM (0.55 a
+// What bounds it is the work around them: 6,500 warp instructions per tile and SM (0.54 a
 // cycle and scheduler), two thirds of them the conversion of K and V, and 2,000 shared-memory
 // and L1 wavefronts besides the 1,246 of the products. With the conversions, the softmax or
 // the products cut short one at a time, a tile takes 7 to 14 % less; more converter warps
-// cost more instructions than they hide. One token over 131,072 rows takes 63 us (13 us at
-// the copy rate): 27 tiles a pair of 1.5 us, 12 us before the first and 5 us of merge.
+// cost more instructions than they hide. How the roles' instructions interleave moves every long
+// case by 1 to 3 % and the ragged one by up to 12 %, in either direction, for changes that do
+// nothing else (the order of two waits, a constant). One token over 131,072 rows takes 65 us (13 us
+// at the copy rate): 27 tiles a pair of 1.6 us, 12 us before the first and 5 us of merge.
 #include <cuda_fp8.h>
 #include <math.h>
 
