@@ -20,6 +20,14 @@
  *   hs_read_rows          read cached rows and index keys back as values
  *   hs_chunk_attention    attention of new tokens over every cached row below their limit
  *
+ * and what requests that share a prompt need around them:
+ *
+ *   hs_rotary             rotary positions of queries and keys
+ *   hs_fork_requests      requests that begin with the first positions of other ones
+ *   hs_copy_pages         copy pages, or move them with every table that names them
+ *   hs_get_pages          read the page tables of requests on the device
+ *   hs_prefix_attention   hs_chunk_attention with the rows that requests share read and multiplied once
+ *
  * Conventions
  * - Every call returns an hs_status. No C++ exception crosses the ABI.
  * - Every call opens an NVTX range named after it (inert unless a profiler is
@@ -403,6 +411,151 @@ hs_status hs_chunk_attention(hs_pool* pool, int32_t layer, int32_t n_segments, c
                              const void* d_q, int64_t q_stride_token, int64_t q_stride_head, float sm_scale,
                              void* d_out, int64_t out_stride_token, int64_t out_stride_head, float* d_lse,
                              void* d_work, int64_t work_bytes, hs_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Requests that share a prompt (graph-capturable). As for prefill, these calls wait for the
+ * previous kernel of the stream before they read anything, let no later kernel start before
+ * they end, and need the pool's device to be current; they are not bounded by max_tokens or
+ * max_q_per_req.
+ * ------------------------------------------------------------------------- */
+
+/* How the frequencies of rotary positions are scaled for contexts beyond the trained one. With
+ * d = dims and pair i in [0, d / 2):
+ *  NONE    f_i = theta^(-2 i / d)
+ *  LINEAR  f_i / factor
+ *  THETA   f_i of theta * factor^(d / (d - 2))
+ *  RAMP    f_i (1 - r_i) + f_i / factor r_i, r_i = clamp((i - low) / (high - low), 0, 1), where low
+ *          (rounded down, at least 0) and high (rounded up, at most d - 1) are the pairs that turn
+ *          beta_fast and beta_slow times over original_ctx positions:
+ *          d ln(original_ctx / (2 pi beta)) / (2 ln theta); and rotated values are multiplied by
+ *          1 + magnitude ln(factor). */
+#define HS_ROTARY_NONE 0
+#define HS_ROTARY_LINEAR 1
+#define HS_ROTARY_THETA 2
+#define HS_ROTARY_RAMP 3
+#define HS_ROTARY_MAX_DIMS 256
+#define HS_ROTARY_MAX_HEADS 1024
+#define HS_ROTARY_MAX_PARTS 4
+#define HS_ROTARY_MAX_FREQUENCY 1024.0 /* radians per position */
+
+typedef struct hs_rotary_config {
+  int32_t dims;        /* rotated dims of a head: even, 2..HS_ROTARY_MAX_DIMS */
+  int32_t scaling;     /* HS_ROTARY_NONE .. HS_ROTARY_RAMP */
+  double theta;        /* > 0 (RAMP: > 1) */
+  double factor;       /* > 0; not used by NONE, THETA needs dims > 2 */
+  double original_ctx; /* > 0; these four by RAMP alone */
+  double beta_fast;    /* > 0 */
+  double beta_slow;    /* > 0 */
+  double magnitude;    /* finite; 0: values are not multiplied */
+} hs_rotary_config;
+
+/* The steps of hs_rotary for a scaling (h_steps [dims / 2]) and what rotated values are multiplied
+ * by (1 but for RAMP); or the steps of n frequencies of the caller's own, in radians per position, at
+ * most HS_ROTARY_MAX_FREQUENCY in magnitude. A step is the frequency in 2^-64 turns per position,
+ * mod 2^64. Host arrays; no GPU needed. */
+hs_status hs_rotary_steps(const hs_rotary_config* cfg, uint64_t* h_steps, float* h_magnitude);
+hs_status hs_rotary_steps_of(int32_t n, const double* h_frequencies, uint64_t* h_steps);
+
+/* Which dims of a head are a pair: neighbours (2 i, 2 i + 1), or (i, i + dims / 2). */
+#define HS_ROTARY_PAIRS 0
+#define HS_ROTARY_HALVES 1
+
+/* One tensor to rotate: element (j, h, i) at j * stride_token + h * stride_head + i, i < dims. A part
+ * of a head is rotated by pointing at its first rotated dim; the other dims are not touched.
+ * d_out may be d_in, with the same strides (in place); otherwise the two do not overlap. Strides in
+ * elements, in >= 0, out >= dims, no two output rows overlapping. Any element-aligned address and
+ * stride; with those of all parts, and dims / 2 elements, multiples of 16 bytes the accesses are wide. */
+typedef struct hs_rotary_part {
+  const void* d_in;
+  void* d_out;
+  int64_t in_stride_token, in_stride_head;
+  int64_t out_stride_token, out_stride_head;
+  int32_t heads;   /* 1..HS_ROTARY_MAX_HEADS */
+  int32_t layout;  /* HS_ROTARY_PAIRS or HS_ROTARY_HALVES */
+} hs_rotary_part;
+
+/* Rotary positions of up to HS_ROTARY_MAX_PARTS tensors of the same n_tokens tokens in one launch
+ * (queries, rope of the new rows, index queries and keys): pair i of position p
+ *   (a, b) -> magnitude (a cos w - b sin w, a sin w + b cos w), w = p f_i,
+ * in fp32, rounded once; inverse != 0 turns by -w (the transpose, and with magnitude 1 the inverse).
+ *  d_pos    [n_tokens] int32, any value (negative ones turn backwards).
+ *  d_steps  [dims / 2] from hs_rotary_steps, on the device, 8-byte aligned. The angle is exact to
+ *           2^-33 turns for positions below 2^21, whatever the frequency.
+ *  dtype    of every part: HS_BF16, HS_FP16 or HS_FP32. Values that are not finite, or leave the
+ *           type's range, become what the arithmetic makes of them, and are no error.
+ *  parts    host array, taken by value. No part's output overlaps another part.
+ * n_tokens at most HS_CACHE_MAX_TOKENS. */
+hs_status hs_rotary(hs_pool* pool, int32_t n_tokens, const int32_t* d_pos, int32_t dims, const uint64_t* d_steps,
+                    float magnitude, int32_t inverse, int32_t dtype, int32_t n_parts, const hs_rotary_part* parts,
+                    hs_stream_t stream);
+
+/* Begin n requests with the first positions of other ones: dst_i gets the first len_i positions of
+ * src_i. Pages that these fill are shared: dst_i's tables name the pool page, index page and host
+ * page that src_i's name (placeholders stay placeholders). Of a last, partly filled page the
+ * len_i mod 64 rows of every layer and index keys of every indexer layer are copied into pages of
+ * dst_i's own, d_tail_page[i] and d_tail_idx_page[i] (not used when there is no such page), which
+ * get no host page. Table entries behind them stay as they were.
+ *  d_src, d_dst, d_len, d_tail_page, d_tail_idx_page  [n] int32, n <= max_requests and 65535. d_tail_idx_page may be NULL:
+ *                the last page's index keys and index page are left alone.
+ * A request may be the source of several forks. A fork with a bad id, a length not in
+ * [0, max_ctx], a destination that is named twice or is also a source, a tail page that is named
+ * twice or is the source's own (for either cache), or a source page to copy from that is in
+ * neither place (HS_ERR_HOST_MISSING; an index page: HS_ERR_BAD_ID) is not made at all, and sets
+ * HS_ERR_BAD_ID or that. A last page whose source is a placeholder is copied from its host copy.
+ * The caller empties dst_i's hot buffers first (hs_hot_release), keeps count of who uses a shared
+ * page, and appends to positions from len_i on, which no shared page holds. */
+hs_status hs_fork_requests(hs_pool* pool, int32_t n, const int32_t* d_src, const int32_t* d_dst, const int32_t* d_len,
+                           const int32_t* d_tail_page, const int32_t* d_tail_idx_page, hs_stream_t stream);
+
+/* Most pages of either kind in one hs_copy_pages call. */
+#define HS_COPY_MAX_PAGES 4096
+
+/* Copy pool pages in every layer (d_from[i] -> d_to[i], n of them) and index pages in every indexer
+ * layer (n_idx of them) in one launch. remap != 0 moves them: after the copies every entry of the
+ * block tables, of the index tables and of the hot buffers that names a page d_from[i] names
+ * d_to[i], so that the pool is compacted and the pages d_from are free (row ids that were resolved
+ * before name the old places). One of n and n_idx may be 0, its arrays NULL.
+ * A page may be copied to several places, and moved to one. A copy with an id out of range, to a
+ * page that is named twice as a destination or is also a source (itself included), or with
+ * remap from a page named twice as a source, is not made and sets HS_ERR_BAD_ID. */
+hs_status hs_copy_pages(hs_pool* pool, int32_t n, const int32_t* d_from, const int32_t* d_to, int32_t n_idx,
+                        const int32_t* d_idx_from, const int32_t* d_idx_to, int32_t remap, hs_stream_t stream);
+
+/* Read the tables of n requests on the device: entries [first_page, first_page + n_pages) of
+ * request d_req[i] to row i of the outputs [n, n_pages] (any of them NULL). A bad request sets
+ * HS_ERR_BAD_ID and gets -1. */
+hs_status hs_get_pages(hs_pool* pool, int32_t n, const int32_t* d_req, int32_t first_page, int32_t n_pages,
+                       int32_t* d_block_table, int32_t* d_idx_pages, int64_t* d_host_pages, hs_stream_t stream);
+
+/* Most groups and tokens of one hs_prefix_attention call. */
+#define HS_PREFIX_MAX_GROUPS 2048
+#define HS_PREFIX_MAX_TOKENS 16384
+
+/* Bytes of device workspace that hs_prefix_attention needs on this pool's device for a call of at
+ * most so many tokens, segments and groups: 4,112 a token and head, 40 MB besides. */
+hs_status hs_prefix_workspace(const hs_pool* pool, int32_t n_tokens, int32_t n_segments, int32_t n_groups, int64_t* bytes);
+
+/* hs_chunk_attention for requests that share their first positions: group i is the segments
+ * [d_group_start[i], d_group_start[i + 1]), whose requests hold the same rows at positions
+ * [0, d_group_len[i]) (by sharing the pages, as after hs_fork_requests, or copies of them). The
+ * whole pages of these are read through the table of the group's first segment, once for
+ * 128 / H tokens of the group, whatever segments they are of; each segment reads the rest, up to its
+ * tokens' limits, through its own request's table. The two parts of a token's sums are joined in
+ * fp32. A group of one segment, and segments of no group, share nothing.
+ *  d_group_start  [n_groups + 1] int32, 0 <= start_0, ascending, the last at most n_segments.
+ *  d_group_len    [n_groups] int32, 0 <= len <= max_ctx; tokens may have limits below it.
+ *  A group start out of order or range is clamped, a length out of range counts as 0; both set
+ *  HS_ERR_BAD_ID.
+ *  d_work         at least hs_prefix_workspace bytes for the call's sizes, 16-byte aligned, used as
+ *                 that of hs_chunk_attention.
+ * Everything else, and the outputs but for the order of sums, as hs_chunk_attention; n_tokens at most
+ * HS_PREFIX_MAX_TOKENS. */
+hs_status hs_prefix_attention(hs_pool* pool, int32_t layer, int32_t n_groups, const int32_t* d_group_start,
+                              const int32_t* d_group_len, int32_t n_segments, const int32_t* d_seg_req,
+                              const int32_t* d_seg_start, int32_t n_tokens, const int32_t* d_limit, int32_t dtype,
+                              const void* d_q, int64_t q_stride_token, int64_t q_stride_head, float sm_scale,
+                              void* d_out, int64_t out_stride_token, int64_t out_stride_head, float* d_lse,
+                              void* d_work, int64_t work_bytes, hs_stream_t stream);
 
 /* hs_indexer_topk for callers that cannot allocate device memory. The pages have
  * no counterpart; this is a deployment variant of the call above.

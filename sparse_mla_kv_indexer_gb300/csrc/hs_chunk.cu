@@ -160,6 +160,49 @@ __host__ __device__ inline ChunkWork work_at(void* base, int pairs) {
           reinterpret_cast<float*>(b + work_part_at(pairs))};
 }
 
+// hs_prefix_attention: its blocks are listed by a kernel before (prefix_plan_kernel), since a token can be
+// in two of them, one of the positions its group shares and one of its own. Their sums then go to the
+// workspace when the block is whole, too. Two 16-byte words of a block:
+//   tok0, n_tok, req (-1: a bad request), limit (the largest of the block's tokens, within the pages)
+//   first page, end page, cap (positions from here on are not of this block), cost of the blocks before
+struct PlanBlock {
+  int4 a, b;
+};
+constexpr int CK_NO_CAP = 0x7FFFFFFF;
+struct SharedHead {
+  int n_blocks, cost, per_pair, pad;
+};
+struct SharedWork {
+  SharedHead* head;
+  PlanBlock* blocks;   // [max_blocks]
+  int2* of_token;      // [tokens]: its blocks, of shared positions and of its own; -1: none
+  float2* stats;       // as of ChunkWork
+  float* part;
+  float2* whole_stats; // [2][tokens * heads]: of shared blocks, of the others
+  float* whole;        // [2][tokens * heads][512]
+};
+__host__ __device__ inline int64_t up256(int64_t x) { return (x + 255) / 256 * 256; }
+// Its arrays in a workspace (base null: their offsets; `end`: its bytes).
+__host__ __device__ inline SharedWork shared_at(void* base, int pairs, int64_t tokens, int64_t rows, int64_t max_blocks, int64_t* end) {
+  uint8_t* b = static_cast<uint8_t*>(base);
+  SharedWork w;
+  int64_t at = 0;
+  auto take = [&](int64_t bytes) {
+    const int64_t here = at;
+    at += up256(bytes);
+    return b + here;
+  };
+  w.head = reinterpret_cast<SharedHead*>(take(sizeof(SharedHead)));
+  w.blocks = reinterpret_cast<PlanBlock*>(take(max_blocks * (int64_t)sizeof(PlanBlock)));
+  w.of_token = reinterpret_cast<int2*>(take(tokens * 8));
+  w.stats = reinterpret_cast<float2*>(take(pairs * CK_SLOT_ROWS * 8));
+  w.part = reinterpret_cast<float*>(take(pairs * CK_SLOT_ROWS * 512 * 4));
+  w.whole_stats = reinterpret_cast<float2*>(take(2 * rows * 8));
+  w.whole = reinterpret_cast<float*>(take(2 * rows * 512 * 4));
+  if (end) *end = at;
+  return w;
+}
+
 struct ChunkArgs {
   int layer, n_seg, n_tok, pairs;
   int small;         // at most 32 segments and blocks: one warp plans
@@ -171,12 +214,19 @@ struct ChunkArgs {
   long long o_tok, o_head;
   float* lse;
   void* work;
+  // hs_prefix_attention alone
+  int n_groups, max_blocks;
+  const int32_t *group_start, *group_len;
 };
+__device__ __forceinline__ SharedWork shared_work(const ChunkArgs& A, int heads) {
+  return shared_at(A.work, A.pairs, A.n_tok, (int64_t)A.n_tok * heads, A.max_blocks, nullptr);
+}
 
 // One block's pages [pg0, pg1) of one pair's range, two 16-byte words in the ring:
 //   tok0, n_tok (tokens of the block; -1: no more pieces), req (-1: a bad request, nothing is
 //   read), limit (the largest of the block's tokens)
-//   pg0, pg1, slot (-1: the whole block, else the workspace slot 0 or 1), 0
+//   pg0, pg1, slot (-1: the whole block, else the workspace slot 0 or 1; 2 and 3: a whole block of shared
+//   positions, and of the others of a token that has both), cap (PlanBlock's)
 struct Piece {
   int4 a, b;
   __device__ int tok0() const { return a.x; }
@@ -602,7 +652,30 @@ __device__ Range plan_range_warp(const Dev& D, const ChunkArgs& A, int pair, int
   return r;
 }
 
-template <typename T>
+// SHARED: the blocks are listed in the workspace. This pair's range, by one warp.
+__device__ Range plan_range_listed(const ChunkArgs& A, const SharedWork& W, int pair) {
+  const int lane = threadIdx.x & 31;
+  const SharedHead head = *W.head;
+  Range r = {};
+  r.per_pair = head.per_pair;
+  r.at = pair * head.per_pair;
+  r.n = max(0, min(head.per_pair, head.cost - r.at));
+  if (r.n == 0) return r;
+  // the last block whose cost begins at or before the range's: 32 probes at a time
+  int lo = 0, n = head.n_blocks;
+  while (n > 1) {
+    const int step = (n + 31) / 32, probe = lo + lane * step;
+    const bool in = lane * step < n && W.blocks[probe].b.w <= r.at;
+    const int last = 31 - __clz(__ballot_sync(0xffffffffu, in));   // of lane 0 it holds: its block begins at or before
+    n = min(step, n - last * step);
+    lo += last * step;
+  }
+  r.seg = lo;   // here the block
+  r.into = r.at - W.blocks[lo].b.w;
+  return r;
+}
+
+template <typename T, bool SHARED>
 __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const Dev D, const ChunkArgs A) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   // at the same offset in both CTAs: the dynamic shared memory of one kernel starts at one address
@@ -657,7 +730,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
   griddep_launch();   // only the merge of this call depends on it, and waits for its end
 
   Range R = {};
-  if (!A.small) {
+  if (!SHARED && !A.small) {
     R = plan_range(D, A, pair, tpb, smem, found);
     __syncthreads();   // the plan's arrays are done with
   }
@@ -668,7 +741,13 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
     // ------------------------------- pieces of the range -------------------------------
     const uint8_t* const kv = D.kv[A.layer];
     WarpPlan mine = {};
-    if (A.small) R = plan_range_warp(D, A, pair, tpb, mine);
+    SharedWork W = {};
+    if constexpr (SHARED) {
+      W = shared_work(A, H);
+      R = plan_range_listed(A, W, pair);
+    } else {
+      if (A.small) R = plan_range_warp(D, A, pair, tpb, mine);
+    }
     int seg = R.seg, t0 = R.tok0, seg_end = R.seg_t1, into = R.into, left = R.n, at = R.at;
     uint32_t k = 0, t = 0;
     int entries = -1;
@@ -676,7 +755,22 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
     bool ok = true;
     for (;; ++k) {
       int4 pa = make_int4(0, -1, -1, 0), pb = make_int4(0, 0, -1, 0);
-      while (left > 0 && pa.y < 0) {   // the range's next pages: none of a block whose fixed cost it ends in
+      if constexpr (SHARED) {
+        while (left > 0 && pa.y < 0) {
+          const PlanBlock B = W.blocks[seg++];
+          const int pages = B.b.y - B.b.x, end = min(pages > 0 ? CK_BLOCK_COST + pages : 0, into + left);
+          const int p0 = max(into - CK_BLOCK_COST, 0), p1 = max(end - CK_BLOCK_COST, 0);
+          if (p1 > p0) {
+            const bool whole = p0 == 0 && p1 == pages;
+            const int kind = B.b.z != CK_NO_CAP ? 2 : B.b.x > 0 ? 3 : -1;
+            pa = B.a;
+            pb = make_int4(B.b.x + p0, B.b.x + p1, whole ? kind : p0 == 0 ? 1 : 0, B.b.z);
+          }
+          left -= end - into;
+          into = 0;
+        }
+      }
+      while (!SHARED && left > 0 && pa.y < 0) {   // the range's next pages: none of a block whose fixed cost it ends in
         int t1, r, lim;
         if (A.small) {
           t0 = __shfl_sync(0xffffffffu, mine.tok0, seg);
@@ -762,7 +856,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
       }
       if (!ok || pa.y < 0) break;
     }
-    if (lane == 0 && rank == 0) work_at(A.work, A.pairs).cut[pair] = cut;
+    if (!SHARED && lane == 0 && rank == 0) work_at(A.work, A.pairs).cut[pair] = cut;
     } else if (warp == CK_MMA_WARP) {
     // ---------------------------------- MMA issue ----------------------------------
     if (rank == 0) {
@@ -1082,6 +1176,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
       if (live && P.req() >= 0) {
         bool ignore = false;
         lim = clamp_limit(D, __ldg(A.limit + P.tok0() + tk), &ignore);
+        if constexpr (SHARED) lim = min(lim, P.b.w);
       }
       if ((2 * (quad & 1) * 32 + (int)rank) >> hs >= P.n_tok()) {
         // none of these 32 rows is a token's (nor of the other three warps'): their P is 0, and
@@ -1264,9 +1359,21 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
         if (A.lse && live && dim == 0)
           A.lse[(size_t)(P.tok0() + tk) * H + h] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
       } else {
-        const ChunkWork W = work_at(A.work, A.pairs);
-        const size_t at = ((size_t)pair * 2 + P.slot()) * CK_ROWS + gr;
-        float* dst = W.part + at * 512 + dim;
+        float* part;
+        float2* stats;
+        size_t at = ((size_t)pair * 2 + P.slot()) * CK_ROWS + gr;
+        if constexpr (SHARED) {
+          const SharedWork W = shared_work(A, H);
+          const bool whole = P.slot() >= 2;
+          part = whole ? W.whole : W.part;
+          stats = whole ? W.whole_stats : W.stats;
+          if (whole) at = ((size_t)(P.slot() - 2) * A.n_tok + P.tok0()) * H + gr;
+        } else {
+          const ChunkWork W = work_at(A.work, A.pairs);
+          part = W.part;
+          stats = W.stats;
+        }
+        float* dst = part + at * 512 + dim;
 #pragma unroll 1
         for (int c = 0; c < 128; c += 16) {
           uint32_t o[16];
@@ -1278,7 +1385,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
             for (int j = 0; j < 4; ++j) d[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
           }
         }
-        if (live && dim == 0) W.stats[at] = make_float2(m, l);
+        if (live && dim == 0) stats[at] = make_float2(m, l);
       }
       tc_fence_before();   // O may be written again once the next tile's P has arrived
     }
@@ -1390,22 +1497,322 @@ __global__ void __launch_bounds__(CM_THREADS) chunk_merge_kernel(const Dev D, co
   if (A.lse && col == 0) A.lse[(size_t)tok * H + h] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
 
+template <typename T, bool SHARED>
+hs_status launch_attention_pairs(hs_pool* p, const ChunkArgs& a, cudaStream_t st) {
+  if (ensure_kernel_attrs(chunk_attention_kernel<T, SHARED>, CK_SMEM) != HS_OK) return HS_ERR_CUDA;
+  // the register shares were counted against a launch of CK_REGS per thread
+  static std::atomic<int> regs{0};
+  if (regs.load(std::memory_order_relaxed) == 0) {
+    cudaFuncAttributes at;
+    if (cudaFuncGetAttributes(&at, chunk_attention_kernel<T, SHARED>) != cudaSuccess) return HS_ERR_CUDA;
+    regs.store(at.numRegs, std::memory_order_relaxed);
+  }
+  if (regs.load(std::memory_order_relaxed) < CK_REGS) return HS_ERR_CUDA;
+  return launch_pdl(chunk_attention_kernel<T, SHARED>, dim3(2 * a.pairs), dim3(CK_THREADS), CK_SMEM, st, 2, p->d, a);
+}
+
+// ---- requests that share their first positions ------------------------------------------
+// The blocks of hs_prefix_attention. A group's whole shared pages are a unit of all its tokens, whatever
+// segments they are of; the other pages are a unit per segment. Each unit is cut into blocks of 128 / H
+// tokens.
+// When it pays. Reading a group's shared pages once saves the tiles of (sum of ceil(t_i / tpb) - ceil(sum
+// t_i / tpb)) blocks over them (t_i: tokens of its segments, tpb: tokens of a block), and costs each of the
+// shared blocks its queries and its sums once more: PP_JOIN pages. A group that saves less, like long
+// segments of 64 heads whose blocks are full anyway, is read by each segment alone.
+constexpr int PP_THREADS = 1024;
+constexpr int PP_JOIN = 8;
+// shared memory, in ints: starts [n_seg + 1], the shared pages of each segment [n_seg], group starts
+// [n_groups + 1], the segment through whose request each group reads [n_groups], blocks before each unit
+// [n_groups + n_seg + 1]
+inline int plan_ints(int n_seg, int n_groups) { return 3 * n_seg + 3 * n_groups + 3; }
+
+// The ascending values v[0 .. n) clamped to [0, most] and to ascend, into dst. All threads; *bad: some were not.
+__device__ void clamp_starts(int* dst, const int32_t* v, int n, int most, int* tmp, bool* bad) {
+  int before = 0;
+  for (int base = 0; base < n; base += PP_THREADS) {
+    const int i = base + threadIdx.x, s = i < n ? __ldg(v + i) : 0, c = min(max(s, 0), most);
+    int m = c;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, m, o);
+      if (lane >= o) m = max(m, u);
+    }
+    __syncthreads();
+    if (lane == 31) tmp[warp] = m;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) m = max(m, tmp[w]);
+    m = max(m, before);
+    for (int w = 0; w < 32; ++w) before = max(before, tmp[w]);
+    if (i < n) {
+      *bad |= s != m;
+      dst[i] = m;
+    }
+  }
+  __syncthreads();
+}
+// Exclusive sum over the CTA's threads; *total the whole. Barriers on both sides.
+__device__ __forceinline__ int plan_scan(int v, int* tmp, int* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int s = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += u;
+  }
+  __syncthreads();
+  if (lane == 31) tmp[warp] = s;
+  __syncthreads();
+  int w = tmp[lane];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, w, o);
+    if (lane >= o) w += u;
+  }
+  *total = __shfl_sync(0xffffffffu, w, 31);
+  return s - v + (warp > 0 ? __shfl_sync(0xffffffffu, w, warp - 1) : 0);
+}
+
+__global__ void __launch_bounds__(PP_THREADS, 1) prefix_plan_kernel(const Dev D, const ChunkArgs A) {
+  extern __shared__ int plan[];
+  __shared__ int tmp[32];
+  griddep_wait();
+  griddep_launch();   // only the attention of this call depends on it, and waits for its end
+  const int tid = threadIdx.x, tpb = CK_ROWS / D.n_heads, units = A.n_groups + A.n_seg;
+  int* const start = plan;
+  int* const shared = start + A.n_seg + 1;
+  int* const group = shared + A.n_seg;
+  int* const reader = group + A.n_groups + 1;
+  int* const before = reader + A.n_groups;
+  const SharedWork W = shared_work(A, D.n_heads);
+  bool bad = false;
+  for (int j = tid; j < A.n_tok; j += PP_THREADS) W.of_token[j] = make_int2(-1, -1);
+  for (int i = tid; i < A.n_seg; i += PP_THREADS) shared[i] = 0;
+  clamp_starts(start, A.seg_start, A.n_seg + 1, A.n_tok, tmp, &bad);
+  if (A.n_groups > 0) clamp_starts(group, A.group_start, A.n_groups + 1, A.n_seg, tmp, &bad);
+  auto blocks_of = [&](int tokens) { return (tokens + tpb - 1) / tpb; };
+  // the groups that share, a warp each
+  for (int g = tid >> 5; g < A.n_groups; g += PP_THREADS / 32) {
+    const int lane = tid & 31, s0 = group[g], s1 = group[g + 1], len = __ldg(A.group_len + g);
+    const bool fits = len >= 0 && len <= D.max_ctx;
+    bad |= !fits;
+    int alone = 0, first = A.n_seg;
+    bool valid = true;   // a segment of a bad request sees nothing, and so shares nothing
+    for (int i = s0 + lane; i < s1; i += 32) {
+      const int n = blocks_of(start[i + 1] - start[i]), r = __ldg(A.seg_req + i);
+      alone += n;
+      if (n > 0) first = min(first, i), valid &= r >= 0 && r < D.max_requests;
+    }
+    alone = __reduce_add_sync(0xffffffffu, alone);
+    first = __reduce_min_sync(0xffffffffu, first);
+    valid = __all_sync(0xffffffffu, valid);
+    if (lane == 0) reader[g] = first;
+    const int together = blocks_of(start[s1] - start[s0]), pages = fits && valid ? len / PAGE : 0;
+    const bool pays = (long long)(alone - together) * pages > (long long)together * PP_JOIN;
+    if (lane == 0) before[g] = pays ? together : 0;
+    if (pays)
+      for (int i = s0 + lane; i < s1; i += 32) shared[i] = pages;
+  }
+  for (int i = tid; i < A.n_seg; i += PP_THREADS) before[A.n_groups + i] = blocks_of(start[i + 1] - start[i]);
+  __syncthreads();
+  int n_blocks = 0;
+  for (int base = 0; base < units; base += PP_THREADS) {
+    const int u = base + tid, v = u < units ? before[u] : 0;
+    int sum;
+    const int at = plan_scan(v, tmp, &sum);
+    if (u < units) before[u] = n_blocks + at;
+    n_blocks += sum;
+  }
+  if (tid == 0) before[units] = n_blocks;
+  __syncthreads();
+  int cost = 0;
+  for (int base = 0; base < n_blocks; base += PP_THREADS) {
+    const int b = base + tid;
+    PlanBlock B = {make_int4(0, 0, -1, 0), make_int4(0, 0, CK_NO_CAP, 0)};
+    bool of_group = false;
+    if (b < n_blocks) {
+      int l = 0, h = units;   // the last unit whose first block is <= b (never one without blocks)
+      while (h - l > 1) {
+        const int mid = (l + h) >> 1;
+        if (before[mid] <= b) l = mid; else h = mid;
+      }
+      of_group = l < A.n_groups;
+      const int seg = of_group ? reader[l] : l - A.n_groups, end = start[of_group ? group[l + 1] : seg + 1];
+      const int pages = shared[seg], r = __ldg(A.seg_req + seg);
+      const bool bad_req = r < 0 || r >= D.max_requests;
+      bad |= bad_req;
+      B.a.x = start[seg] + (b - before[l]) * tpb;
+      B.a.y = min(tpb, end - B.a.x);
+      B.a.z = bad_req ? -1 : r;
+      const int lim = block_limit(D, A.limit, B.a.x, B.a.x + B.a.y, &bad);
+      if (of_group) {
+        B.b.y = min(pages, pages_of(lim));
+        B.b.z = pages * PAGE;
+        B.a.w = bad_req ? 0 : min(lim, pages * PAGE);
+      } else {
+        B.b.x = pages;
+        B.b.y = pages > 0 ? max(pages, pages_of(lim)) : pages_of(lim);
+        B.a.w = bad_req ? 0 : lim;
+      }
+    }
+    const int n = B.b.y - B.b.x;
+    int sum;
+    B.b.w = cost + plan_scan(n > 0 ? CK_BLOCK_COST + n : 0, tmp, &sum);
+    cost += sum;
+    if (b < n_blocks) {
+      W.blocks[b] = B;
+      if (n > 0)
+        for (int j = B.a.x; j < B.a.x + B.a.y; ++j) (of_group ? W.of_token[j].x : W.of_token[j].y) = b;
+    }
+  }
+  if (bad) set_status(D.status, HS_ERR_BAD_ID);
+  if (tid == 0) *W.head = {n_blocks, cost, max((cost + A.pairs - 1) / A.pairs, CK_MIN_COST), 0};
+}
+
+// Joins what the blocks of a token left in the workspace, in the order of its blocks and pairs: of a token
+// with two blocks both, of one with a cut block its parts. WIDE (few rows): 512 threads to a row, its parts
+// dealt to four slices; otherwise a slice of 128 to a row.
+template <typename T, bool WIDE>
+__global__ void __launch_bounds__(CM_THREADS) prefix_merge_kernel(const Dev D, const ChunkArgs A) {
+  __shared__ float4 acc[CM_SLICES][128];
+  __shared__ float2 ml[CM_SLICES];
+  griddep_wait();
+  const int tid = threadIdx.x, slice = tid >> 7, col = tid & 127, H = D.n_heads;
+  const long long row = WIDE ? (long long)blockIdx.x : (long long)blockIdx.x * CM_SLICES + slice, rows = (long long)A.n_tok * H;
+  if (row >= rows) return;
+  const int tok = (int)(row / H), h = (int)(row - (long long)tok * H);
+  const SharedWork W = shared_work(A, H);
+  const int2 of = W.of_token[tok];
+  const int per_pair = W.head->per_pair;
+  // its parts: those of the block of shared positions, then those of its own
+  struct Parts {
+    int n, first;       // first: of the pairs that hold a cut block
+    long long at;       // where a whole one is; the row in a cut one's slots
+  };
+  auto parts_of = [&](int b, int kind) {
+    Parts p = {0, -1, 0};
+    if (b < 0) return p;
+    const PlanBlock B = W.blocks[b];
+    const int c = B.b.w + CK_BLOCK_COST, first = c / per_pair, last = (c + B.b.y - B.b.x - 1) / per_pair;
+    p.n = last - first + 1;
+    if (p.n == 1) {
+      p.at = (long long)kind * rows + row;
+    } else {
+      p.first = first;
+      p.at = (long long)(tok - B.a.x) * H + h;
+    }
+    return p;
+  };
+  const Parts x = parts_of(of.x, 0), y = parts_of(of.y, 1);
+  const int n = x.n + y.n;
+  if (n == 0 || (of.x < 0 && y.n == 1 && W.blocks[of.y].b.x == 0)) return;   // of no segment; written by the attention itself
+  const int step = WIDE ? CM_SLICES : 1;
+  float m = -INFINITY, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  constexpr int AHEAD = 4;   // parts whose loads are in flight
+  for (int i = WIDE ? slice : 0; i < n; i += AHEAD * step) {
+    float2 s[AHEAD];
+    float4 v[AHEAD];
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) {
+      const int k = i + u * step;
+      s[u] = make_float2(-INFINITY, 0.f);
+      v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (k >= n) continue;
+      const Parts& p = k < x.n ? x : y;
+      const int j = k < x.n ? k : k - x.n;
+      const bool whole = p.first < 0;
+      const size_t at = whole ? (size_t)p.at : ((size_t)(p.first + j) * 2 + (j == 0 ? 1 : 0)) * CK_ROWS + p.at;
+      s[u] = (whole ? W.whole_stats : W.stats)[at];
+      v[u] = *(reinterpret_cast<const float4*>((whole ? W.whole : W.part) + at * 512) + col);
+    }
+    float mn = m;
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) mn = fmaxf(mn, s[u].x);
+    if (mn == -INFINITY) continue;
+    const float f = exp2f(m - mn);
+    m = mn;
+    l *= f;
+    o.x *= f, o.y *= f, o.z *= f, o.w *= f;
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) {
+      if (s[u].x == -INFINITY) continue;   // what lies there may be anything
+      const float w = exp2f(s[u].x - mn);
+      l += w * s[u].y;
+      o.x += w * v[u].x, o.y += w * v[u].y, o.z += w * v[u].z, o.w += w * v[u].w;
+    }
+  }
+  if (WIDE) {
+    acc[slice][col] = o;
+    if (col == 0) ml[slice] = make_float2(m, l);
+    __syncthreads();
+    if (slice > 0) return;
+    m = fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x));
+    l = 0.f;
+    o = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (m > -INFINITY) {
+#pragma unroll
+      for (int u = 0; u < CM_SLICES; ++u) {
+        const float w = exp2f(ml[u].x - m);
+        const float4 v = acc[u][col];
+        l += w * ml[u].y;
+        o.x += w * v.x, o.y += w * v.y, o.z += w * v.z, o.w += w * v.w;
+      }
+    }
+  }
+  if (only_low(m)) {
+    l = 0.f;
+    if (col == 0) set_status(D.status, HS_ERR_RANGE);
+  }
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  T* op = static_cast<T*>(A.out) + tok * A.o_tok + h * A.o_head + col * 4;
+  *reinterpret_cast<uint2*>(op) = make_uint2(pack2<T>(o.x * inv, o.y * inv), pack2<T>(o.z * inv, o.w * inv));
+  if (A.lse && col == 0) A.lse[row] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+}
+
+int prefix_blocks(int n_tok, int n_seg, int n_groups, int tpb) { return n_seg + n_groups + 2 * (n_tok / tpb) + 1; }
+
+constexpr long long PM_WIDE_ROWS = 4096;
+template <typename T>
+hs_status launch_prefix(hs_pool* p, const ChunkArgs& a, cudaStream_t st) {
+  const int smem = plan_ints(a.n_seg, a.n_groups) * 4;
+  if (ensure_kernel_attrs(prefix_plan_kernel, smem) != HS_OK) return HS_ERR_CUDA;
+  hs_status s = launch_pdl(prefix_plan_kernel, dim3(1), dim3(PP_THREADS), smem, st, 0, p->d, a);
+  if (s == HS_OK) s = launch_attention_pairs<T, true>(p, a, st);
+  if (s != HS_OK) return s;
+  const long long rows = (long long)a.n_tok * p->cfg.n_heads;
+  if (rows <= PM_WIDE_ROWS)
+    return launch_pdl(prefix_merge_kernel<T, true>, dim3((unsigned)rows), dim3(CM_THREADS), 0, st, 0, p->d, a);
+  return launch_pdl(prefix_merge_kernel<T, false>, dim3((unsigned)((rows + CM_SLICES - 1) / CM_SLICES)), dim3(CM_THREADS), 0, st, 0,
+                    p->d, a);
+}
+
 bool stride_ok(int64_t s, int64_t least) { return s >= least && s < (1ll << 40) && s % 8 == 0; }
+
+// The checks that both calls share; need: bytes of workspace.
+hs_status check_attention(hs_pool* p, int32_t layer, int32_t n_seg, const int32_t* d_seg_req, const int32_t* d_seg_start, int32_t n,
+                          int32_t most_tokens, const int32_t* d_limit, int32_t dtype, const void* d_q, int64_t q_tok,
+                          int64_t q_head, float sm_scale, const void* d_out, int64_t o_tok, int64_t o_head, const float* d_lse,
+                          const void* d_work, int64_t work_bytes, int64_t need) {
+  if (!p || layer < 0 || layer >= p->cfg.n_layers || n_seg < 0 || n_seg > HS_CHUNK_MAX_SEGMENTS || n < 0 || n > most_tokens ||
+      (dtype != HS_BF16 && dtype != HS_FP16) || !on_pool_device(p))
+    return HS_ERR_INVALID;
+  if (n == 0 || n_seg == 0) return HS_OK;
+  const auto aligned = [](const void* x) { return x && (reinterpret_cast<uintptr_t>(x) & 15) == 0; };
+  if (!d_seg_req || !d_seg_start || !d_limit || !aligned(d_q) || !aligned(d_out) || !aligned(d_work) || !words_ok(d_seg_req) ||
+      !words_ok(d_seg_start) || !words_ok(d_limit) || !words_ok(d_lse) || work_bytes < need ||
+      !(fabsf(sm_scale) <= CK_MAX_SM_SCALE))
+    return HS_ERR_INVALID;
+  if (!stride_ok(q_tok, 0) || !stride_ok(q_head, 0) || !stride_ok(o_tok, LATENT) || !stride_ok(o_head, LATENT))
+    return HS_ERR_INVALID;
+  return HS_OK;
+}
 
 int chunk_pairs() { return num_sms() / 2 > 0 ? num_sms() / 2 : 1; }
 
 template <typename T>
 hs_status launch_chunk(hs_pool* p, const ChunkArgs& a, cudaStream_t st) {
-  if (ensure_kernel_attrs(chunk_attention_kernel<T>, CK_SMEM) != HS_OK) return HS_ERR_CUDA;
-  // the register shares were counted against a launch of CK_REGS per thread
-  static std::atomic<int> regs{0};
-  if (regs.load(std::memory_order_relaxed) == 0) {
-    cudaFuncAttributes at;
-    if (cudaFuncGetAttributes(&at, chunk_attention_kernel<T>) != cudaSuccess) return HS_ERR_CUDA;
-    regs.store(at.numRegs, std::memory_order_relaxed);
-  }
-  if (regs.load(std::memory_order_relaxed) < CK_REGS) return HS_ERR_CUDA;
-  const hs_status s = launch_pdl(chunk_attention_kernel<T>, dim3(2 * a.pairs), dim3(CK_THREADS), CK_SMEM, st, 2, p->d, a);
+  const hs_status s = launch_attention_pairs<T, false>(p, a, st);
   if (s != HS_OK) return s;
   // a pair has at most one cut, and there are no more cuts than blocks
   const int tpb = CK_ROWS / p->cfg.n_heads;
@@ -1437,24 +1844,59 @@ extern "C" hs_status hs_chunk_attention(hs_pool* p, int32_t layer, int32_t n_seg
                                         int64_t o_tok, int64_t o_head, float* d_lse, void* d_work, int64_t work_bytes,
                                         hs_stream_t stream) {
   CallRange nvtx_range("hs_chunk_attention");
-  if (!p || layer < 0 || layer >= p->cfg.n_layers || n_seg < 0 || n_seg > HS_CHUNK_MAX_SEGMENTS || n < 0 ||
-      n > HS_CHUNK_MAX_TOKENS || (dtype != HS_BF16 && dtype != HS_FP16) || !on_pool_device(p))
-    return HS_ERR_INVALID;
   const int pairs = chunk_pairs();
-  if (n > 0 && n_seg > 0) {
-    const auto aligned = [](const void* x) { return x && (reinterpret_cast<uintptr_t>(x) & 15) == 0; };
-    if (!d_seg_req || !d_seg_start || !d_limit || !aligned(d_q) || !aligned(d_out) || !aligned(d_work) ||
-        !words_ok(d_seg_req) || !words_ok(d_seg_start) || !words_ok(d_limit) || !words_ok(d_lse) ||
-        work_bytes < work_bytes_for(pairs) || !(fabsf(sm_scale) <= CK_MAX_SM_SCALE))
-      return HS_ERR_INVALID;
-    if (!stride_ok(q_tok, 0) || !stride_ok(q_head, 0) || !stride_ok(o_tok, LATENT) || !stride_ok(o_head, LATENT))
-      return HS_ERR_INVALID;
-  }
+  const hs_status s = check_attention(p, layer, n_seg, d_seg_req, d_seg_start, n, HS_CHUNK_MAX_TOKENS, d_limit, dtype, d_q, q_tok,
+                                      q_head, sm_scale, d_out, o_tok, o_head, d_lse, d_work, work_bytes, work_bytes_for(pairs));
+  if (s != HS_OK) return s;
   p->settled_rows = nullptr;
   if (n == 0 || n_seg == 0) return HS_OK;
   const int small = n_seg + n / (CK_ROWS / p->cfg.n_heads) <= 32;
   const ChunkArgs a = {layer, n_seg, n, pairs, small, d_seg_req, d_seg_start, d_limit, d_q, q_tok, q_head, sm_scale * CK_LOG2E,
-                       d_out, o_tok, o_head, d_lse, d_work};
+                       d_out, o_tok, o_head, d_lse, d_work, 0, 0, nullptr, nullptr};
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   return dtype == HS_BF16 ? launch_chunk<__nv_bfloat16>(p, a, st) : launch_chunk<__half>(p, a, st);
+}
+
+namespace {
+int64_t prefix_bytes(const hs_pool* p, int n_tok, int n_seg, int n_groups, int* max_blocks) {
+  const int heads = p->cfg.n_heads, blocks = prefix_blocks(n_tok, n_seg, n_groups, CK_ROWS / heads);
+  int64_t end = 0;
+  shared_at(nullptr, chunk_pairs(), n_tok, (int64_t)n_tok * heads, blocks, &end);
+  if (max_blocks) *max_blocks = blocks;
+  return end;
+}
+bool prefix_sizes_ok(int32_t n_tok, int32_t n_seg, int32_t n_groups) {
+  return n_tok >= 0 && n_tok <= HS_PREFIX_MAX_TOKENS && n_seg >= 0 && n_seg <= HS_CHUNK_MAX_SEGMENTS && n_groups >= 0 &&
+         n_groups <= HS_PREFIX_MAX_GROUPS;
+}
+}  // namespace
+
+extern "C" hs_status hs_prefix_workspace(const hs_pool* p, int32_t n_tok, int32_t n_seg, int32_t n_groups, int64_t* bytes) {
+  if (!p || !bytes || !prefix_sizes_ok(n_tok, n_seg, n_groups) || !on_pool_device(p)) return HS_ERR_INVALID;
+  *bytes = prefix_bytes(p, n_tok, n_seg, n_groups, nullptr);
+  return HS_OK;
+}
+
+extern "C" hs_status hs_prefix_attention(hs_pool* p, int32_t layer, int32_t n_groups, const int32_t* d_group_start,
+                                         const int32_t* d_group_len, int32_t n_seg, const int32_t* d_seg_req,
+                                         const int32_t* d_seg_start, int32_t n, const int32_t* d_limit, int32_t dtype,
+                                         const void* d_q, int64_t q_tok, int64_t q_head, float sm_scale, void* d_out,
+                                         int64_t o_tok, int64_t o_head, float* d_lse, void* d_work, int64_t work_bytes,
+                                         hs_stream_t stream) {
+  CallRange nvtx_range("hs_prefix_attention");
+  if (!p || !prefix_sizes_ok(n, n_seg, n_groups)) return HS_ERR_INVALID;
+  int max_blocks = 0;
+  const int64_t need = prefix_bytes(p, n, n_seg, n_groups, &max_blocks);
+  const hs_status s = check_attention(p, layer, n_seg, d_seg_req, d_seg_start, n, HS_PREFIX_MAX_TOKENS, d_limit, dtype, d_q, q_tok,
+                                      q_head, sm_scale, d_out, o_tok, o_head, d_lse, d_work, work_bytes, need);
+  if (s != HS_OK) return s;
+  if (n > 0 && n_seg > 0 && n_groups > 0 &&
+      (!d_group_start || !d_group_len || !words_ok(d_group_start) || !words_ok(d_group_len)))
+    return HS_ERR_INVALID;
+  p->settled_rows = nullptr;
+  if (n == 0 || n_seg == 0) return HS_OK;
+  const ChunkArgs a = {layer, n_seg, n, chunk_pairs(), 0, d_seg_req, d_seg_start, d_limit, d_q, q_tok, q_head, sm_scale * CK_LOG2E,
+                       d_out, o_tok, o_head, d_lse, d_work, n_groups, max_blocks, d_group_start, d_group_len};
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  return dtype == HS_BF16 ? launch_prefix<__nv_bfloat16>(p, a, st) : launch_prefix<__half>(p, a, st);
 }

@@ -1,0 +1,346 @@
+// Pages that requests share: forks of a request, copies and moves of pages, and the tables read back.
+//
+// "vLLM introduces Hybrid HiSparse hybrid sparse offloading for GLM 5.3" (vLLM blog Part 1), section
+// "How it works": the block table holds real blocks and empty placeholders, and hot-buffer pages come
+// from the same pool. So a request can begin with another one's pages by naming them, and a page can go
+// anywhere in the pool as long as every table that names it follows.
+//
+// All of it is copying: bytes read once and written once bound the large calls, launches the small ones.
+#include <math.h>
+
+#include "hs_chunk.cuh"
+
+namespace hs {
+
+namespace {
+
+constexpr int KV_CHUNKS = PAGE * ROW / 16;        // 2,624 16-byte chunks of a page of one layer
+
+// ---- forks ----------------------------------------------------------------------------
+// A fork is several CTAs: of its table entries, of its last page's rows in each layer, of its index keys
+// in each indexer layer. Each finds for itself whether the fork may be made: no fork writes what decides
+// that (a destination is nobody's source).
+constexpr int FK_THREADS = 256;
+constexpr int FK_ENTRIES = 4;                      // table entries of a thread
+struct ForkArgs {
+  int n, table_ctas;
+  const int32_t *src, *dst, *len, *tail, *idx_tail;
+};
+
+__global__ void __launch_bounds__(FK_THREADS) fork_kernel(const Dev D, const ForkArgs A) {
+  griddep_wait();
+  const int i = blockIdx.y, tid = threadIdx.x;
+  const int src = A.src[i], dst = A.dst[i], len = A.len[i];
+  const int tail = A.tail[i], idx_tail = A.idx_tail ? A.idx_tail[i] : -1;
+  const int whole = len >> 6, rows = len & 63;
+  bool bad = false;
+  for (int j = tid; j < A.n; j += FK_THREADS) {
+    const bool other = j != i, uses = rows && (A.len[j] & 63);
+    bad |= A.src[j] == dst || (other && A.dst[j] == dst);
+    bad |= other && uses && (A.tail[j] == tail || (A.idx_tail && A.idx_tail[j] == idx_tail));
+  }
+  if (src < 0 || src >= D.max_requests || dst < 0 || dst >= D.max_requests || len < 0 || len > D.max_ctx) bad = true;
+  const uint8_t* page = nullptr;    // of the CTA's layer
+  int from_idx = -1, err = HS_OK;
+  const int piece = blockIdx.x - A.table_ctas;     // < 0: table entries; then layers, then indexer layers
+  if (!bad && rows) {
+    const size_t at = (size_t)src * D.max_pages + whole;
+    page = page_rows(D, piece >= 0 && piece < D.n_layers ? piece : 0, src, whole, &err);
+    bad |= tail < 0 || tail >= D.num_pages || D.bt[at] == tail;
+    if (A.idx_tail) {
+      from_idx = D.idx_bt[at];
+      bad |= idx_tail < 0 || idx_tail >= D.num_idx_pages || from_idx < 0 || from_idx >= D.num_idx_pages || from_idx == idx_tail;
+    }
+    if (bad) err = HS_ERR_BAD_ID;
+  }
+  const int any = __syncthreads_or(bad);
+  if (any || err != HS_OK) {
+    if (blockIdx.x == 0 && tid == 0) set_status(D.status, any ? HS_ERR_BAD_ID : err);
+    return;
+  }
+  if (piece < 0) {
+    const size_t from = (size_t)src * D.max_pages, to = (size_t)dst * D.max_pages;
+    const int first = blockIdx.x * FK_THREADS * FK_ENTRIES + tid;
+    int32_t b[FK_ENTRIES], x[FK_ENTRIES];
+    int64_t h[FK_ENTRIES];
+#pragma unroll
+    for (int k = 0; k < FK_ENTRIES; ++k) {
+      const int e = first + k * FK_THREADS;
+      if (e < whole) b[k] = D.bt[from + e], x[k] = D.idx_bt[from + e], h[k] = D.host_pg[from + e];
+    }
+#pragma unroll
+    for (int k = 0; k < FK_ENTRIES; ++k) {
+      const int e = first + k * FK_THREADS;
+      if (e < whole) D.bt[to + e] = b[k], D.idx_bt[to + e] = x[k], D.host_pg[to + e] = h[k];
+    }
+    if (blockIdx.x == 0 && tid == 0 && rows) {
+      D.bt[to + whole] = tail;
+      D.host_pg[to + whole] = -1;
+      if (A.idx_tail) D.idx_bt[to + whole] = idx_tail;
+    }
+    // a later kernel may read the tables before it waits for this one's end (which it starts after)
+    __threadfence();
+  } else if (rows) {
+    const bool kv = piece < D.n_layers;
+    const uint4* from;
+    uint4* to;
+    int chunks;
+    if (kv) {
+      from = reinterpret_cast<const uint4*>(page);
+      to = reinterpret_cast<uint4*>(D.kv[piece] + (size_t)tail * PAGE * ROW);
+      chunks = rows * ROW_CHUNKS;
+    } else {
+      if (!A.idx_tail) return;
+      int8_t* keys = D.idx[piece - D.n_layers];
+      from = reinterpret_cast<const uint4*>(keys + (size_t)from_idx * D.idx_page_bytes);
+      to = reinterpret_cast<uint4*>(keys + (size_t)idx_tail * D.idx_page_bytes);
+      chunks = rows * (IDX_DIM / 16);
+      if (D.idx_fmt == HS_IDX_FP8 && tid < rows)   // the keys' scales, behind the page's keys
+        reinterpret_cast<uint32_t*>(to)[PAGE * IDX_DIM / 4 + tid] =
+            reinterpret_cast<const uint32_t*>(from)[PAGE * IDX_DIM / 4 + tid];
+    }
+    constexpr int AHEAD = 11;   // of 63 x 41 chunks, 256 threads: all in flight at once
+    uint4 v[AHEAD];
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k)
+      if (tid + k * FK_THREADS < chunks) v[k] = from[tid + k * FK_THREADS];
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k)
+      if (tid + k * FK_THREADS < chunks) to[tid + k * FK_THREADS] = v[k];
+    static_assert(63 * ROW_CHUNKS <= AHEAD * FK_THREADS, "chunks of a last page");
+  }
+}
+
+// ---- copies and moves -----------------------------------------------------------------
+// Which copies are made. Every CTA builds a table of the pages that the call names in shared memory (open
+// addressing, at most 3 of 4 slots in use): how often each is a destination and a source, and where it
+// goes. That takes the place of an array of all pages that would have to be cleared again.
+constexpr int CP_THREADS = 512, CP_WARPS = CP_THREADS / 32;
+constexpr uint32_t CP_EMPTY = 0xFFFFFFFFu;
+constexpr int CP_SOURCE = 1 << 13;                  // one more as a source (counts up to 4,096 in 13 bits)
+static_assert(HS_COPY_MAX_PAGES < CP_SOURCE, "counts");
+
+struct Named {
+  uint32_t* key;     // page, CP_EMPTY
+  uint32_t* count;
+  int32_t* to;       // for remap: where the page goes
+  uint32_t mask;
+};
+__device__ __forceinline__ uint32_t slot_hash(uint32_t page) { return page * 2654435761u >> 12; }
+__device__ __forceinline__ void name_page(const Named& t, uint32_t page, uint32_t add, int to) {
+  uint32_t s = slot_hash(page) & t.mask;
+  for (;;) {   // ends: a quarter of the slots stay empty
+    const uint32_t was = atomicCAS(t.key + s, CP_EMPTY, page);
+    if (was == CP_EMPTY || was == page) break;
+    s = (s + 1) & t.mask;
+  }
+  atomicAdd(t.count + s, add);
+  if (add == CP_SOURCE && t.to) t.to[s] = to;
+}
+__device__ __forceinline__ int find_page(const Named& t, uint32_t page) {   // its slot, or -1
+  uint32_t s = slot_hash(page) & t.mask;
+  for (;;) {
+    const uint32_t k = t.key[s];
+    if (k == page) return (int)s;
+    if (k == CP_EMPTY) return -1;
+    s = (s + 1) & t.mask;
+  }
+}
+// All threads of the CTA. Pages out of range are not named (a copy from or to one is not made).
+__device__ void name_pages(const Named& t, int n, const int32_t* from, const int32_t* to, int pages) {
+  for (uint32_t s = threadIdx.x; s <= t.mask; s += blockDim.x) t.key[s] = CP_EMPTY, t.count[s] = 0;
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += blockDim.x) {
+    const int f = from[i], d = to[i];
+    if (f >= 0 && f < pages) name_page(t, (uint32_t)f, CP_SOURCE, d);
+    if (d >= 0 && d < pages) name_page(t, (uint32_t)d, 1, 0);
+  }
+  __syncthreads();
+}
+__device__ __forceinline__ bool copy_made(const Named& t, int f, int d, int pages, bool remap) {
+  if (f < 0 || f >= pages || d < 0 || d >= pages) return false;
+  if (t.count[find_page(t, (uint32_t)d)] != 1) return false;   // another destination, or a source
+  return !remap || (t.count[find_page(t, (uint32_t)f)] & ~(CP_SOURCE - 1)) == CP_SOURCE;
+}
+
+struct CopyList {
+  int n, pages;               // copies; pages of this kind in the pool
+  const int32_t *from, *to;
+};
+struct CopyArgs {
+  CopyList kv, idx;
+  int kv_ctas, remap;         // the first kv_ctas CTAs copy KV pages, the others index pages
+  uint32_t kv_mask, idx_mask; // slots - 1
+};
+__host__ __device__ inline uint32_t slots_for(int n) {
+  uint32_t s = 64;
+  while (3 * s < 8u * (uint32_t)n) s *= 2;
+  return s;
+}
+
+// A warp's unit is 1/8 of a page of one layer (5,248 bytes) or 1/2 of an index page of one indexer layer,
+// all of its loads in flight at once.
+constexpr int CP_KV_SLICES = 8, CP_IDX_SLICES = 2, CP_AHEAD = 11;
+static_assert(KV_CHUNKS / CP_KV_SLICES <= 32 * CP_AHEAD && HS_IDX_FP8_PAGE_BYTES / 16 / CP_IDX_SLICES <= 32 * CP_AHEAD, "unit");
+__global__ void __launch_bounds__(CP_THREADS, 2) copy_pages_kernel(const Dev D, const CopyArgs A) {
+  extern __shared__ uint32_t slots[];
+  griddep_wait();
+  const bool kv = (int)blockIdx.x < A.kv_ctas;
+  const CopyList L = kv ? A.kv : A.idx;
+  const uint32_t mask = kv ? A.kv_mask : A.idx_mask;
+  const Named t = {slots, slots + mask + 1, nullptr, mask};
+  name_pages(t, L.n, L.from, L.to, L.pages);
+  const int lane = threadIdx.x & 31, cta = kv ? blockIdx.x : blockIdx.x - A.kv_ctas, ctas = kv ? A.kv_ctas : gridDim.x - A.kv_ctas;
+  const int layers = kv ? D.n_layers : D.n_groups, slices = kv ? CP_KV_SLICES : CP_IDX_SLICES;
+  const int page_bytes = kv ? PAGE * ROW : D.idx_page_bytes, chunks = page_bytes / 16 / slices;
+  const int per_page = layers * slices;
+  const long long units = (long long)L.n * per_page;
+  for (long long u = (long long)cta * CP_WARPS + (threadIdx.x >> 5); u < units; u += (long long)ctas * CP_WARPS) {
+    const int i = (int)(u / per_page), r = (int)(u - (long long)i * per_page), layer = r / slices, slice = r - layer * slices;
+    const int f = L.from[i], d = L.to[i];
+    if (!copy_made(t, f, d, L.pages, A.remap)) {
+      if (lane == 0) set_status(D.status, HS_ERR_BAD_ID);
+      continue;
+    }
+    uint8_t* const pages = kv ? D.kv[layer] : reinterpret_cast<uint8_t*>(D.idx[layer]);
+    const uint4* const from = reinterpret_cast<const uint4*>(pages + (size_t)f * page_bytes) + slice * chunks;
+    uint4* const to = reinterpret_cast<uint4*>(pages + (size_t)d * page_bytes) + slice * chunks;
+    uint4 v[CP_AHEAD];
+#pragma unroll
+    for (int k = 0; k < CP_AHEAD; ++k)
+      if (lane + 32 * k < chunks) v[k] = from[lane + 32 * k];
+#pragma unroll
+    for (int k = 0; k < CP_AHEAD; ++k)
+      if (lane + 32 * k < chunks) to[lane + 32 * k] = v[k];
+  }
+}
+
+// Every table entry that names a moved page, after the copies: the same table in shared memory, with where
+// each page goes.
+constexpr int RM_ENTRIES = 8;      // of a thread at a time
+__global__ void __launch_bounds__(CP_THREADS) remap_kernel(const Dev D, const CopyArgs A) {
+  extern __shared__ uint32_t slots[];
+  griddep_wait();
+  const long long per_table = (long long)D.max_requests * D.max_pages;
+#pragma unroll 1
+  for (int kind = 0; kind < 2; ++kind) {
+    const CopyList L = kind == 0 ? A.kv : A.idx;
+    if (L.n == 0) continue;
+    const uint32_t mask = kind == 0 ? A.kv_mask : A.idx_mask;
+    const Named t = {slots, slots + mask + 1, reinterpret_cast<int32_t*>(slots + 2 * (mask + 1)), mask};
+    __syncthreads();
+    name_pages(t, L.n, L.from, L.to, L.pages);
+#pragma unroll 1
+    for (int table = 0; table < (kind == 0 ? 2 : 1); ++table) {
+      int32_t* const entries = kind == 1 ? D.idx_bt : table == 0 ? D.bt : D.hot_pages;
+      const long long n = table == 0 ? per_table : (long long)D.max_requests * D.n_groups * D.hot_pages_max;
+      const long long stride = (long long)gridDim.x * CP_THREADS;
+      for (long long e0 = (long long)blockIdx.x * CP_THREADS + threadIdx.x; e0 < n; e0 += RM_ENTRIES * stride) {
+        int32_t v[RM_ENTRIES];
+#pragma unroll
+        for (int k = 0; k < RM_ENTRIES; ++k) v[k] = e0 + k * stride < n ? entries[e0 + k * stride] : -1;
+#pragma unroll
+        for (int k = 0; k < RM_ENTRIES; ++k) {
+          if (v[k] < 0) continue;
+          const int s = find_page(t, (uint32_t)v[k]);
+          if (s < 0 || t.count[s] < CP_SOURCE) continue;
+          const int to = t.to[s];
+          if (copy_made(t, v[k], to, L.pages, true)) entries[e0 + k * stride] = to;
+        }
+      }
+    }
+  }
+  __threadfence();   // as the forks'
+}
+
+// ---- the tables -----------------------------------------------------------------------
+__global__ void __launch_bounds__(256) get_pages_kernel(const Dev D, int n, const int32_t* __restrict__ req, int first, int count,
+                                                        int32_t* bt, int32_t* idx, int64_t* host) {
+  griddep_wait();
+  const long long total = (long long)n * count, stride = (long long)gridDim.x * blockDim.x;
+  for (long long e = (long long)blockIdx.x * blockDim.x + threadIdx.x; e < total; e += stride) {
+    const int i = (int)(e / count), r = req[i];
+    const bool ok = r >= 0 && r < D.max_requests;
+    if (!ok) set_status(D.status, HS_ERR_BAD_ID);
+    const size_t at = (size_t)(ok ? r : 0) * D.max_pages + first + (e - (long long)i * count);
+    if (bt) bt[e] = ok ? D.bt[at] : -1;
+    if (idx) idx[e] = ok ? D.idx_bt[at] : -1;
+    if (host) host[e] = ok ? D.host_pg[at] : -1;
+  }
+}
+
+}  // namespace
+
+}  // namespace hs
+
+using namespace hs;
+
+extern "C" hs_status hs_fork_requests(hs_pool* p, int32_t n, const int32_t* d_src, const int32_t* d_dst, const int32_t* d_len,
+                                      const int32_t* d_tail, const int32_t* d_idx_tail, hs_stream_t stream) {
+  CallRange nvtx_range("hs_fork_requests");
+  if (!p || n < 0 || n > p->cfg.max_requests || !on_pool_device(p)) return HS_ERR_INVALID;
+  if (n > 0 && (!d_src || !d_dst || !d_len || !d_tail || !words_ok(d_src) || !words_ok(d_dst) || !words_ok(d_len) ||
+                !words_ok(d_tail) || !words_ok(d_idx_tail)))
+    return HS_ERR_INVALID;
+  p->settled_rows = nullptr;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const int table_ctas = (p->d.max_pages + FK_THREADS * FK_ENTRIES - 1) / (FK_THREADS * FK_ENTRIES);
+  if (n == 0) return HS_OK;
+  if (n > 65535) return HS_ERR_INVALID;   // the grid's second dimension
+  const ForkArgs a = {n, table_ctas, d_src, d_dst, d_len, d_tail, d_idx_tail};
+  return launch_pdl(fork_kernel, dim3(table_ctas + p->d.n_layers + p->d.n_groups, n), dim3(FK_THREADS), 0, st, 0, p->d, a);
+}
+
+extern "C" hs_status hs_copy_pages(hs_pool* p, int32_t n, const int32_t* d_from, const int32_t* d_to, int32_t n_idx,
+                                   const int32_t* d_idx_from, const int32_t* d_idx_to, int32_t remap, hs_stream_t stream) {
+  CallRange nvtx_range("hs_copy_pages");
+  if (!p || n < 0 || n > HS_COPY_MAX_PAGES || n_idx < 0 || n_idx > HS_COPY_MAX_PAGES || !on_pool_device(p)) return HS_ERR_INVALID;
+  if (n > 0 && (!d_from || !d_to || !words_ok(d_from) || !words_ok(d_to))) return HS_ERR_INVALID;
+  if (n_idx > 0 && (!d_idx_from || !d_idx_to || !words_ok(d_idx_from) || !words_ok(d_idx_to))) return HS_ERR_INVALID;
+  p->settled_rows = nullptr;
+  if (n == 0 && n_idx == 0) return HS_OK;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  CopyArgs a = {};
+  a.kv = {n, p->cfg.num_pages, d_from, d_to};
+  a.idx = {n_idx, p->cfg.num_idx_pages, d_idx_from, d_idx_to};
+  a.kv_mask = slots_for(n) - 1;
+  a.idx_mask = slots_for(n_idx) - 1;
+  a.remap = remap != 0;
+  const int slots = (int)((a.kv_mask > a.idx_mask ? a.kv_mask : a.idx_mask) + 1), smem = slots * 8;
+  // CTAs for both kinds by their bytes, as many as are resident at once
+  const long long kv_units = (long long)n * p->d.n_layers * CP_KV_SLICES, idx_units = (long long)n_idx * p->d.n_groups * CP_IDX_SLICES;
+  const long long kv_bytes = (long long)n * p->d.n_layers * PAGE * ROW, idx_bytes = (long long)n_idx * p->d.n_groups * p->d.idx_page_bytes;
+  const int most = num_sms() * (smem > 110 * 1024 ? 1 : 2);
+  const auto ctas_for = [&](long long units, long long bytes) -> int {
+    if (units == 0) return 0;
+    const long long share = (long long)((double)most * bytes / (kv_bytes + idx_bytes)), need = (units + CP_WARPS - 1) / CP_WARPS;
+    const long long c = share < 1 ? 1 : share;
+    return (int)(c < need ? c : need);
+  };
+  a.kv_ctas = ctas_for(kv_units, kv_bytes);
+  const int ctas = a.kv_ctas + ctas_for(idx_units, idx_bytes);
+  if (ensure_kernel_attrs(copy_pages_kernel, smem) != HS_OK) return HS_ERR_CUDA;
+  hs_status s = launch_pdl(copy_pages_kernel, dim3(ctas), dim3(CP_THREADS), smem, st, 0, p->d, a);
+  if (s != HS_OK || !remap) return s;
+  const int smem_remap = slots * 12;
+  if (ensure_kernel_attrs(remap_kernel, smem_remap) != HS_OK) return HS_ERR_CUDA;
+  const long long entries = (long long)p->cfg.max_requests * p->d.max_pages, need = (entries + CP_THREADS * RM_ENTRIES - 1) / (CP_THREADS * RM_ENTRIES);
+  const int grid = (int)(need < num_sms() ? need : num_sms());
+  return launch_pdl(remap_kernel, dim3(grid), dim3(CP_THREADS), smem_remap, st, 0, p->d, a);
+}
+
+extern "C" hs_status hs_get_pages(hs_pool* p, int32_t n, const int32_t* d_req, int32_t first, int32_t count, int32_t* d_bt,
+                                  int32_t* d_idx, int64_t* d_host, hs_stream_t stream) {
+  CallRange nvtx_range("hs_get_pages");
+  if (!p || n < 0 || first < 0 || count < 0 || (long long)first + count > p->d.max_pages || n > HS_CACHE_MAX_TOKENS ||
+      !on_pool_device(p))
+    return HS_ERR_INVALID;
+  if (n > 0 && count > 0 && (!d_req || !words_ok(d_req) || !words_ok(d_bt) || !words_ok(d_idx) ||
+                             (reinterpret_cast<uintptr_t>(d_host) & 7)))
+    return HS_ERR_INVALID;
+  p->settled_rows = nullptr;
+  if (n == 0 || count == 0 || (!d_bt && !d_idx && !d_host)) return HS_OK;
+  const long long need = ((long long)n * count + 255) / 256, most = (long long)num_sms() * 8;
+  return launch_pdl(get_pages_kernel, dim3((unsigned)(need < most ? need : most)), dim3(256), 0,
+                    reinterpret_cast<cudaStream_t>(stream), 0, p->d, n, d_req, first, count, d_bt, d_idx, d_host);
+}

@@ -53,6 +53,23 @@ BF16, FP16, FP32 = 0, 1, 2   # HS_BF16, HS_FP16, HS_FP32
 CACHE_MAX_TOKENS = 1 << 24   # HS_CACHE_MAX_TOKENS
 CHUNK_MAX_SEGMENTS = 4096    # HS_CHUNK_MAX_SEGMENTS
 CHUNK_MAX_TOKENS = 65536     # HS_CHUNK_MAX_TOKENS
+COPY_MAX_PAGES = 4096        # HS_COPY_MAX_PAGES
+PREFIX_MAX_GROUPS, PREFIX_MAX_TOKENS = 2048, 16384   # HS_PREFIX_MAX_*
+ROTARY_MAX_DIMS, ROTARY_MAX_HEADS, ROTARY_MAX_PARTS = 256, 1024, 4   # HS_ROTARY_MAX_*
+ROTARY_LAYOUTS = {"pairs": 0, "halves": 1}                        # HS_ROTARY_PAIRS, HS_ROTARY_HALVES
+ROTARY_SCALINGS = {"none": 0, "linear": 1, "theta": 2, "ramp": 3}  # HS_ROTARY_NONE .. HS_ROTARY_RAMP
+
+
+class RotaryConfig(ctypes.Structure):
+    _fields_ = [("dims", ctypes.c_int32), ("scaling", ctypes.c_int32)] + \
+               [(n, ctypes.c_double) for n in ("theta", "factor", "original_ctx", "beta_fast", "beta_slow", "magnitude")]
+
+
+class RotaryPart(ctypes.Structure):
+    _fields_ = [("d_in", ctypes.c_void_p), ("d_out", ctypes.c_void_p)] + \
+               [(n, ctypes.c_int64) for n in ("in_stride_token", "in_stride_head", "out_stride_token", "out_stride_head")] + \
+               [("heads", ctypes.c_int32), ("layout", ctypes.c_int32)]
+
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int32
@@ -76,6 +93,14 @@ _SIGS = {
     "hs_read_rows": [_P, _I, _I, _P, _P, _I, _P, _L, _P, _L, _P, _L, ctypes.c_float, _P],
     "hs_chunk_workspace": [_P, ctypes.POINTER(_L)],
     "hs_chunk_attention": [_P, _I, _I, _P, _P, _I, _P, _I, _P, _L, _L, ctypes.c_float, _P, _L, _L, _P, _P, _L, _P],
+    "hs_rotary_steps": [ctypes.POINTER(RotaryConfig), _P, ctypes.POINTER(ctypes.c_float)],
+    "hs_rotary_steps_of": [_I, _P, _P],
+    "hs_rotary": [_P, _I, _P, _I, _P, ctypes.c_float, _I, _I, _I, ctypes.POINTER(RotaryPart), _P],
+    "hs_fork_requests": [_P, _I, _P, _P, _P, _P, _P, _P],
+    "hs_copy_pages": [_P, _I, _P, _P, _I, _P, _P, _I, _P],
+    "hs_get_pages": [_P, _I, _P, _I, _I, _P, _P, _P, _P],
+    "hs_prefix_workspace": [_P, _I, _I, _I, ctypes.POINTER(_L)],
+    "hs_prefix_attention": [_P, _I, _I, _P, _P, _I, _P, _P, _I, _P, _I, _P, _L, _L, ctypes.c_float, _P, _L, _L, _P, _P, _L, _P],
     "hs_get_error": [_P, ctypes.POINTER(ctypes.c_int), _P],
     "hs_set_select_mode": [_P, _I],
     "hs_select_selftest": [_P, _I, _P, _P, _P],
@@ -140,19 +165,26 @@ class _Torch:
     time for a small call, the host's share of each call counts."""
     codes: dict = {}
     int32 = None
+    int64 = None
+    steps: tuple = ()
     raw_stream = None
 
     @classmethod
     def load(cls) -> None:
         import torch
-        cls.int32 = torch.int32
+        cls.int32, cls.int64 = torch.int32, torch.int64
+        cls.steps = (torch.int64, torch.uint64)
         cls.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         cls.codes = {torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32}
 
+    @classmethod
+    def load_once(cls) -> None:
+        if not cls.codes:
+            cls.load()
+
 
 def _dtype(t) -> int:
-    if not _Torch.codes:
-        _Torch.load()
+    _Torch.load_once()
     code = _Torch.codes.get(t.dtype)
     if code is None:
         raise ValueError(f"element type {t.dtype}: bfloat16, float16 or float32 is wanted")
@@ -189,6 +221,30 @@ def _values(name: str, t, n: int, width: int, dtype, device: int):
     if t.get_device() != device:
         _on(name, t, device)
     return t.data_ptr(), t.stride(0) if n > 1 else width
+
+
+def rotary_steps(dims: int, theta: float, scaling: str = "none", factor: float = 1.0, original_ctx: float = 0.0,
+                 beta_fast: float = 32.0, beta_slow: float = 1.0, magnitude: float = 0.0):
+    """hs_rotary_steps: the steps [dims / 2] of Pool.rotary (an int64 tensor on the host, to be moved to the
+    device once) for a scaling of ROTARY_SCALINGS, and the magnitude to give with them."""
+    import torch
+    if scaling not in ROTARY_SCALINGS:
+        raise ValueError(f"scaling {scaling!r}: one of {', '.join(ROTARY_SCALINGS)} is wanted")
+    cfg = RotaryConfig(dims, ROTARY_SCALINGS[scaling], theta, factor, original_ctx, beta_fast, beta_slow, magnitude)
+    steps, m = torch.empty(max(dims, 0) // 2, dtype=torch.int64), ctypes.c_float(0.0)
+    _check("hs_rotary_steps", lib.hs_rotary_steps(ctypes.byref(cfg), steps.data_ptr(), ctypes.byref(m)))
+    return steps, m.value
+
+
+def rotary_steps_of(frequencies):
+    """hs_rotary_steps_of: the steps of frequencies of one's own, in radians per position."""
+    import torch
+    f = torch.as_tensor(frequencies, dtype=torch.float64, device="cpu").contiguous()
+    if f.dim() != 1:
+        raise ValueError("frequencies: one dimension is wanted")
+    steps = torch.empty(f.numel(), dtype=torch.int64)
+    _check("hs_rotary_steps_of", lib.hs_rotary_steps_of(f.numel(), f.data_ptr(), steps.data_ptr()))
+    return steps
 
 
 def config_ok(cfg: PoolConfig) -> bool:
@@ -330,6 +386,10 @@ class Pool:
         tokens [seg_start[i], seg_start[i + 1]) of request seg_req[i]; limit [n]; q [n, H, 576]
         and out [n, H, 512] bf16 or fp16, the last dimension contiguous; lse [n, H] fp32;
         work: chunk_workspace_bytes() bytes that no overlapping call uses."""
+        _check("hs_chunk_attention", lib.hs_chunk_attention(
+            self.handle, layer, *self._attention_args(seg_req, seg_start, limit, q, sm_scale, out, work, lse, stream)))
+
+    def _attention_args(self, seg_req, seg_start, limit, q, sm_scale, out, work, lse, stream):
         code, n, segs, heads, dev = _dtype(q), limit.shape[0], seg_req.shape[0], self.cfg.n_heads, self._device()
         if q.shape != (n, heads, 576) or out.shape != (n, heads, 512) or out.dtype is not q.dtype:
             raise ValueError(f"q [{n}, {heads}, 576] and out [{n}, {heads}, 512] of one type are wanted")
@@ -343,11 +403,103 @@ class Pool:
         if q.get_device() != dev or out.get_device() != dev or work.get_device() != dev or \
                 (lse is not None and lse.get_device() != dev):
             raise ValueError(f"q, out, lse or work is not on the pool's device, cuda:{dev}")
-        _check("hs_chunk_attention", lib.hs_chunk_attention(
-            self.handle, layer, segs, _ids("seg_req", seg_req, segs, dev), _ids("seg_start", seg_start, segs + 1, dev),
-            n, _ids("limit", limit, n, dev), code, q.data_ptr(), qs[0] if n > 1 else heads * 576, qs[1], sm_scale,
-            out.data_ptr(), os[0] if n > 1 else heads * 512, os[1], None if lse is None else lse.data_ptr(),
-            work.data_ptr(), work.numel() * work.element_size(), _stream_of(stream, dev)))
+        return (segs, _ids("seg_req", seg_req, segs, dev), _ids("seg_start", seg_start, segs + 1, dev),
+                n, _ids("limit", limit, n, dev), code, q.data_ptr(), qs[0] if n > 1 else heads * 576, qs[1], sm_scale,
+                out.data_ptr(), os[0] if n > 1 else heads * 512, os[1], None if lse is None else lse.data_ptr(),
+                work.data_ptr(), work.numel() * work.element_size(), _stream_of(stream, dev))
+
+    # -- requests that share a prompt ---------------------------------------------------
+    def rotary(self, pos, steps, parts, magnitude: float = 1.0, inverse: bool = False, stream=None) -> None:
+        """Rotary positions of up to four tensors of the same tokens in one launch. pos [n] int32; steps
+        [dims / 2] from rotary_steps, on the device; parts: (x, out, layout) with x and out [n, heads, dims]
+        or [n, dims] of one type, views of the rotated dims with a contiguous last one, out x itself for
+        in place; layout "pairs" or "halves". inverse turns backwards (the transpose)."""
+        if not 0 < len(parts) <= ROTARY_MAX_PARTS:
+            raise ValueError(f"1 to {ROTARY_MAX_PARTS} parts are wanted")
+        first = parts[0][0]
+        code, dtype, n, dev = _dtype(first), first.dtype, pos.shape[0], self._device()
+        dims = first.shape[-1]
+        args = (RotaryPart * len(parts))()
+        for a, (x, out, layout) in zip(args, parts):
+            shape, xs, os = x.shape, x.stride(), out.stride()
+            if len(shape) not in (2, 3) or shape[0] != n or shape[-1] != dims or out.shape != shape:
+                raise ValueError(f"x and out [{n}, heads, {dims}] or [{n}, {dims}] of one shape are wanted")
+            if x.dtype is not dtype or out.dtype is not dtype:
+                raise ValueError("all parts of one element type are wanted")
+            if (xs[-1] != 1 or os[-1] != 1) and dims > 1:
+                raise ValueError("x and out: a contiguous last dimension is wanted")
+            if x.get_device() != dev or out.get_device() != dev:
+                raise ValueError(f"x or out is not on the pool's device, cuda:{dev}")
+            if layout not in ROTARY_LAYOUTS:
+                raise ValueError(f"layout {layout!r}: pairs or halves is wanted")
+            heads = shape[1] if len(shape) == 3 else 1
+            a.d_in, a.d_out, a.heads, a.layout = x.data_ptr(), out.data_ptr(), heads, ROTARY_LAYOUTS[layout]
+            a.in_stride_token, a.out_stride_token = (xs[0], os[0]) if n > 1 else (dims, dims)
+            a.in_stride_head, a.out_stride_head = (xs[1], os[1]) if heads > 1 else (dims, dims)
+        if steps.shape != (dims // 2,) or steps.dtype not in _Torch.steps or not steps.is_contiguous():
+            raise ValueError(f"steps: a contiguous int64 tensor of {dims // 2} elements is wanted")
+        _on("steps", steps, dev)
+        _check("hs_rotary", lib.hs_rotary(self.handle, n, _ids("pos", pos, n, dev), dims, steps.data_ptr(), magnitude,
+                                          1 if inverse else 0, code, len(parts), args, _stream_of(stream, dev)))
+
+    def fork_requests(self, src, dst, length, tail_pages, tail_idx_pages=None, stream=None) -> None:
+        """Begin requests dst[i] with the first length[i] positions of src[i]: whole pages shared, the rows of
+        a last, partly filled page copied into tail_pages[i] and tail_idx_pages[i]. All [n] int32 on the device."""
+        n, dev = src.shape[0], self._device()
+        _Torch.load_once()
+        _check("hs_fork_requests", lib.hs_fork_requests(
+            self.handle, n, _ids("src", src, n, dev), _ids("dst", dst, n, dev), _ids("length", length, n, dev),
+            _ids("tail_pages", tail_pages, n, dev),
+            None if tail_idx_pages is None else _ids("tail_idx_pages", tail_idx_pages, n, dev), _stream_of(stream, dev)))
+
+    def copy_pages(self, src=None, dst=None, idx_src=None, idx_dst=None, remap: bool = False, stream=None) -> None:
+        """Copy pool pages src[i] -> dst[i] in every layer and index pages idx_src[i] -> idx_dst[i] in every
+        indexer layer (int32 on the device, either kind may be left out); remap: move them, every table entry
+        that names src[i] naming dst[i] afterwards."""
+        if (src is None) != (dst is None) or (idx_src is None) != (idx_dst is None):
+            raise ValueError("sources and destinations: both or neither are wanted")
+        dev = self._device()
+        _Torch.load_once()
+        n, m = 0 if src is None else src.shape[0], 0 if idx_src is None else idx_src.shape[0]
+        ids = lambda name, t, k: None if t is None else _ids(name, t, k, dev)  # noqa: E731
+        _check("hs_copy_pages", lib.hs_copy_pages(
+            self.handle, n, ids("src", src, n), ids("dst", dst, n), m, ids("idx_src", idx_src, m), ids("idx_dst", idx_dst, m),
+            1 if remap else 0, _stream_of(stream, dev)))
+
+    def prefix_workspace_bytes(self, n_tokens: int, n_segments: int, n_groups: int) -> int:
+        """Bytes of device workspace that prefix_attention needs for a call of at most these sizes."""
+        n = _L(0)
+        _check("hs_prefix_workspace", lib.hs_prefix_workspace(self.handle, n_tokens, n_segments, n_groups, ctypes.byref(n)))
+        return n.value
+
+    def prefix_attention(self, layer: int, group_start, group_len, seg_req, seg_start, limit, q, sm_scale: float, out, work,
+                         lse=None, stream=None) -> None:
+        """chunk_attention for requests that share their first positions: group i is the segments
+        [group_start[i], group_start[i + 1]), whose requests hold the same rows at positions [0, group_len[i]);
+        these are read and multiplied once for the tokens of all of them. work: prefix_workspace_bytes() bytes."""
+        args = self._attention_args(seg_req, seg_start, limit, q, sm_scale, out, work, lse, stream)
+        groups, dev = group_len.shape[0], self._device()
+        _check("hs_prefix_attention", lib.hs_prefix_attention(
+            self.handle, layer, groups, _ids("group_start", group_start, groups + 1, dev),
+            _ids("group_len", group_len, groups, dev), *args))
+
+    def get_pages(self, req, first_page: int, block_table=None, idx_pages=None, host_pages=None, stream=None) -> None:
+        """Read table entries [first_page, first_page + n_pages) of requests req [n] into block_table and
+        idx_pages (int32) and host_pages (int64), each [n, n_pages] on the device, any of them left out."""
+        outs = [t for t in (block_table, idx_pages, host_pages) if t is not None]
+        if not outs:
+            raise ValueError("none of block_table, idx_pages and host_pages is given")
+        n, dev = req.shape[0], self._device()
+        _Torch.load_once()
+        for name, t, dtype in (("block_table", block_table, _Torch.int32), ("idx_pages", idx_pages, _Torch.int32),
+                               ("host_pages", host_pages, _Torch.int64)):
+            if t is None:
+                continue
+            if t.dim() != 2 or t.shape[0] != n or t.shape != outs[0].shape or t.dtype is not dtype or not t.is_contiguous():
+                raise ValueError(f"{name}: a contiguous {dtype} tensor [{n}, pages] is wanted, of one shape with the others")
+            _on(name, t, dev)
+        _check("hs_get_pages", lib.hs_get_pages(self.handle, n, _ids("req", req, n, dev), first_page, outs[0].shape[1],
+                                                _ptr(block_table), _ptr(idx_pages), _ptr(host_pages), _stream_of(stream, dev)))
 
     # -- status --------------------------------------------------------------------
     def get_error(self, stream=None) -> int:
