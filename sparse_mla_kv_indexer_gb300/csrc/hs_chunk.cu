@@ -175,7 +175,7 @@ struct SharedHead {
 struct SharedWork {
   SharedHead* head;
   PlanBlock* blocks;   // [max_blocks]
-  int2* of_token;      // [tokens]: its blocks, of shared positions and of its own; -1: none
+  int2* of_token;      // [tokens]: what is to be joined of its blocks of shared positions, and of its own (ToJoin)
   float2* stats;       // as of ChunkWork
   float* part;
   float2* whole_stats; // [2][tokens * heads]: of shared blocks, of the others
@@ -1573,6 +1573,16 @@ __device__ __forceinline__ int plan_scan(int v, int* tmp, int* total) {
   return s - v + (warp > 0 ? __shfl_sync(0xffffffffu, w, warp - 1) : 0);
 }
 
+// Where the parts of one of a token's blocks lie, in one word (0: there are none, or the attention wrote the
+// output itself): a whole block's in the rows of all tokens, a cut one's in the slots of n pairs from `first` on,
+// at the token's place in its block.
+struct ToJoin {
+  int n, first, place;
+  bool whole;
+};
+__device__ __forceinline__ int join_word(const ToJoin& j) { return j.n | j.first << 12 | j.place << 24 | (j.whole ? 1 << 30 : 0); }
+__device__ __forceinline__ ToJoin join_of(int w) { return {w & 0xFFF, w >> 12 & 0xFFF, w >> 24 & 0xF, (w >> 30 & 1) != 0}; }
+
 __global__ void __launch_bounds__(PP_THREADS, 1) prefix_plan_kernel(const Dev D, const ChunkArgs A) {
   extern __shared__ int plan[];
   __shared__ int tmp[32];
@@ -1586,7 +1596,7 @@ __global__ void __launch_bounds__(PP_THREADS, 1) prefix_plan_kernel(const Dev D,
   int* const before = reader + A.n_groups;
   const SharedWork W = shared_work(A, D.n_heads);
   bool bad = false;
-  for (int j = tid; j < A.n_tok; j += PP_THREADS) W.of_token[j] = make_int2(-1, -1);
+  for (int j = tid; j < A.n_tok; j += PP_THREADS) W.of_token[j] = make_int2(0, 0);
   for (int i = tid; i < A.n_seg; i += PP_THREADS) shared[i] = 0;
   clamp_starts(start, A.seg_start, A.n_seg + 1, A.n_tok, tmp, &bad);
   if (A.n_groups > 0) clamp_starts(group, A.group_start, A.n_groups + 1, A.n_seg, tmp, &bad);
@@ -1626,9 +1636,10 @@ __global__ void __launch_bounds__(PP_THREADS, 1) prefix_plan_kernel(const Dev D,
   if (tid == 0) before[units] = n_blocks;
   __syncthreads();
   int cost = 0;
+  PlanBlock B;
   for (int base = 0; base < n_blocks; base += PP_THREADS) {
     const int b = base + tid;
-    PlanBlock B = {make_int4(0, 0, -1, 0), make_int4(0, 0, CK_NO_CAP, 0)};
+    B = {make_int4(0, 0, -1, 0), make_int4(0, 0, CK_NO_CAP, 0)};
     bool of_group = false;
     if (b < n_blocks) {
       int l = 0, h = units;   // the last unit whose first block is <= b (never one without blocks)
@@ -1659,120 +1670,117 @@ __global__ void __launch_bounds__(PP_THREADS, 1) prefix_plan_kernel(const Dev D,
     int sum;
     B.b.w = cost + plan_scan(n > 0 ? CK_BLOCK_COST + n : 0, tmp, &sum);
     cost += sum;
-    if (b < n_blocks) {
-      W.blocks[b] = B;
-      if (n > 0)
-        for (int j = B.a.x; j < B.a.x + B.a.y; ++j) (of_group ? W.of_token[j].x : W.of_token[j].y) = b;
-    }
+    if (b < n_blocks) W.blocks[b] = B;
   }
   if (bad) set_status(D.status, HS_ERR_BAD_ID);
-  if (tid == 0) *W.head = {n_blocks, cost, max((cost + A.pairs - 1) / A.pairs, CK_MIN_COST), 0};
+  const int per_pair = max((cost + A.pairs - 1) / A.pairs, CK_MIN_COST);
+  if (tid == 0) *W.head = {n_blocks, cost, per_pair, 0};
+  // what is joined of each token, now that the ranges are known: the last blocks first, which are at hand
+  for (int base = (n_blocks - 1) / PP_THREADS * PP_THREADS, last = base; base >= 0; base -= PP_THREADS) {
+    const int b = base + tid;
+    if (b >= n_blocks) continue;
+    if (base != last) B = W.blocks[b];
+    const int pages = B.b.y - B.b.x;
+    if (pages <= 0) continue;
+    const int c = B.b.w + CK_BLOCK_COST, first = c / per_pair, n = (c + pages - 1) / per_pair - first + 1;
+    const bool of_group = B.b.z != CK_NO_CAP;
+    if (n == 1 && !of_group && B.b.x == 0) continue;
+    for (int j = 0; j < B.a.y; ++j)
+      (of_group ? W.of_token[B.a.x + j].x : W.of_token[B.a.x + j].y) = join_word({n, first, j, n == 1});
+  }
 }
 
 // Joins what the blocks of a token left in the workspace, in the order of its blocks and pairs: of a token
-// with two blocks both, of one with a cut block its parts. WIDE (few rows): 512 threads to a row, its parts
-// dealt to four slices; otherwise a slice of 128 to a row.
+// with two blocks both, of one with a cut block its parts. A slice of 128 threads has a row; WIDE (few rows, of
+// many parts each) deals a row's parts to a CTA's four slices. The CTAs go through the tasks in steps of the
+// grid and look up 32 tokens at a time, for most may have nothing to join.
+constexpr int PM_AHEAD = 6;   // parts whose loads are in flight
 template <typename T, bool WIDE>
-__global__ void __launch_bounds__(CM_THREADS) prefix_merge_kernel(const Dev D, const ChunkArgs A) {
-  __shared__ float4 acc[CM_SLICES][128];
+__global__ void __launch_bounds__(CM_THREADS, 2) prefix_merge_kernel(const Dev D, const ChunkArgs A) {
+  __shared__ float4 acc[WIDE ? CM_SLICES : 1][128];
   __shared__ float2 ml[CM_SLICES];
   griddep_wait();
-  const int tid = threadIdx.x, slice = tid >> 7, col = tid & 127, H = D.n_heads;
-  const long long row = WIDE ? (long long)blockIdx.x : (long long)blockIdx.x * CM_SLICES + slice, rows = (long long)A.n_tok * H;
-  if (row >= rows) return;
-  const int tok = (int)(row / H), h = (int)(row - (long long)tok * H);
+  const int tid = threadIdx.x, slice = tid >> 7, col = tid & 127, lane = tid & 31, H = D.n_heads;
   const SharedWork W = shared_work(A, H);
-  const int2 of = W.of_token[tok];
-  const int per_pair = W.head->per_pair;
-  // its parts: those of the block of shared positions, then those of its own
-  struct Parts {
-    int n, first;       // first: of the pairs that hold a cut block
-    long long at;       // where a whole one is; the row in a cut one's slots
-  };
-  auto parts_of = [&](int b, int kind) {
-    Parts p = {0, -1, 0};
-    if (b < 0) return p;
-    const PlanBlock B = W.blocks[b];
-    const int c = B.b.w + CK_BLOCK_COST, first = c / per_pair, last = (c + B.b.y - B.b.x - 1) / per_pair;
-    p.n = last - first + 1;
-    if (p.n == 1) {
-      p.at = (long long)kind * rows + row;
-    } else {
-      p.first = first;
-      p.at = (long long)(tok - B.a.x) * H + h;
-    }
-    return p;
-  };
-  const Parts x = parts_of(of.x, 0), y = parts_of(of.y, 1);
-  const int n = x.n + y.n;
-  if (n == 0 || (of.x < 0 && y.n == 1 && W.blocks[of.y].b.x == 0)) return;   // of no segment; written by the attention itself
-  const int step = WIDE ? CM_SLICES : 1;
-  float m = -INFINITY, l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  constexpr int AHEAD = 4;   // parts whose loads are in flight
-  for (int i = WIDE ? slice : 0; i < n; i += AHEAD * step) {
-    float2 s[AHEAD];
-    float4 v[AHEAD];
+  const int per_task = WIDE ? 1 : CM_SLICES, per_token = H / per_task, tasks = A.n_tok * per_token, rows = A.n_tok * H;
+  for (int base = blockIdx.x; base < tasks; base += 32 * gridDim.x) {
+    const int mine = base + lane * gridDim.x;
+    const int2 of = mine < tasks ? W.of_token[mine / per_token] : make_int2(0, 0);
+    for (unsigned todo = __ballot_sync(0xffffffffu, (of.x | of.y) != 0); todo; todo &= todo - 1) {
+      const int k = __ffs(todo) - 1, task = base + k * gridDim.x, row = task * per_task + (WIDE ? 0 : slice);
+      const ToJoin x = join_of(__shfl_sync(0xffffffffu, of.x, k)), y = join_of(__shfl_sync(0xffffffffu, of.y, k));
+      const int tok = task / per_token, h = row - tok * H, n = x.n + y.n;
+      const int step = WIDE ? CM_SLICES : 1;
+      float m = -INFINITY, l = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int i = WIDE ? slice : 0; i < n; i += PM_AHEAD * step) {
+        float2 s[PM_AHEAD];
+        float4 v[PM_AHEAD];
 #pragma unroll
-    for (int u = 0; u < AHEAD; ++u) {
-      const int k = i + u * step;
-      s[u] = make_float2(-INFINITY, 0.f);
-      v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (k >= n) continue;
-      const Parts& p = k < x.n ? x : y;
-      const int j = k < x.n ? k : k - x.n;
-      const bool whole = p.first < 0;
-      const size_t at = whole ? (size_t)p.at : ((size_t)(p.first + j) * 2 + (j == 0 ? 1 : 0)) * CK_ROWS + p.at;
-      s[u] = (whole ? W.whole_stats : W.stats)[at];
-      v[u] = *(reinterpret_cast<const float4*>((whole ? W.whole : W.part) + at * 512) + col);
-    }
-    float mn = m;
+        for (int u = 0; u < PM_AHEAD; ++u) {
+          const int q = i + u * step;
+          s[u] = make_float2(-INFINITY, 0.f);
+          v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (q >= n) continue;
+          const bool shared = q < x.n, whole = shared ? x.whole : y.whole;
+          const int j = shared ? q : q - x.n, first = shared ? x.first : y.first, place = shared ? x.place : y.place;
+          const size_t at = whole ? (size_t)(shared ? 0 : rows) + row
+                                  : ((size_t)(first + j) * 2 + (j == 0 ? 1 : 0)) * CK_ROWS + place * H + h;
+          s[u] = (whole ? W.whole_stats : W.stats)[at];
+          v[u] = *(reinterpret_cast<const float4*>((whole ? W.whole : W.part) + at * 512) + col);
+        }
+        float mn = m;
 #pragma unroll
-    for (int u = 0; u < AHEAD; ++u) mn = fmaxf(mn, s[u].x);
-    if (mn == -INFINITY) continue;
-    const float f = exp2f(m - mn);
-    m = mn;
-    l *= f;
-    o.x *= f, o.y *= f, o.z *= f, o.w *= f;
+        for (int u = 0; u < PM_AHEAD; ++u) mn = fmaxf(mn, s[u].x);
+        if (mn == -INFINITY) continue;
+        const float f = exp2f(m - mn);
+        m = mn;
+        l *= f;
+        o.x *= f, o.y *= f, o.z *= f, o.w *= f;
 #pragma unroll
-    for (int u = 0; u < AHEAD; ++u) {
-      if (s[u].x == -INFINITY) continue;   // what lies there may be anything
-      const float w = exp2f(s[u].x - mn);
-      l += w * s[u].y;
-      o.x += w * v[u].x, o.y += w * v[u].y, o.z += w * v[u].z, o.w += w * v[u].w;
-    }
-  }
-  if (WIDE) {
-    acc[slice][col] = o;
-    if (col == 0) ml[slice] = make_float2(m, l);
-    __syncthreads();
-    if (slice > 0) return;
-    m = fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x));
-    l = 0.f;
-    o = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (m > -INFINITY) {
-#pragma unroll
-      for (int u = 0; u < CM_SLICES; ++u) {
-        const float w = exp2f(ml[u].x - m);
-        const float4 v = acc[u][col];
-        l += w * ml[u].y;
-        o.x += w * v.x, o.y += w * v.y, o.z += w * v.z, o.w += w * v.w;
+        for (int u = 0; u < PM_AHEAD; ++u) {
+          const float w = exp2f(s[u].x - mn);   // 0 of a part that sees nothing, whose sums are 0
+          l += w * s[u].y;
+          o.x += w * v[u].x, o.y += w * v[u].y, o.z += w * v[u].z, o.w += w * v[u].w;
+        }
       }
+      if (WIDE) {
+        acc[slice][col] = o;
+        if (col == 0) ml[slice] = make_float2(m, l);
+        __syncthreads();
+        if (slice == 0) {
+          m = fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x));
+          l = 0.f;
+          o = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (m > -INFINITY) {
+#pragma unroll
+            for (int u = 0; u < CM_SLICES; ++u) {
+              const float w = exp2f(ml[u].x - m);
+              const float4 v = acc[u][col];
+              l += w * ml[u].y;
+              o.x += w * v.x, o.y += w * v.y, o.z += w * v.z, o.w += w * v.w;
+            }
+          }
+        }
+      }
+      if (!WIDE || slice == 0) {
+        if (only_low(m)) {
+          l = 0.f;
+          if (col == 0) set_status(D.status, HS_ERR_RANGE);
+        }
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        T* op = static_cast<T*>(A.out) + tok * A.o_tok + h * A.o_head + col * 4;
+        *reinterpret_cast<uint2*>(op) = make_uint2(pack2<T>(o.x * inv, o.y * inv), pack2<T>(o.z * inv, o.w * inv));
+        if (A.lse && col == 0) A.lse[row] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+      }
+      if (WIDE) __syncthreads();   // the slices' sums are read
     }
   }
-  if (only_low(m)) {
-    l = 0.f;
-    if (col == 0) set_status(D.status, HS_ERR_RANGE);
-  }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  T* op = static_cast<T*>(A.out) + tok * A.o_tok + h * A.o_head + col * 4;
-  *reinterpret_cast<uint2*>(op) = make_uint2(pack2<T>(o.x * inv, o.y * inv), pack2<T>(o.z * inv, o.w * inv));
-  if (A.lse && col == 0) A.lse[row] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
 
 int prefix_blocks(int n_tok, int n_seg, int n_groups, int tpb) { return n_seg + n_groups + 2 * (n_tok / tpb) + 1; }
 
-constexpr long long PM_WIDE_ROWS = 4096;
+constexpr int PM_WIDE_ROWS = 1024;
 template <typename T>
 hs_status launch_prefix(hs_pool* p, const ChunkArgs& a, cudaStream_t st) {
   const int smem = plan_ints(a.n_seg, a.n_groups) * 4;
@@ -1780,11 +1788,11 @@ hs_status launch_prefix(hs_pool* p, const ChunkArgs& a, cudaStream_t st) {
   hs_status s = launch_pdl(prefix_plan_kernel, dim3(1), dim3(PP_THREADS), smem, st, 0, p->d, a);
   if (s == HS_OK) s = launch_attention_pairs<T, true>(p, a, st);
   if (s != HS_OK) return s;
-  const long long rows = (long long)a.n_tok * p->cfg.n_heads;
+  const int rows = a.n_tok * p->cfg.n_heads, most = 2 * num_sms();   // resident at once
+  const auto grid = [&](int tasks) { return dim3(tasks < most ? tasks : most); };
   if (rows <= PM_WIDE_ROWS)
-    return launch_pdl(prefix_merge_kernel<T, true>, dim3((unsigned)rows), dim3(CM_THREADS), 0, st, 0, p->d, a);
-  return launch_pdl(prefix_merge_kernel<T, false>, dim3((unsigned)((rows + CM_SLICES - 1) / CM_SLICES)), dim3(CM_THREADS), 0, st, 0,
-                    p->d, a);
+    return launch_pdl(prefix_merge_kernel<T, true>, grid(rows), dim3(CM_THREADS), 0, st, 0, p->d, a);
+  return launch_pdl(prefix_merge_kernel<T, false>, grid(rows / CM_SLICES), dim3(CM_THREADS), 0, st, 0, p->d, a);
 }
 
 bool stride_ok(int64_t s, int64_t least) { return s >= least && s < (1ll << 40) && s % 8 == 0; }

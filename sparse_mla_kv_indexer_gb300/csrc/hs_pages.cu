@@ -112,145 +112,121 @@ __global__ void __launch_bounds__(FK_THREADS) fork_kernel(const Dev D, const For
 }
 
 // ---- copies and moves -----------------------------------------------------------------
-// Which copies are made. Every CTA builds a table of the pages that the call names in shared memory (open
-// addressing, at most 3 of 4 slots in use): how often each is a destination and a source, and where it
-// goes. That takes the place of an array of all pages that would have to be cleared again.
+// Two launches: which copies are made, then the copies themselves, with the tables' entries beside them.
 constexpr int CP_THREADS = 512, CP_WARPS = CP_THREADS / 32;
-constexpr uint32_t CP_EMPTY = 0xFFFFFFFFu;
-constexpr int CP_SOURCE = 1 << 13;                  // one more as a source (counts up to 4,096 in 13 bits)
-static_assert(HS_COPY_MAX_PAGES < CP_SOURCE, "counts");
-
-struct Named {
-  uint32_t* key;     // page, CP_EMPTY
-  uint32_t* count;
-  int32_t* to;       // for remap: where the page goes
-  uint32_t mask;
-};
-__device__ __forceinline__ uint32_t slot_hash(uint32_t page) { return page * 2654435761u >> 12; }
-__device__ __forceinline__ void name_page(const Named& t, uint32_t page, uint32_t add, int to) {
-  uint32_t s = slot_hash(page) & t.mask;
-  for (;;) {   // ends: a quarter of the slots stay empty
-    const uint32_t was = atomicCAS(t.key + s, CP_EMPTY, page);
-    if (was == CP_EMPTY || was == page) break;
-    s = (s + 1) & t.mask;
-  }
-  atomicAdd(t.count + s, add);
-  if (add == CP_SOURCE && t.to) t.to[s] = to;
-}
-__device__ __forceinline__ int find_page(const Named& t, uint32_t page) {   // its slot, or -1
-  uint32_t s = slot_hash(page) & t.mask;
-  for (;;) {
-    const uint32_t k = t.key[s];
-    if (k == page) return (int)s;
-    if (k == CP_EMPTY) return -1;
-    s = (s + 1) & t.mask;
-  }
-}
-// All threads of the CTA. Pages out of range are not named (a copy from or to one is not made).
-__device__ void name_pages(const Named& t, int n, const int32_t* from, const int32_t* to, int pages) {
-  for (uint32_t s = threadIdx.x; s <= t.mask; s += blockDim.x) t.key[s] = CP_EMPTY, t.count[s] = 0;
-  __syncthreads();
-  for (int i = threadIdx.x; i < n; i += blockDim.x) {
-    const int f = from[i], d = to[i];
-    if (f >= 0 && f < pages) name_page(t, (uint32_t)f, CP_SOURCE, d);
-    if (d >= 0 && d < pages) name_page(t, (uint32_t)d, 1, 0);
-  }
-  __syncthreads();
-}
-__device__ __forceinline__ bool copy_made(const Named& t, int f, int d, int pages, bool remap) {
-  if (f < 0 || f >= pages || d < 0 || d >= pages) return false;
-  if (t.count[find_page(t, (uint32_t)d)] != 1) return false;   // another destination, or a source
-  return !remap || (t.count[find_page(t, (uint32_t)f)] & ~(CP_SOURCE - 1)) == CP_SOURCE;
-}
-
 struct CopyList {
   int n, pages;               // copies; pages of this kind in the pool
   const int32_t *from, *to;
 };
 struct CopyArgs {
   CopyList kv, idx;
-  int kv_ctas, remap;         // the first kv_ctas CTAs copy KV pages, the others index pages
-  uint32_t kv_mask, idx_mask; // slots - 1
+  int remap, remap_ctas, kv_ctas;   // CTAs of the second launch: tables, then KV pages, then index pages
 };
-__host__ __device__ inline uint32_t slots_for(int n) {
-  uint32_t s = 64;
-  while (3 * s < 8u * (uint32_t)n) s *= 2;
-  return s;
+
+// Every copy against all the others of its kind, a warp each, from shared memory: at most 4,096 x 8,192
+// comparisons of whole numbers over the whole GPU are less than building a table of the pages in every CTA was
+// (10 us for 2,500 pages; the search for an entry's page in it 20 us). With remap the copies that are made are
+// marked in the pool's array of pages, with a number of the call's own, so that nothing has to be cleared.
+__global__ void __launch_bounds__(CP_THREADS) check_copies_kernel(const Dev D, const CopyArgs A) {
+  extern __shared__ int32_t named[];
+  griddep_wait();
+  const bool kv = blockIdx.y == 0;
+  const CopyList L = kv ? A.kv : A.idx;
+  const uint32_t epoch = D.copy_epoch[0] + 1;   // of this call; the second launch keeps it
+  if (blockIdx.x == 0 && kv && threadIdx.x == 0) D.copy_epoch[1] = epoch;
+  int32_t *const from = named, *const to = named + L.n;
+  #pragma unroll 8
+  for (int i = threadIdx.x; i < L.n; i += CP_THREADS) from[i] = L.from[i], to[i] = L.to[i];
+  __syncthreads();
+  const int lane = threadIdx.x & 31;
+  for (int i = blockIdx.x * CP_WARPS + (threadIdx.x >> 5); i < L.n; i += gridDim.x * CP_WARPS) {
+    const int f = from[i], d = to[i];
+    int sources = 0, dests = 0, chained = 0;
+#pragma unroll 4
+    for (int j = lane; j < L.n; j += 32) {
+      const int fj = from[j];
+      sources += fj == f;
+      chained |= fj == d;
+      dests += to[j] == d;
+    }
+    sources = __reduce_add_sync(0xffffffffu, sources);
+    dests = __reduce_add_sync(0xffffffffu, dests);
+    chained = __reduce_or_sync(0xffffffffu, chained);
+    const bool ok = f >= 0 && f < L.pages && d >= 0 && d < L.pages && dests == 1 && !chained && (!A.remap || sources == 1);
+    if (lane == 0) {
+      D.copy_ok[(kv ? 0 : HS_COPY_MAX_PAGES) + i] = ok;
+      if (!ok) set_status(D.status, HS_ERR_BAD_ID);
+      else if (A.remap) D.page_map[(kv ? 0 : D.num_pages) + f] = make_int2((int)epoch, d);
+    }
+  }
 }
 
 // A warp's unit is 1/8 of a page of one layer (5,248 bytes) or 1/2 of an index page of one indexer layer,
-// all of its loads in flight at once.
+// all of its loads in flight at once, and the next unit's pages beside them.
 constexpr int CP_KV_SLICES = 8, CP_IDX_SLICES = 2, CP_AHEAD = 11;
 static_assert(KV_CHUNKS / CP_KV_SLICES <= 32 * CP_AHEAD && HS_IDX_FP8_PAGE_BYTES / 16 / CP_IDX_SLICES <= 32 * CP_AHEAD, "unit");
-__global__ void __launch_bounds__(CP_THREADS, 2) copy_pages_kernel(const Dev D, const CopyArgs A) {
-  extern __shared__ uint32_t slots[];
-  griddep_wait();
-  const bool kv = (int)blockIdx.x < A.kv_ctas;
-  const CopyList L = kv ? A.kv : A.idx;
-  const uint32_t mask = kv ? A.kv_mask : A.idx_mask;
-  const Named t = {slots, slots + mask + 1, nullptr, mask};
-  name_pages(t, L.n, L.from, L.to, L.pages);
-  const int lane = threadIdx.x & 31, cta = kv ? blockIdx.x : blockIdx.x - A.kv_ctas, ctas = kv ? A.kv_ctas : gridDim.x - A.kv_ctas;
-  const int layers = kv ? D.n_layers : D.n_groups, slices = kv ? CP_KV_SLICES : CP_IDX_SLICES;
-  const int page_bytes = kv ? PAGE * ROW : D.idx_page_bytes, chunks = page_bytes / 16 / slices;
-  const int per_page = layers * slices;
-  const long long units = (long long)L.n * per_page;
-  for (long long u = (long long)cta * CP_WARPS + (threadIdx.x >> 5); u < units; u += (long long)ctas * CP_WARPS) {
-    const int i = (int)(u / per_page), r = (int)(u - (long long)i * per_page), layer = r / slices, slice = r - layer * slices;
-    const int f = L.from[i], d = L.to[i];
-    if (!copy_made(t, f, d, L.pages, A.remap)) {
-      if (lane == 0) set_status(D.status, HS_ERR_BAD_ID);
-      continue;
-    }
-    uint8_t* const pages = kv ? D.kv[layer] : reinterpret_cast<uint8_t*>(D.idx[layer]);
-    const uint4* const from = reinterpret_cast<const uint4*>(pages + (size_t)f * page_bytes) + slice * chunks;
-    uint4* const to = reinterpret_cast<uint4*>(pages + (size_t)d * page_bytes) + slice * chunks;
-    uint4 v[CP_AHEAD];
+constexpr int RM_ENTRIES = 8;      // table entries of a thread at a time
+
+// The entries of a table that name a marked page.
+__device__ __forceinline__ void remap_table(int32_t* entries, long long n, const int2* map, int pages, int epoch, int cta, int ctas) {
+  const long long stride = (long long)ctas * CP_THREADS;
+  for (long long e0 = (long long)cta * CP_THREADS + threadIdx.x; e0 < n; e0 += RM_ENTRIES * stride) {
+    int32_t v[RM_ENTRIES];
+    int2 to[RM_ENTRIES];
 #pragma unroll
-    for (int k = 0; k < CP_AHEAD; ++k)
-      if (lane + 32 * k < chunks) v[k] = from[lane + 32 * k];
+    for (int k = 0; k < RM_ENTRIES; ++k) v[k] = e0 + k * stride < n ? entries[e0 + k * stride] : -1;
 #pragma unroll
-    for (int k = 0; k < CP_AHEAD; ++k)
-      if (lane + 32 * k < chunks) to[lane + 32 * k] = v[k];
+    for (int k = 0; k < RM_ENTRIES; ++k) to[k] = v[k] >= 0 && v[k] < pages ? map[v[k]] : make_int2(epoch - 1, 0);
+#pragma unroll
+    for (int k = 0; k < RM_ENTRIES; ++k)
+      if (to[k].x == epoch) entries[e0 + k * stride] = to[k].y;
   }
 }
 
-// Every table entry that names a moved page, after the copies: the same table in shared memory, with where
-// each page goes.
-constexpr int RM_ENTRIES = 8;      // of a thread at a time
-__global__ void __launch_bounds__(CP_THREADS) remap_kernel(const Dev D, const CopyArgs A) {
-  extern __shared__ uint32_t slots[];
+__global__ void __launch_bounds__(CP_THREADS, 2) copy_pages_kernel(const Dev D, const CopyArgs A) {
   griddep_wait();
-  const long long per_table = (long long)D.max_requests * D.max_pages;
-#pragma unroll 1
-  for (int kind = 0; kind < 2; ++kind) {
-    const CopyList L = kind == 0 ? A.kv : A.idx;
-    if (L.n == 0) continue;
-    const uint32_t mask = kind == 0 ? A.kv_mask : A.idx_mask;
-    const Named t = {slots, slots + mask + 1, reinterpret_cast<int32_t*>(slots + 2 * (mask + 1)), mask};
-    __syncthreads();
-    name_pages(t, L.n, L.from, L.to, L.pages);
-#pragma unroll 1
-    for (int table = 0; table < (kind == 0 ? 2 : 1); ++table) {
-      int32_t* const entries = kind == 1 ? D.idx_bt : table == 0 ? D.bt : D.hot_pages;
-      const long long n = table == 0 ? per_table : (long long)D.max_requests * D.n_groups * D.hot_pages_max;
-      const long long stride = (long long)gridDim.x * CP_THREADS;
-      for (long long e0 = (long long)blockIdx.x * CP_THREADS + threadIdx.x; e0 < n; e0 += RM_ENTRIES * stride) {
-        int32_t v[RM_ENTRIES];
-#pragma unroll
-        for (int k = 0; k < RM_ENTRIES; ++k) v[k] = e0 + k * stride < n ? entries[e0 + k * stride] : -1;
-#pragma unroll
-        for (int k = 0; k < RM_ENTRIES; ++k) {
-          if (v[k] < 0) continue;
-          const int s = find_page(t, (uint32_t)v[k]);
-          if (s < 0 || t.count[s] < CP_SOURCE) continue;
-          const int to = t.to[s];
-          if (copy_made(t, v[k], to, L.pages, true)) entries[e0 + k * stride] = to;
-        }
-      }
+  int cta = blockIdx.x;
+  if (cta < A.remap_ctas) {
+    const int epoch = (int)D.copy_epoch[1];
+    const long long n = (long long)D.max_requests * D.max_pages;
+    if (A.kv.n > 0) {
+      remap_table(D.bt, n, D.page_map, D.num_pages, epoch, cta, A.remap_ctas);
+      remap_table(D.hot_pages, (long long)D.max_requests * D.n_groups * D.hot_pages_max, D.page_map, D.num_pages, epoch, cta, A.remap_ctas);
     }
+    if (A.idx.n > 0) remap_table(D.idx_bt, n, D.page_map + D.num_pages, D.num_idx_pages, epoch, cta, A.remap_ctas);
+    if (cta == 0 && threadIdx.x == 0) D.copy_epoch[0] = (uint32_t)epoch;
+    __threadfence();   // as the forks'
+    return;
   }
-  __threadfence();   // as the forks'
+  cta -= A.remap_ctas;
+  const bool kv = cta < A.kv_ctas;
+  const CopyList L = kv ? A.kv : A.idx;
+  const uint8_t* const ok = D.copy_ok + (kv ? 0 : HS_COPY_MAX_PAGES);
+  const int ctas = kv ? A.kv_ctas : gridDim.x - A.remap_ctas - A.kv_ctas;
+  if (!kv) cta -= A.kv_ctas;
+  const int lane = threadIdx.x & 31, slices = kv ? CP_KV_SLICES : CP_IDX_SLICES, per_page = (kv ? D.n_layers : D.n_groups) * slices;
+  const int page_bytes = kv ? PAGE * ROW : D.idx_page_bytes, chunks = page_bytes / 16 / slices;
+  const int units = L.n * per_page, step = ctas * CP_WARPS;   // at most 4,096 x 64 x 8
+  int u = cta * CP_WARPS + (threadIdx.x >> 5);
+  if (u >= units) return;
+  int i = u / per_page, f = L.from[i], d = L.to[i];
+  bool made = ok[i];
+  for (; u < units;) {
+    const int r = u - i * per_page, layer = r / slices, slice = r - layer * slices;
+    uint8_t* const pages = kv ? D.kv[layer] : reinterpret_cast<uint8_t*>(D.idx[layer]);
+    const uint4* const from = reinterpret_cast<const uint4*>(pages + (size_t)(made ? f : 0) * page_bytes) + slice * chunks;
+    uint4* const to = reinterpret_cast<uint4*>(pages + (size_t)(made ? d : 0) * page_bytes) + slice * chunks;
+    uint4 v[CP_AHEAD];
+#pragma unroll
+    for (int k = 0; k < CP_AHEAD; ++k)
+      if (made && lane + 32 * k < chunks) v[k] = __ldcs(from + lane + 32 * k);
+    const bool now = made;
+    u += step;
+    if (u < units) i = u / per_page, f = L.from[i], d = L.to[i], made = ok[i];
+#pragma unroll
+    for (int k = 0; k < CP_AHEAD; ++k)
+      if (now && lane + 32 * k < chunks) __stcs(to + lane + 32 * k, v[k]);
+  }
 }
 
 // ---- the tables -----------------------------------------------------------------------
@@ -303,30 +279,26 @@ extern "C" hs_status hs_copy_pages(hs_pool* p, int32_t n, const int32_t* d_from,
   CopyArgs a = {};
   a.kv = {n, p->cfg.num_pages, d_from, d_to};
   a.idx = {n_idx, p->cfg.num_idx_pages, d_idx_from, d_idx_to};
-  a.kv_mask = slots_for(n) - 1;
-  a.idx_mask = slots_for(n_idx) - 1;
   a.remap = remap != 0;
-  const int slots = (int)((a.kv_mask > a.idx_mask ? a.kv_mask : a.idx_mask) + 1), smem = slots * 8;
-  // CTAs for both kinds by their bytes, as many as are resident at once
+  const int sms = num_sms(), most_listed = n > n_idx ? n : n_idx, checks = (most_listed + CP_WARPS - 1) / CP_WARPS;
+  const hs_status s = launch_pdl(check_copies_kernel, dim3(checks < sms ? checks : sms, 2), dim3(CP_THREADS), most_listed * 8, st, 0, p->d, a);
+  if (s != HS_OK) return s;
+  // CTAs for both kinds by their bytes, two on an SM
   const long long kv_units = (long long)n * p->d.n_layers * CP_KV_SLICES, idx_units = (long long)n_idx * p->d.n_groups * CP_IDX_SLICES;
   const long long kv_bytes = (long long)n * p->d.n_layers * PAGE * ROW, idx_bytes = (long long)n_idx * p->d.n_groups * p->d.idx_page_bytes;
-  const int most = num_sms() * (smem > 110 * 1024 ? 1 : 2);
   const auto ctas_for = [&](long long units, long long bytes) -> int {
     if (units == 0) return 0;
-    const long long share = (long long)((double)most * bytes / (kv_bytes + idx_bytes)), need = (units + CP_WARPS - 1) / CP_WARPS;
+    const long long share = (long long)(2.0 * sms * bytes / (kv_bytes + idx_bytes)), need = (units + CP_WARPS - 1) / CP_WARPS;
     const long long c = share < 1 ? 1 : share;
     return (int)(c < need ? c : need);
   };
   a.kv_ctas = ctas_for(kv_units, kv_bytes);
-  const int ctas = a.kv_ctas + ctas_for(idx_units, idx_bytes);
-  if (ensure_kernel_attrs(copy_pages_kernel, smem) != HS_OK) return HS_ERR_CUDA;
-  hs_status s = launch_pdl(copy_pages_kernel, dim3(ctas), dim3(CP_THREADS), smem, st, 0, p->d, a);
-  if (s != HS_OK || !remap) return s;
-  const int smem_remap = slots * 12;
-  if (ensure_kernel_attrs(remap_kernel, smem_remap) != HS_OK) return HS_ERR_CUDA;
-  const long long entries = (long long)p->cfg.max_requests * p->d.max_pages, need = (entries + CP_THREADS * RM_ENTRIES - 1) / (CP_THREADS * RM_ENTRIES);
-  const int grid = (int)(need < num_sms() ? need : num_sms());
-  return launch_pdl(remap_kernel, dim3(grid), dim3(CP_THREADS), smem_remap, st, 0, p->d, a);
+  if (remap) {
+    const long long entries = (long long)p->cfg.max_requests * p->d.max_pages, each = CP_THREADS * RM_ENTRIES;
+    a.remap_ctas = (int)((entries + each - 1) / each < sms ? (entries + each - 1) / each : sms);
+  }
+  const int ctas = a.remap_ctas + a.kv_ctas + ctas_for(idx_units, idx_bytes);
+  return launch_pdl(copy_pages_kernel, dim3(ctas), dim3(CP_THREADS), 0, st, 0, p->d, a);
 }
 
 extern "C" hs_status hs_get_pages(hs_pool* p, int32_t n, const int32_t* d_req, int32_t first, int32_t count, int32_t* d_bt,

@@ -363,6 +363,9 @@ hs_status hs_pool_init(const hs_pool_config* cfg, void* const* d_kv_layers, void
     D.bsel_tokens = c.max_tokens < BS_MAX_TOKENS ? c.max_tokens : BS_MAX_TOKENS;
     chk(dev_alloc(p, &D.bsel, (size_t)D.bsel_tokens * sizeof(BselTok), 0));
   }
+  chk(dev_alloc(p, &D.page_map, (size_t)c.num_pages + c.num_idx_pages, 0));
+  chk(dev_alloc(p, &D.copy_ok, 2 * (size_t)HS_COPY_MAX_PAGES, 0));
+  chk(dev_alloc(p, &D.copy_epoch, 2, 0));
   if (s == HS_OK) {
     if (cudaMemcpy(D.kv, d_kv_layers, sizeof(void*) * c.n_layers, cudaMemcpyHostToDevice) != cudaSuccess ||
         cudaMemcpy(D.idx, d_idx_layers, sizeof(void*) * n_groups, cudaMemcpyHostToDevice) != cudaSuccess ||

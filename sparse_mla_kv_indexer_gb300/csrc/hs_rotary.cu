@@ -23,11 +23,13 @@ namespace hs {
 
 namespace {
 
-constexpr int RO_THREADS = 256;
+constexpr int RO_THREADS = 512;      // at most
+constexpr int RO_SOME = 256;
+constexpr int RO_RESIDENT = 2;       // CTAs of as many threads on an SM, by their registers
 constexpr int RO_PARTS = HS_ROTARY_MAX_PARTS;
 constexpr int RO_MAX_PAIRS = HS_ROTARY_MAX_DIMS / 2;
 constexpr int RO_TABLE = 2048;       // (cos, sin) of a CTA's tokens, at most
-constexpr int RO_AHEAD = 2;          // units of a thread in flight
+constexpr int RO_AHEAD = 3;          // units of a thread in flight
 
 struct RotaryPart {
   const void* in;
@@ -54,96 +56,129 @@ __device__ __forceinline__ float2 cos_sin(uint64_t phase) {
   return make_float2(((quarter + 1) & 2) ? -u : u, (quarter & 2) ? -v : v);
 }
 
-// V pairs of one row: V neighbouring pairs, or V values of either half.
+// V pairs of one row: V neighbouring pairs, or V values of either half, as they are stored.
 template <typename T, int V>
 struct Unit {
   T a[V], b[V];
 };
 template <typename T, int V>
-__device__ __forceinline__ void copy_values(T* to, const T* from) {
+__device__ __forceinline__ void load_values(T (&to)[V], const T* from) {
   if constexpr (V * sizeof(T) == 16) {
-    *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(from);
+    const uint4 v = *reinterpret_cast<const uint4*>(from);
+    memcpy(to, &v, 16);
   } else {
 #pragma unroll
     for (int i = 0; i < V; ++i) to[i] = from[i];
   }
 }
+template <typename T, int V>
+__device__ __forceinline__ void store_values(T* to, const T (&from)[V]) {
+  if constexpr (V * sizeof(T) == 16) {
+    uint4 v;
+    memcpy(&v, from, 16);
+    *reinterpret_cast<uint4*>(to) = v;
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) to[i] = from[i];
+  }
+}
+// (a, b) -> (a c - b s, a s + b c) of V pairs, two at a time; c and s in shared memory.
+template <int V>
+__device__ __forceinline__ void turn(float (&a)[V], float (&b)[V], const float* c, const float* s) {
+  if constexpr (V % 4 == 0) {
+#pragma unroll
+    for (int j = 0; j < V; j += 4) {
+      const uint4 c4 = *reinterpret_cast<const uint4*>(c + j), s4 = *reinterpret_cast<const uint4*>(s + j);
+#pragma unroll
+      for (int k = 0; k < 4; k += 2) {
+        const F2 x = f2(__float_as_uint(a[j + k]), __float_as_uint(a[j + k + 1])), y = f2(__float_as_uint(b[j + k]), __float_as_uint(b[j + k + 1]));
+        const F2 cc = k ? f2(c4.z, c4.w) : f2(c4.x, c4.y), ss = k ? f2(s4.z, s4.w) : f2(s4.x, s4.y);
+        const F2 minus_y = f2(__float_as_uint(-b[j + k]), __float_as_uint(-b[j + k + 1]));
+        unpack(fma2(x, cc, mul2(minus_y, ss)), a[j + k], a[j + k + 1]);
+        unpack(fma2(x, ss, mul2(y, cc)), b[j + k], b[j + k + 1]);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const float x = a[j], y = b[j];
+      a[j] = x * c[j] - y * s[j];
+      b[j] = x * s[j] + y * c[j];
+    }
+  }
+}
 
 template <typename T, int V>
-__global__ void __launch_bounds__(RO_THREADS) rotary_kernel(const __grid_constant__ RotaryArgs A) {
-  __shared__ float2 table[RO_TABLE];
+__global__ void __launch_bounds__(RO_THREADS, RO_RESIDENT) rotary_kernel(const __grid_constant__ RotaryArgs A) {
+  __shared__ __align__(16) float cosines[RO_TABLE], sines[RO_TABLE];
   griddep_wait();
-  const int tid = threadIdx.x, per_head = A.pairs / V;
+  const int tid = threadIdx.x, threads = blockDim.x;
   const int group = blockIdx.x / A.splits, split = blockIdx.x - group * A.splits;
   const int tok0 = group * A.tokens, n_tok = min(A.tokens, A.n - tok0);
-  const int row0 = split * A.rows, n_rows = min(A.rows, A.heads - row0);
-  const int units = n_tok * n_rows * per_head;
+  const int row0 = split * A.rows, n_rows = min(A.rows, A.heads - row0), all = n_tok * n_rows;
+  // a thread has the same pairs of every row that it takes
+  const int per_head = A.pairs / V, step = threads / per_head, mine = tid / per_head, at = (tid - mine * per_head) * V;
   struct Place {
     T* out;
-    int cs, halves;
+    int halves, cs;   // the row's layout; where its cosines are
   };
-  auto load = [&](int u, Unit<T, V>& x) {
+  auto load = [&](int row, Unit<T, V>& x) {
     Place p;
-    const int row = u / per_head, at = (u - row * per_head) * V, tk = row / n_rows, h = row0 + row - tk * n_rows;
+    const int tk = n_tok == 1 ? 0 : row / n_rows, h = row0 + row - tk * n_rows;
     int k = 0;
 #pragma unroll
     for (int i = 1; i < RO_PARTS; ++i)
       if (i < A.n_parts && h >= A.part[i].first) k = i;
     const RotaryPart& P = A.part[k];
+    const long long t = tok0 + tk, hd = h - P.first;
+    const int lo = P.halves ? at : 2 * at;
     p.halves = P.halves;
     p.cs = tk * A.pairs + at;
-    const long long t = tok0 + tk, hd = h - P.first;
-    const T* in = static_cast<const T*>(P.in) + t * P.in_tok + hd * P.in_head;
-    p.out = static_cast<T*>(P.out) + t * P.out_tok + hd * P.out_head + (p.halves ? at : 2 * at);
-    in += p.halves ? at : 2 * at;
-    copy_values<T, V>(x.a, in);
-    copy_values<T, V>(x.b, in + (p.halves ? A.pairs : V));
+    p.out = static_cast<T*>(P.out) + t * P.out_tok + hd * P.out_head + lo;
+    const T* in = static_cast<const T*>(P.in) + t * P.in_tok + hd * P.in_head + lo;
+    load_values(x.a, in);
+    load_values(x.b, in + (P.halves ? A.pairs : V));
     return p;
   };
   Unit<T, V> x[RO_AHEAD];
   Place p[RO_AHEAD];
 #pragma unroll
   for (int i = 0; i < RO_AHEAD; ++i)
-    if (tid + i * RO_THREADS < units) p[i] = load(tid + i * RO_THREADS, x[i]);
-  for (int i = tid; i < n_tok * A.pairs; i += RO_THREADS) {
+    if (mine < step && mine + i * step < all) p[i] = load(mine + i * step, x[i]);
+  for (int i = tid; i < n_tok * A.pairs; i += threads) {
     const int tk = i / A.pairs;
     const float2 cs = cos_sin((uint64_t)(int64_t)A.pos[tok0 + tk] * A.steps[i - tk * A.pairs]);
-    table[i] = make_float2(cs.x * A.magnitude, cs.y * A.magnitude * A.sign);
+    cosines[i] = cs.x * A.magnitude;
+    sines[i] = cs.y * A.magnitude * A.sign;
   }
   __syncthreads();
-  for (int u0 = tid; u0 < units; u0 += RO_AHEAD * RO_THREADS) {
-    if (u0 != tid) {
+  if (mine >= step) return;
+  for (int r0 = mine; r0 < all; r0 += RO_AHEAD * step) {
+    if (r0 != mine) {
 #pragma unroll
       for (int i = 0; i < RO_AHEAD; ++i)
-        if (u0 + i * RO_THREADS < units) p[i] = load(u0 + i * RO_THREADS, x[i]);
+        if (r0 + i * step < all) p[i] = load(r0 + i * step, x[i]);
     }
 #pragma unroll
     for (int i = 0; i < RO_AHEAD; ++i) {
-      if (u0 + i * RO_THREADS >= units) break;
+      if (r0 + i * step >= all) break;
+      float a[V], b[V];
       Unit<T, V> y;
-      const float2* cs = table + p[i].cs;
       if (p[i].halves) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-          const float a = to_f32(x[i].a[j]), b = to_f32(x[i].b[j]);
-          y.a[j] = from_f32<T>(a * cs[j].x - b * cs[j].y);
-          y.b[j] = from_f32<T>(a * cs[j].y + b * cs[j].x);
-        }
-      } else {
-        // values 0 .. 2 V - 1 in a, then b: pair j is values 2 j and 2 j + 1
-        const T* v = x[i].a;
-        T* w = y.a;
+        for (int j = 0; j < V; ++j) a[j] = to_f32(x[i].a[j]), b[j] = to_f32(x[i].b[j]);
+        turn(a, b, cosines + p[i].cs, sines + p[i].cs);
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-          const float a = to_f32(2 * j < V ? v[2 * j] : x[i].b[2 * j - V]);
-          const float b = to_f32(2 * j + 1 < V ? v[2 * j + 1] : x[i].b[2 * j + 1 - V]);
-          const T ra = from_f32<T>(a * cs[j].x - b * cs[j].y), rb = from_f32<T>(a * cs[j].y + b * cs[j].x);
-          if (2 * j < V) w[2 * j] = ra; else y.b[2 * j - V] = ra;
-          if (2 * j + 1 < V) w[2 * j + 1] = rb; else y.b[2 * j + 1 - V] = rb;
-        }
+        for (int j = 0; j < V; ++j) y.a[j] = from_f32<T>(a[j]), y.b[j] = from_f32<T>(b[j]);
+      } else {   // the 2 V values in order: pair j is values 2 j and 2 j + 1
+#pragma unroll
+        for (int j = 0; j < 2 * V; ++j) (j & 1 ? b : a)[j >> 1] = to_f32(j < V ? x[i].a[j] : x[i].b[j - V]);
+        turn(a, b, cosines + p[i].cs, sines + p[i].cs);
+#pragma unroll
+        for (int j = 0; j < 2 * V; ++j) (j < V ? y.a[j] : y.b[j - V]) = from_f32<T>((j & 1 ? b : a)[j >> 1]);
       }
-      copy_values<T, V>(p[i].out, y.a);
-      copy_values<T, V>(p[i].out + (p[i].halves ? A.pairs : V), y.b);
+      store_values(p[i].out, y.a);
+      store_values(p[i].out + (p[i].halves ? A.pairs : V), y.b);
     }
   }
 }
@@ -158,27 +193,30 @@ bool wide_part(const hs_rotary_part& p, int pairs, int size) {
 template <typename T>
 hs_status launch_rotary(RotaryArgs& a, bool wide, cudaStream_t st) {
   const int v = wide ? 16 / (int)sizeof(T) : 1, per_head = a.pairs / v, sms = num_sms();
-  const int unit_room = RO_THREADS * RO_AHEAD;   // a CTA's units that are all in flight at once
-  const int most = RO_TABLE / a.pairs;
-  // tokens of a CTA: one, or of few heads as many as fill it; but at least a CTA for every SM
-  int tokens = unit_room / (a.heads * per_head);
+  // tokens of a CTA: one, or of few heads as many as keep 256 threads busy; but at least a CTA for every SM
+  int tokens = RO_SOME * RO_AHEAD / (a.heads * per_head);
+  const int most = RO_TABLE / a.pairs, spread = (a.n + sms - 1) / sms;
   if (tokens > most) tokens = most;
-  if (tokens > (a.n + sms - 1) / sms) tokens = (a.n + sms - 1) / sms;
+  if (tokens > spread) tokens = spread;
   a.tokens = tokens < 1 ? 1 : tokens;
   const int groups = (a.n + a.tokens - 1) / a.tokens;
   // few tokens: their heads dealt to several CTAs, a unit per thread
   int rows = a.heads;
   if (groups < sms) {
-    const int least = (RO_THREADS + per_head * a.tokens - 1) / (per_head * a.tokens);
+    const int least = (RO_SOME + per_head * a.tokens - 1) / (per_head * a.tokens);
     const int even = (int)(((long long)a.heads * groups + sms - 1) / sms);
     rows = even > least ? even : least;
     if (rows > a.heads) rows = a.heads;
   }
   a.rows = rows;
   a.splits = (a.heads + rows - 1) / rows;
+  // threads: as many as take the rows in the fewest rounds, evenly (130 rows of four units by 288 threads in one
+  // round; 256 threads would begin another one for the last two rows)
+  const int all = a.tokens * rows, round = RO_THREADS / per_head * RO_AHEAD, rounds = (all + round - 1) / round;
+  const int step = (all + rounds * RO_AHEAD - 1) / (rounds * RO_AHEAD), threads = (step * per_head + 31) / 32 * 32;
   const dim3 grid((unsigned)((long long)groups * a.splits));
-  return wide ? launch_pdl(rotary_kernel<T, 16 / (int)sizeof(T)>, grid, dim3(RO_THREADS), 0, st, 0, a)
-              : launch_pdl(rotary_kernel<T, 1>, grid, dim3(RO_THREADS), 0, st, 0, a);
+  return wide ? launch_pdl(rotary_kernel<T, 16 / (int)sizeof(T)>, grid, dim3(threads), 0, st, 0, a)
+              : launch_pdl(rotary_kernel<T, 1>, grid, dim3(threads), 0, st, 0, a);
 }
 
 bool finite_positive(double x) { return x > 0 && isfinite(x); }
