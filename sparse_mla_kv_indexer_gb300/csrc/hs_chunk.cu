@@ -169,11 +169,13 @@ struct PlanBlock {
   int4 a, b;
 };
 constexpr int CK_NO_CAP = 0x7FFFFFFF;
-struct SharedHead {
-  int n_blocks, cost, per_pair, pad;
+constexpr int PP_BLOCK_COST = 4;   // what a listed block costs besides its pages (3: 394 us for 64 tokens behind 32,768 rows, 4: 386, 7: 390)
+struct PairStart {     // a pair's range: its first block (and its index), how far into its cost it starts, its units of cost
+  int block, into, n, pad;
+  PlanBlock first;
 };
 struct SharedWork {
-  SharedHead* head;
+  PairStart* start;    // [pairs]
   PlanBlock* blocks;   // [max_blocks]
   int2* of_token;      // [tokens]: what is to be joined of its blocks of shared positions, and of its own (ToJoin)
   float2* stats;       // as of ChunkWork
@@ -192,7 +194,7 @@ __host__ __device__ inline SharedWork shared_at(void* base, int pairs, int64_t t
     at += up256(bytes);
     return b + here;
   };
-  w.head = reinterpret_cast<SharedHead*>(take(sizeof(SharedHead)));
+  w.start = reinterpret_cast<PairStart*>(take(pairs * (int64_t)sizeof(PairStart)));
   w.blocks = reinterpret_cast<PlanBlock*>(take(max_blocks * (int64_t)sizeof(PlanBlock)));
   w.of_token = reinterpret_cast<int2*>(take(tokens * 8));
   w.stats = reinterpret_cast<float2*>(take(pairs * CK_SLOT_ROWS * 8));
@@ -652,29 +654,6 @@ __device__ Range plan_range_warp(const Dev& D, const ChunkArgs& A, int pair, int
   return r;
 }
 
-// SHARED: the blocks are listed in the workspace. This pair's range, by one warp.
-__device__ Range plan_range_listed(const ChunkArgs& A, const SharedWork& W, int pair) {
-  const int lane = threadIdx.x & 31;
-  const SharedHead head = *W.head;
-  Range r = {};
-  r.per_pair = head.per_pair;
-  r.at = pair * head.per_pair;
-  r.n = max(0, min(head.per_pair, head.cost - r.at));
-  if (r.n == 0) return r;
-  // the last block whose cost begins at or before the range's: 32 probes at a time
-  int lo = 0, n = head.n_blocks;
-  while (n > 1) {
-    const int step = (n + 31) / 32, probe = lo + lane * step;
-    const bool in = lane * step < n && W.blocks[probe].b.w <= r.at;
-    const int last = 31 - __clz(__ballot_sync(0xffffffffu, in));   // of lane 0 it holds: its block begins at or before
-    n = min(step, n - last * step);
-    lo += last * step;
-  }
-  r.seg = lo;   // here the block
-  r.into = r.at - W.blocks[lo].b.w;
-  return r;
-}
-
 template <typename T, bool SHARED>
 __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const Dev D, const ChunkArgs A) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -742,9 +721,12 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
     const uint8_t* const kv = D.kv[A.layer];
     WarpPlan mine = {};
     SharedWork W = {};
+    PlanBlock next = {};   // SHARED: the block `seg`, the workspace's list read one block ahead
     if constexpr (SHARED) {
       W = shared_work(A, H);
-      R = plan_range_listed(A, W, pair);
+      const PairStart s = W.start[pair];
+      R.seg = s.block, R.into = s.into, R.n = s.n;
+      next = s.first;
     } else {
       if (A.small) R = plan_range_warp(D, A, pair, tpb, mine);
     }
@@ -757,9 +739,9 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
       int4 pa = make_int4(0, -1, -1, 0), pb = make_int4(0, 0, -1, 0);
       if constexpr (SHARED) {
         while (left > 0 && pa.y < 0) {
-          const PlanBlock B = W.blocks[seg++];
-          const int pages = B.b.y - B.b.x, end = min(pages > 0 ? CK_BLOCK_COST + pages : 0, into + left);
-          const int p0 = max(into - CK_BLOCK_COST, 0), p1 = max(end - CK_BLOCK_COST, 0);
+          const PlanBlock B = next;
+          const int pages = B.b.y - B.b.x, end = min(pages > 0 ? PP_BLOCK_COST + pages : 0, into + left);
+          const int p0 = max(into - PP_BLOCK_COST, 0), p1 = max(end - PP_BLOCK_COST, 0);
           if (p1 > p0) {
             const bool whole = p0 == 0 && p1 == pages;
             const int kind = B.b.z != CK_NO_CAP ? 2 : B.b.x > 0 ? 3 : -1;
@@ -768,6 +750,8 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
           }
           left -= end - into;
           into = 0;
+          ++seg;
+          if (left > 0) next = W.blocks[seg];
         }
       }
       while (!SHARED && left > 0 && pa.y < 0) {   // the range's next pages: none of a block whose fixed cost it ends in
@@ -1519,39 +1503,47 @@ hs_status launch_attention_pairs(hs_pool* p, const ChunkArgs& a, cudaStream_t st
 // t_i / tpb)) blocks over them (t_i: tokens of its segments, tpb: tokens of a block), and costs each of the
 // shared blocks its queries and its sums once more: PP_JOIN pages. A group that saves less, like long
 // segments of 64 heads whose blocks are full anyway, is read by each segment alone.
-constexpr int PP_THREADS = 1024;
 constexpr int PP_JOIN = 8;
-// shared memory, in ints: starts [n_seg + 1], the shared pages of each segment [n_seg], group starts
-// [n_groups + 1], the segment through whose request each group reads [n_groups], blocks before each unit
-// [n_groups + n_seg + 1]
-inline int plan_ints(int n_seg, int n_groups) { return 3 * n_seg + 3 * n_groups + 3; }
+constexpr int PP_LIMITS = 4096;    // limits of so many tokens are kept in shared memory
+constexpr int PP_FEW = 256;        // segments, groups and blocks of as many threads: 256 instead of 1,024
+// shared memory, in ints: segment starts [n_seg + 1], requests [n_seg] and shared pages [n_seg], group starts
+// [n_groups + 1], lengths [n_groups] and the segment through whose request each group reads [n_groups], blocks before
+// each unit [n_groups + n_seg + 1], limits
+inline int plan_ints(int n_seg, int n_groups, int n_tok) {
+  return 4 * n_seg + 4 * n_groups + 3 + (n_tok <= PP_LIMITS ? n_tok : 0);
+}
 
-// The ascending values v[0 .. n) clamped to [0, most] and to ascend, into dst. All threads; *bad: some were not.
-__device__ void clamp_starts(int* dst, const int32_t* v, int n, int most, int* tmp, bool* bad) {
+// Clamps the values v[0 .. n) to [0, most] and to ascend. All threads; returns whether some of this thread's were not.
+template <int THREADS>
+__device__ __forceinline__ bool clamp_starts(int* v, int n, int most, int* tmp) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  bool bad = false;
   int before = 0;
-  for (int base = 0; base < n; base += PP_THREADS) {
-    const int i = base + threadIdx.x, s = i < n ? __ldg(v + i) : 0, c = min(max(s, 0), most);
-    int m = c;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int base = 0; base < n; base += THREADS) {
+    const int i = base + threadIdx.x, s = i < n ? v[i] : 0;
+    int m = min(max(s, 0), most);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int u = __shfl_up_sync(0xffffffffu, m, o);
       if (lane >= o) m = max(m, u);
     }
-    __syncthreads();
     if (lane == 31) tmp[warp] = m;
     __syncthreads();
-    for (int w = 0; w < warp; ++w) m = max(m, tmp[w]);
-    m = max(m, before);
-    for (int w = 0; w < 32; ++w) before = max(before, tmp[w]);
+    int w = lane < THREADS / 32 ? tmp[lane] : 0;
+    const int all = __reduce_max_sync(0xffffffffu, w);
+    if (lane >= warp) w = 0;
+    m = max(max(m, before), __reduce_max_sync(0xffffffffu, w));
+    before = max(before, all);
     if (i < n) {
-      *bad |= s != m;
-      dst[i] = m;
+      bad |= s != m;
+      v[i] = m;
     }
+    __syncthreads();
   }
-  __syncthreads();
+  return bad;
 }
-// Exclusive sum over the CTA's threads; *total the whole. Barriers on both sides.
+// Exclusive sum over the CTA's threads; *total the whole.
+template <int THREADS>
 __device__ __forceinline__ int plan_scan(int v, int* tmp, int* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int s = v;
@@ -1560,17 +1552,13 @@ __device__ __forceinline__ int plan_scan(int v, int* tmp, int* total) {
     const int u = __shfl_up_sync(0xffffffffu, s, o);
     if (lane >= o) s += u;
   }
-  __syncthreads();
   if (lane == 31) tmp[warp] = s;
   __syncthreads();
-  int w = tmp[lane];
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int u = __shfl_up_sync(0xffffffffu, w, o);
-    if (lane >= o) w += u;
-  }
-  *total = __shfl_sync(0xffffffffu, w, 31);
-  return s - v + (warp > 0 ? __shfl_sync(0xffffffffu, w, warp - 1) : 0);
+  const int w = lane < THREADS / 32 ? tmp[lane] : 0;
+  *total = __reduce_add_sync(0xffffffffu, w);
+  const int ahead = __reduce_add_sync(0xffffffffu, lane < warp ? w : 0);
+  __syncthreads();
+  return s - v + ahead;
 }
 
 // Where the parts of one of a token's blocks lie, in one word (0: there are none, or the attention wrote the
@@ -1583,53 +1571,68 @@ struct ToJoin {
 __device__ __forceinline__ int join_word(const ToJoin& j) { return j.n | j.first << 12 | j.place << 24 | (j.whole ? 1 << 30 : 0); }
 __device__ __forceinline__ ToJoin join_of(int w) { return {w & 0xFFF, w >> 12 & 0xFFF, w >> 24 & 0xF, (w >> 30 & 1) != 0}; }
 
-__global__ void __launch_bounds__(PP_THREADS, 1) prefix_plan_kernel(const Dev D, const ChunkArgs A) {
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS, 1) prefix_plan_kernel(const Dev D, const ChunkArgs A) {
   extern __shared__ int plan[];
   __shared__ int tmp[32];
   griddep_wait();
   griddep_launch();   // only the attention of this call depends on it, and waits for its end
   const int tid = threadIdx.x, tpb = CK_ROWS / D.n_heads, units = A.n_groups + A.n_seg;
   int* const start = plan;
-  int* const shared = start + A.n_seg + 1;
+  int* const req = start + A.n_seg + 1;
+  int* const shared = req + A.n_seg;
   int* const group = shared + A.n_seg;
-  int* const reader = group + A.n_groups + 1;
+  int* const length = group + A.n_groups + 1;
+  int* const reader = length + A.n_groups;
   int* const before = reader + A.n_groups;
+  int* const limits = before + units + 1;
+  const bool kept = A.n_tok <= PP_LIMITS;
   const SharedWork W = shared_work(A, D.n_heads);
-  bool bad = false;
-  for (int j = tid; j < A.n_tok; j += PP_THREADS) W.of_token[j] = make_int2(0, 0);
-  for (int i = tid; i < A.n_seg; i += PP_THREADS) shared[i] = 0;
-  clamp_starts(start, A.seg_start, A.n_seg + 1, A.n_tok, tmp, &bad);
-  if (A.n_groups > 0) clamp_starts(group, A.group_start, A.n_groups + 1, A.n_seg, tmp, &bad);
+  // everything that the plan goes by, read at once
+  for (int i = tid; i <= A.n_seg; i += THREADS) {
+    start[i] = __ldg(A.seg_start + i);
+    if (i < A.n_seg) req[i] = __ldg(A.seg_req + i), shared[i] = 0;
+  }
+  if (A.n_groups > 0)
+    for (int i = tid; i <= A.n_groups; i += THREADS) {
+      group[i] = __ldg(A.group_start + i);
+      if (i < A.n_groups) length[i] = __ldg(A.group_len + i);
+    }
+  if (kept)
+    for (int j = tid; j < A.n_tok; j += THREADS) limits[j] = __ldg(A.limit + j);
+  for (int j = tid; j < A.n_tok; j += THREADS) W.of_token[j] = make_int2(0, 0);
+  __syncthreads();
+  bool bad = clamp_starts<THREADS>(start, A.n_seg + 1, A.n_tok, tmp);
+  if (A.n_groups > 0) bad |= clamp_starts<THREADS>(group, A.n_groups + 1, A.n_seg, tmp);
   auto blocks_of = [&](int tokens) { return (tokens + tpb - 1) / tpb; };
   // the groups that share, a warp each
-  for (int g = tid >> 5; g < A.n_groups; g += PP_THREADS / 32) {
-    const int lane = tid & 31, s0 = group[g], s1 = group[g + 1], len = __ldg(A.group_len + g);
+  for (int g = tid >> 5; g < A.n_groups; g += THREADS / 32) {
+    const int lane = tid & 31, s0 = group[g], s1 = group[g + 1], len = length[g];
     const bool fits = len >= 0 && len <= D.max_ctx;
     bad |= !fits;
     int alone = 0, first = A.n_seg;
     bool valid = true;   // a segment of a bad request sees nothing, and so shares nothing
     for (int i = s0 + lane; i < s1; i += 32) {
-      const int n = blocks_of(start[i + 1] - start[i]), r = __ldg(A.seg_req + i);
+      const int n = blocks_of(start[i + 1] - start[i]), r = req[i];
       alone += n;
       if (n > 0) first = min(first, i), valid &= r >= 0 && r < D.max_requests;
     }
     alone = __reduce_add_sync(0xffffffffu, alone);
     first = __reduce_min_sync(0xffffffffu, first);
     valid = __all_sync(0xffffffffu, valid);
-    if (lane == 0) reader[g] = first;
     const int together = blocks_of(start[s1] - start[s0]), pages = fits && valid ? len / PAGE : 0;
     const bool pays = (long long)(alone - together) * pages > (long long)together * PP_JOIN;
-    if (lane == 0) before[g] = pays ? together : 0;
+    if (lane == 0) reader[g] = first, before[g] = pays ? together : 0;
     if (pays)
       for (int i = s0 + lane; i < s1; i += 32) shared[i] = pages;
   }
-  for (int i = tid; i < A.n_seg; i += PP_THREADS) before[A.n_groups + i] = blocks_of(start[i + 1] - start[i]);
+  for (int i = tid; i < A.n_seg; i += THREADS) before[A.n_groups + i] = blocks_of(start[i + 1] - start[i]);
   __syncthreads();
   int n_blocks = 0;
-  for (int base = 0; base < units; base += PP_THREADS) {
+  for (int base = 0; base < units; base += THREADS) {
     const int u = base + tid, v = u < units ? before[u] : 0;
     int sum;
-    const int at = plan_scan(v, tmp, &sum);
+    const int at = plan_scan<THREADS>(v, tmp, &sum);
     if (u < units) before[u] = n_blocks + at;
     n_blocks += sum;
   }
@@ -1637,25 +1640,29 @@ __global__ void __launch_bounds__(PP_THREADS, 1) prefix_plan_kernel(const Dev D,
   __syncthreads();
   int cost = 0;
   PlanBlock B;
-  for (int base = 0; base < n_blocks; base += PP_THREADS) {
+  for (int base = 0; base < n_blocks; base += THREADS) {
     const int b = base + tid;
     B = {make_int4(0, 0, -1, 0), make_int4(0, 0, CK_NO_CAP, 0)};
-    bool of_group = false;
     if (b < n_blocks) {
       int l = 0, h = units;   // the last unit whose first block is <= b (never one without blocks)
       while (h - l > 1) {
         const int mid = (l + h) >> 1;
         if (before[mid] <= b) l = mid; else h = mid;
       }
-      of_group = l < A.n_groups;
+      const bool of_group = l < A.n_groups;
       const int seg = of_group ? reader[l] : l - A.n_groups, end = start[of_group ? group[l + 1] : seg + 1];
-      const int pages = shared[seg], r = __ldg(A.seg_req + seg);
+      const int pages = shared[seg], r = req[seg];
       const bool bad_req = r < 0 || r >= D.max_requests;
       bad |= bad_req;
       B.a.x = start[seg] + (b - before[l]) * tpb;
       B.a.y = min(tpb, end - B.a.x);
       B.a.z = bad_req ? -1 : r;
-      const int lim = block_limit(D, A.limit, B.a.x, B.a.x + B.a.y, &bad);
+      int lim = 0;
+      if (kept) {
+        for (int j = 0; j < B.a.y; ++j) lim = max(lim, clamp_limit(D, limits[B.a.x + j], &bad));
+      } else {
+        lim = block_limit(D, A.limit, B.a.x, B.a.x + B.a.y, &bad);
+      }
       if (of_group) {
         B.b.y = min(pages, pages_of(lim));
         B.b.z = pages * PAGE;
@@ -1668,21 +1675,24 @@ __global__ void __launch_bounds__(PP_THREADS, 1) prefix_plan_kernel(const Dev D,
     }
     const int n = B.b.y - B.b.x;
     int sum;
-    B.b.w = cost + plan_scan(n > 0 ? CK_BLOCK_COST + n : 0, tmp, &sum);
+    B.b.w = cost + plan_scan<THREADS>(n > 0 ? PP_BLOCK_COST + n : 0, tmp, &sum);
     cost += sum;
     if (b < n_blocks) W.blocks[b] = B;
   }
   if (bad) set_status(D.status, HS_ERR_BAD_ID);
   const int per_pair = max((cost + A.pairs - 1) / A.pairs, CK_MIN_COST);
-  if (tid == 0) *W.head = {n_blocks, cost, per_pair, 0};
-  // what is joined of each token, now that the ranges are known: the last blocks first, which are at hand
-  for (int base = (n_blocks - 1) / PP_THREADS * PP_THREADS, last = base; base >= 0; base -= PP_THREADS) {
+  for (int p = tid; p < A.pairs; p += THREADS)
+    if (p * per_pair >= cost) W.start[p] = {0, 0, 0, 0, {make_int4(0, 0, -1, 0), make_int4(0, 0, CK_NO_CAP, 0)}};
+  // the ranges that begin in each block, and what is joined of its tokens: the last blocks first, which are at hand
+  for (int base = (n_blocks - 1) / THREADS * THREADS, last = base; base >= 0; base -= THREADS) {
     const int b = base + tid;
     if (b >= n_blocks) continue;
     if (base != last) B = W.blocks[b];
     const int pages = B.b.y - B.b.x;
     if (pages <= 0) continue;
-    const int c = B.b.w + CK_BLOCK_COST, first = c / per_pair, n = (c + pages - 1) / per_pair - first + 1;
+    for (int p = (B.b.w + per_pair - 1) / per_pair; p * per_pair < B.b.w + PP_BLOCK_COST + pages; ++p)
+      W.start[p] = {b, p * per_pair - B.b.w, min(per_pair, cost - p * per_pair), 0, B};
+    const int c = B.b.w + PP_BLOCK_COST, first = c / per_pair, n = (c + pages - 1) / per_pair - first + 1;
     const bool of_group = B.b.z != CK_NO_CAP;
     if (n == 1 && !of_group && B.b.x == 0) continue;
     for (int j = 0; j < B.a.y; ++j)
@@ -1783,9 +1793,14 @@ int prefix_blocks(int n_tok, int n_seg, int n_groups, int tpb) { return n_seg + 
 constexpr int PM_WIDE_ROWS = 1024;
 template <typename T>
 hs_status launch_prefix(hs_pool* p, const ChunkArgs& a, cudaStream_t st) {
-  const int smem = plan_ints(a.n_seg, a.n_groups) * 4;
-  if (ensure_kernel_attrs(prefix_plan_kernel, smem) != HS_OK) return HS_ERR_CUDA;
-  hs_status s = launch_pdl(prefix_plan_kernel, dim3(1), dim3(PP_THREADS), smem, st, 0, p->d, a);
+  const int smem = plan_ints(a.n_seg, a.n_groups, a.n_tok) * 4;
+  hs_status s;
+  if (a.max_blocks <= PP_FEW) {
+    s = launch_pdl(prefix_plan_kernel<256>, dim3(1), dim3(256), smem, st, 0, p->d, a);
+  } else {
+    s = ensure_kernel_attrs(prefix_plan_kernel<1024>, smem);
+    if (s == HS_OK) s = launch_pdl(prefix_plan_kernel<1024>, dim3(1), dim3(1024), smem, st, 0, p->d, a);
+  }
   if (s == HS_OK) s = launch_attention_pairs<T, true>(p, a, st);
   if (s != HS_OK) return s;
   const int rows = a.n_tok * p->cfg.n_heads, most = 2 * num_sms();   // resident at once

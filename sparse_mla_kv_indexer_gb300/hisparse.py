@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import sys
 from typing import Optional, Sequence
 
@@ -71,6 +72,10 @@ class RotaryPart(ctypes.Structure):
                [("heads", ctypes.c_int32), ("layout", ctypes.c_int32)]
 
 
+_ROTARY_PART = struct.Struct("=QQqqqqii")   # RotaryPart in one call: each field set by itself takes longer than the kernel
+assert _ROTARY_PART.size == ctypes.sizeof(RotaryPart)
+
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int32
 _L = ctypes.c_int64
@@ -95,7 +100,7 @@ _SIGS = {
     "hs_chunk_attention": [_P, _I, _I, _P, _P, _I, _P, _I, _P, _L, _L, ctypes.c_float, _P, _L, _L, _P, _P, _L, _P],
     "hs_rotary_steps": [ctypes.POINTER(RotaryConfig), _P, ctypes.POINTER(ctypes.c_float)],
     "hs_rotary_steps_of": [_I, _P, _P],
-    "hs_rotary": [_P, _I, _P, _I, _P, ctypes.c_float, _I, _I, _I, ctypes.POINTER(RotaryPart), _P],
+    "hs_rotary": [_P, _I, _P, _I, _P, ctypes.c_float, _I, _I, _I, _P, _P],
     "hs_fork_requests": [_P, _I, _P, _P, _P, _P, _P, _P],
     "hs_copy_pages": [_P, _I, _P, _P, _I, _P, _P, _I, _P],
     "hs_get_pages": [_P, _I, _P, _I, _I, _P, _P, _P, _P],
@@ -419,28 +424,36 @@ class Pool:
         first = parts[0][0]
         code, dtype, n, dev = _dtype(first), first.dtype, pos.shape[0], self._device()
         dims = first.shape[-1]
-        args = (RotaryPart * len(parts))()
-        for a, (x, out, layout) in zip(args, parts):
+        packed = bytearray(_ROTARY_PART.size * len(parts))
+        at = 0
+        for x, out, layout in parts:
             shape, xs, os = x.shape, x.stride(), out.stride()
-            if len(shape) not in (2, 3) or shape[0] != n or shape[-1] != dims or out.shape != shape:
+            if out.shape != shape or shape[0] != n or shape[-1] != dims:
                 raise ValueError(f"x and out [{n}, heads, {dims}] or [{n}, {dims}] of one shape are wanted")
+            if len(xs) == 3:
+                heads, xh, oh = shape[1], xs[1], os[1]
+                if heads == 1:
+                    xh = oh = dims
+            elif len(xs) == 2:
+                heads, xh, oh = 1, dims, dims
+            else:
+                raise ValueError(f"x and out [{n}, heads, {dims}] or [{n}, {dims}] are wanted")
             if x.dtype is not dtype or out.dtype is not dtype:
                 raise ValueError("all parts of one element type are wanted")
-            if (xs[-1] != 1 or os[-1] != 1) and dims > 1:
+            if xs[-1] != 1 or os[-1] != 1:
                 raise ValueError("x and out: a contiguous last dimension is wanted")
             if x.get_device() != dev or out.get_device() != dev:
                 raise ValueError(f"x or out is not on the pool's device, cuda:{dev}")
             if layout not in ROTARY_LAYOUTS:
                 raise ValueError(f"layout {layout!r}: pairs or halves is wanted")
-            heads = shape[1] if len(shape) == 3 else 1
-            a.d_in, a.d_out, a.heads, a.layout = x.data_ptr(), out.data_ptr(), heads, ROTARY_LAYOUTS[layout]
-            a.in_stride_token, a.out_stride_token = (xs[0], os[0]) if n > 1 else (dims, dims)
-            a.in_stride_head, a.out_stride_head = (xs[1], os[1]) if heads > 1 else (dims, dims)
+            xt, ot = (xs[0], os[0]) if n > 1 else (dims, dims)
+            _ROTARY_PART.pack_into(packed, at, x.data_ptr(), out.data_ptr(), xt, xh, ot, oh, heads, ROTARY_LAYOUTS[layout])
+            at += _ROTARY_PART.size
         if steps.shape != (dims // 2,) or steps.dtype not in _Torch.steps or not steps.is_contiguous():
             raise ValueError(f"steps: a contiguous int64 tensor of {dims // 2} elements is wanted")
         _on("steps", steps, dev)
         _check("hs_rotary", lib.hs_rotary(self.handle, n, _ids("pos", pos, n, dev), dims, steps.data_ptr(), magnitude,
-                                          1 if inverse else 0, code, len(parts), args, _stream_of(stream, dev)))
+                                          1 if inverse else 0, code, len(parts), bytes(packed), _stream_of(stream, dev)))
 
     def fork_requests(self, src, dst, length, tail_pages, tail_idx_pages=None, stream=None) -> None:
         """Begin requests dst[i] with the first length[i] positions of src[i]: whole pages shared, the rows of
