@@ -151,6 +151,15 @@ struct ChunkWork {
   float* part;       // [pairs][2][128][512]
 };
 constexpr int64_t CK_SLOT_ROWS = 2 * CK_ROWS;
+// Where four output dims (4 c4 .. + 3) of a row lie among its slot's, in 16 bytes: groups of eight rows, in them every
+// c4's rows of one CTA next to one another. A warp of the attention, which has every other row, then stores 64
+// contiguous bytes for four of its lanes (16 bytes of 32 rows' own lines took 6 us when all SMs wrote their cut blocks
+// at once, now XXX), and the joins read four rows at a time.
+__device__ __forceinline__ size_t part_unit(size_t row, int c4) {
+  return ((row >> 3) * 128 + c4) * 8 + (row & 1) * 4 + ((row >> 1) & 3);
+}
+// The j-th row of four that are next to one another.
+__device__ __forceinline__ int quad_row(int four, int j) { return (four >> 1) * 8 + (four & 1) + 2 * j; }
 __host__ __device__ inline int64_t work_stats_at(int pairs) { return ((int64_t)pairs * 16 + 255) / 256 * 256; }
 __host__ __device__ inline int64_t work_part_at(int pairs) { return work_stats_at(pairs) + (int64_t)pairs * CK_SLOT_ROWS * 8; }
 inline int64_t work_bytes_for(int pairs) { return work_part_at(pairs) + (int64_t)pairs * CK_SLOT_ROWS * 512 * 4; }
@@ -1357,16 +1366,15 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
           part = W.part;
           stats = W.stats;
         }
-        float* dst = part + at * 512 + dim;
+        uint4* const dst = reinterpret_cast<uint4*>(part) + part_unit(at, dim / 4);
 #pragma unroll 1
         for (int c = 0; c < 128; c += 16) {
           uint32_t o[16];
           tmem_ld16(o_col + c, o);
           tmem_wait_ld();
           if (live) {
-            uint4* d = reinterpret_cast<uint4*>(dst + c);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) d[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+            for (int j = 0; j < 4; ++j) dst[(c / 4 + j) * 8] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
           }
         }
         if (live && dim == 0) stats[at] = make_float2(m, l);
@@ -1389,19 +1397,21 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
 }
 
 // The rows of cut blocks: out = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i over the parts,
-// in pair order. A CTA has four slices of 128 threads. WIDE (few cuts, of many parts each): CTA
-// (row, k) joins that row of the k-th cut, its parts dealt to the slices. Otherwise each slice
-// joins one row of one pair's cut.
+// in pair order, for four rows that lie next to one another at a time. WIDE (few cuts, of many parts
+// each): CTA (four rows and a quarter of their dims, k) of the k-th cut, its parts dealt to four slices of
+// 128 threads. Otherwise CTA (four rows, p) of the cut of pair p.
 constexpr int CM_SLICES = 4, CM_THREADS = 128 * CM_SLICES, CM_WIDE_CUTS = 32;
 template <typename T, bool WIDE>
 __global__ void __launch_bounds__(CM_THREADS) chunk_merge_kernel(const Dev D, const ChunkArgs A) {
   __shared__ float4 acc[CM_SLICES][128];
-  __shared__ float2 ml[CM_SLICES];
+  __shared__ float2 ml[CM_SLICES][4];
   __shared__ int mine;
   griddep_wait();
   const ChunkWork W = work_at(A.work, A.pairs);
-  const int tid = threadIdx.x, slice = tid >> 7, col = tid & 127, row = blockIdx.x, H = D.n_heads;
-  int p = blockIdx.y * CM_SLICES + slice;
+  const int tid = threadIdx.x, slice = WIDE ? tid >> 7 : 0, H = D.n_heads;
+  const int col = WIDE ? (blockIdx.x & 3) * 32 + (tid >> 2 & 31) : tid >> 2;
+  const int row = quad_row(WIDE ? blockIdx.x >> 2 : blockIdx.x, tid & 3);
+  int p = blockIdx.y;
   if (WIDE) {   // the blockIdx.y-th pair that has a cut
     if (tid == 0) mine = A.pairs;
     __syncthreads();
@@ -1417,11 +1427,9 @@ __global__ void __launch_bounds__(CM_THREADS) chunk_merge_kernel(const Dev D, co
     __syncthreads();
     p = mine;
     if (p >= A.pairs) return;
-  } else if (p >= A.pairs) {
-    return;
   }
   const ChunkCut cut = W.cut[p];
-  if (row >= cut.n_tok * H) return;
+  if (row >= cut.n_tok * H) return;   // all of the CTA's rows, or none
   auto part_at = [&](int i) { return ((size_t)i * 2 + (i == p ? 1 : 0)) * CK_ROWS + row; };
   const int step = WIDE ? CM_SLICES : 1;
   float m = -INFINITY, l = 0.f;
@@ -1434,7 +1442,7 @@ __global__ void __launch_bounds__(CM_THREADS) chunk_merge_kernel(const Dev D, co
     for (int u = 0; u < 8; ++u) {
       const bool in = i + u * step <= cut.last_pair;
       s[u] = in ? W.stats[part_at(i + u * step)] : make_float2(-INFINITY, 0.f);
-      v[u] = in ? *(reinterpret_cast<const float4*>(W.part + part_at(i + u * step) * 512) + col) : make_float4(0.f, 0.f, 0.f, 0.f);
+      v[u] = in ? reinterpret_cast<const float4*>(W.part)[part_unit(part_at(i + u * step), col)] : make_float4(0.f, 0.f, 0.f, 0.f);
     }
     float mn = m;
 #pragma unroll
@@ -1452,19 +1460,20 @@ __global__ void __launch_bounds__(CM_THREADS) chunk_merge_kernel(const Dev D, co
     }
   }
   if (WIDE) {
-    acc[slice][col] = o;
-    if (col == 0) ml[slice] = make_float2(m, l);
+    const int j = tid & 3;
+    acc[slice][tid & 127] = o;
+    if ((tid & 127) < 4) ml[slice][j] = make_float2(m, l);
     __syncthreads();
     if (slice > 0) return;
-    m = fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x));
+    m = fmaxf(fmaxf(ml[0][j].x, ml[1][j].x), fmaxf(ml[2][j].x, ml[3][j].x));
     l = 0.f;
     o = make_float4(0.f, 0.f, 0.f, 0.f);
     if (m > -INFINITY) {
 #pragma unroll
       for (int u = 0; u < CM_SLICES; ++u) {
-        const float w = exp2f(ml[u].x - m);
-        const float4 v = acc[u][col];
-        l += w * ml[u].y;
+        const float w = exp2f(ml[u][j].x - m);
+        const float4 v = acc[u][tid];
+        l += w * ml[u][j].y;
         o.x += w * v.x, o.y += w * v.y, o.z += w * v.z, o.w += w * v.w;
       }
     }
@@ -1701,23 +1710,25 @@ __global__ void __launch_bounds__(THREADS, 1) prefix_plan_kernel(const Dev D, co
 }
 
 // Joins what the blocks of a token left in the workspace, in the order of its blocks and pairs: of a token
-// with two blocks both, of one with a cut block its parts. A slice of 128 threads has a row; WIDE (few rows, of
-// many parts each) deals a row's parts to a CTA's four slices. The CTAs go through the tasks in steps of the
-// grid and look up 32 tokens at a time, for most may have nothing to join.
+// with two blocks both, of one with a cut block its parts. A CTA has four rows of a token that lie next to one
+// another; WIDE (few rows, of many parts each) a quarter of their dims, the parts dealt to four slices of 128
+// threads. The CTAs go through the tasks in steps of the grid and look up 32 tokens at a time, for most may have
+// nothing to join.
 constexpr int PM_AHEAD = 6;   // parts whose loads are in flight
 template <typename T, bool WIDE>
 __global__ void __launch_bounds__(CM_THREADS, 2) prefix_merge_kernel(const Dev D, const ChunkArgs A) {
   __shared__ float4 acc[WIDE ? CM_SLICES : 1][128];
-  __shared__ float2 ml[CM_SLICES];
+  __shared__ float2 ml[CM_SLICES][4];
   griddep_wait();
-  const int tid = threadIdx.x, slice = tid >> 7, col = tid & 127, lane = tid & 31, H = D.n_heads;
+  const int tid = threadIdx.x, slice = WIDE ? tid >> 7 : 0, quad = tid & 3, lane = tid & 31, H = D.n_heads;
   const SharedWork W = shared_work(A, H);
-  const int per_task = WIDE ? 1 : CM_SLICES, per_token = H / per_task, tasks = A.n_tok * per_token, rows = A.n_tok * H;
+  const int per_token = WIDE ? H : H / 4, tasks = A.n_tok * per_token, rows = A.n_tok * H;
   for (int base = blockIdx.x; base < tasks; base += 32 * gridDim.x) {
     const int mine = base + lane * gridDim.x;
     const int2 of = mine < tasks ? W.of_token[mine / per_token] : make_int2(0, 0);
     for (unsigned todo = __ballot_sync(0xffffffffu, (of.x | of.y) != 0); todo; todo &= todo - 1) {
-      const int k = __ffs(todo) - 1, task = base + k * gridDim.x, row = task * per_task + (WIDE ? 0 : slice);
+      const int k = __ffs(todo) - 1, task = base + k * gridDim.x, row = quad_row(WIDE ? task >> 2 : task, quad);
+      const int col = WIDE ? (task & 3) * 32 + (tid >> 2 & 31) : tid >> 2;
       const ToJoin x = join_of(__shfl_sync(0xffffffffu, of.x, k)), y = join_of(__shfl_sync(0xffffffffu, of.y, k));
       const int tok = task / per_token, h = row - tok * H, n = x.n + y.n;
       const int step = WIDE ? CM_SLICES : 1;
@@ -1737,7 +1748,7 @@ __global__ void __launch_bounds__(CM_THREADS, 2) prefix_merge_kernel(const Dev D
           const size_t at = whole ? (size_t)(shared ? 0 : rows) + row
                                   : ((size_t)(first + j) * 2 + (j == 0 ? 1 : 0)) * CK_ROWS + place * H + h;
           s[u] = (whole ? W.whole_stats : W.stats)[at];
-          v[u] = *(reinterpret_cast<const float4*>((whole ? W.whole : W.part) + at * 512) + col);
+          v[u] = reinterpret_cast<const float4*>(whole ? W.whole : W.part)[part_unit(at, col)];
         }
         float mn = m;
 #pragma unroll
@@ -1755,19 +1766,19 @@ __global__ void __launch_bounds__(CM_THREADS, 2) prefix_merge_kernel(const Dev D
         }
       }
       if (WIDE) {
-        acc[slice][col] = o;
-        if (col == 0) ml[slice] = make_float2(m, l);
+        acc[slice][tid & 127] = o;
+        if ((tid & 127) < 4) ml[slice][quad] = make_float2(m, l);
         __syncthreads();
         if (slice == 0) {
-          m = fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x));
+          m = fmaxf(fmaxf(ml[0][quad].x, ml[1][quad].x), fmaxf(ml[2][quad].x, ml[3][quad].x));
           l = 0.f;
           o = make_float4(0.f, 0.f, 0.f, 0.f);
           if (m > -INFINITY) {
 #pragma unroll
             for (int u = 0; u < CM_SLICES; ++u) {
-              const float w = exp2f(ml[u].x - m);
-              const float4 v = acc[u][col];
-              l += w * ml[u].y;
+              const float w = exp2f(ml[u][quad].x - m);
+              const float4 v = acc[u][tid];
+              l += w * ml[u][quad].y;
               o.x += w * v.x, o.y += w * v.y, o.z += w * v.z, o.w += w * v.w;
             }
           }
@@ -1807,7 +1818,7 @@ hs_status launch_prefix(hs_pool* p, const ChunkArgs& a, cudaStream_t st) {
   const auto grid = [&](int tasks) { return dim3(tasks < most ? tasks : most); };
   if (rows <= PM_WIDE_ROWS)
     return launch_pdl(prefix_merge_kernel<T, true>, grid(rows), dim3(CM_THREADS), 0, st, 0, p->d, a);
-  return launch_pdl(prefix_merge_kernel<T, false>, grid(rows / CM_SLICES), dim3(CM_THREADS), 0, st, 0, p->d, a);
+  return launch_pdl(prefix_merge_kernel<T, false>, grid(rows / 4), dim3(CM_THREADS), 0, st, 0, p->d, a);
 }
 
 bool stride_ok(int64_t s, int64_t least) { return s >= least && s < (1ll << 40) && s % 8 == 0; }
@@ -1845,8 +1856,7 @@ hs_status launch_chunk(hs_pool* p, const ChunkArgs& a, cudaStream_t st) {
   const int grid_rows = rows < CK_ROWS ? (int)rows : CK_ROWS;
   if (cuts <= CM_WIDE_CUTS)
     return launch_pdl(chunk_merge_kernel<T, true>, dim3(grid_rows, cuts), dim3(CM_THREADS), 0, st, 0, p->d, a);
-  return launch_pdl(chunk_merge_kernel<T, false>, dim3(grid_rows, (a.pairs + CM_SLICES - 1) / CM_SLICES), dim3(CM_THREADS), 0,
-                    st, 0, p->d, a);
+  return launch_pdl(chunk_merge_kernel<T, false>, dim3(grid_rows / 4, a.pairs), dim3(CM_THREADS), 0, st, 0, p->d, a);
 }
 
 }  // namespace
