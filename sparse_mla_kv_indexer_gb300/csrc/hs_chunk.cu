@@ -178,7 +178,6 @@ struct PlanBlock {
   int4 a, b;
 };
 constexpr int CK_NO_CAP = 0x7FFFFFFF;
-constexpr int PP_BLOCK_COST = 4;   // what a listed block costs besides its pages (3: 394 us for 64 tokens behind 32,768 rows, 4: 386, 7: 390)
 struct PairStart {     // a pair's range: its first block (and its index), how far into its cost it starts, its units of cost
   int block, into, n, pad;
   PlanBlock first;
@@ -749,8 +748,8 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
       if constexpr (SHARED) {
         while (left > 0 && pa.y < 0) {
           const PlanBlock B = next;
-          const int pages = B.b.y - B.b.x, end = min(pages > 0 ? PP_BLOCK_COST + pages : 0, into + left);
-          const int p0 = max(into - PP_BLOCK_COST, 0), p1 = max(end - PP_BLOCK_COST, 0);
+          const int pages = B.b.y - B.b.x, end = min(pages > 0 ? CK_BLOCK_COST + pages : 0, into + left);
+          const int p0 = max(into - CK_BLOCK_COST, 0), p1 = max(end - CK_BLOCK_COST, 0);
           if (p1 > p0) {
             const bool whole = p0 == 0 && p1 == pages;
             const int kind = B.b.z != CK_NO_CAP ? 2 : B.b.x > 0 ? 3 : -1;
@@ -1684,7 +1683,7 @@ __global__ void __launch_bounds__(THREADS, 1) prefix_plan_kernel(const Dev D, co
     }
     const int n = B.b.y - B.b.x;
     int sum;
-    B.b.w = cost + plan_scan<THREADS>(n > 0 ? PP_BLOCK_COST + n : 0, tmp, &sum);
+    B.b.w = cost + plan_scan<THREADS>(n > 0 ? CK_BLOCK_COST + n : 0, tmp, &sum);
     cost += sum;
     if (b < n_blocks) W.blocks[b] = B;
   }
@@ -1699,9 +1698,9 @@ __global__ void __launch_bounds__(THREADS, 1) prefix_plan_kernel(const Dev D, co
     if (base != last) B = W.blocks[b];
     const int pages = B.b.y - B.b.x;
     if (pages <= 0) continue;
-    for (int p = (B.b.w + per_pair - 1) / per_pair; p * per_pair < B.b.w + PP_BLOCK_COST + pages; ++p)
+    for (int p = (B.b.w + per_pair - 1) / per_pair; p * per_pair < B.b.w + CK_BLOCK_COST + pages; ++p)
       W.start[p] = {b, p * per_pair - B.b.w, min(per_pair, cost - p * per_pair), 0, B};
-    const int c = B.b.w + PP_BLOCK_COST, first = c / per_pair, n = (c + pages - 1) / per_pair - first + 1;
+    const int c = B.b.w + CK_BLOCK_COST, first = c / per_pair, n = (c + pages - 1) / per_pair - first + 1;
     const bool of_group = B.b.z != CK_NO_CAP;
     if (n == 1 && !of_group && B.b.x == 0) continue;
     for (int j = 0; j < B.a.y; ++j)
