@@ -975,7 +975,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
       if (it > 0 && !ck_wait(bar(B_SD + ((it - 1) & 1)), ((it - 1) >> 1) & 1, D.status, dead)) return false;
       const T* q = static_cast<const T*>(A.q) + (long long)tok0 * A.q_tok;
       q_first();
-#pragma unroll 1
+#pragma unroll 3
       for (int k = 0; k < 18; ++k, q_next()) {
         const int gr = 2 * qr + (int)rank, tk = gr >> hs, h = gr & (H - 1);
         if (tk < n_tok) {
