@@ -53,7 +53,8 @@
  *   the indexer's d_q and d_w, the attention's d_q), the block tables and the
  *   hot-buffer state are read before that wait, so they must be final before the
  *   previous kernel started. That holds for values written by the host (copies are
- *   stream-ordered), by this library's own calls (none writes them in a kernel) and
+ *   stream-ordered), by this library's own calls (those that write them in a kernel,
+ *   hs_rotary, hs_fork_requests and hs_copy_pages, let none start before they end) and
  *   by any ordinary kernel launch, which lets no dependent start before it ends; it
  *   does not hold for a kernel that itself lets its dependents start early
  *   (griddepcontrol.launch_dependents) and writes them afterwards.
@@ -511,7 +512,7 @@ hs_status hs_fork_requests(hs_pool* pool, int32_t n, const int32_t* d_src, const
 #define HS_COPY_MAX_PAGES 4096
 
 /* Copy pool pages in every layer (d_from[i] -> d_to[i], n of them) and index pages in every indexer
- * layer (n_idx of them) in one launch. remap != 0 moves them: after the copies every entry of the
+ * layer (n_idx of them). remap != 0 moves them: after the copies every entry of the
  * block tables, of the index tables and of the hot buffers that names a page d_from[i] names
  * d_to[i], so that the pool is compacted and the pages d_from are free (row ids that were resolved
  * before name the old places). One of n and n_idx may be 0, its arrays NULL.

@@ -59,9 +59,6 @@ struct Dev {
   int32_t sel_ws_tokens;
   uint8_t* bsel;        // [bsel_tokens] BselTok: chunked selection scratch (many query tokens)
   int32_t bsel_tokens;
-  int2* page_map;       // [num_pages + num_idx_pages] (call, page): where a page went in the hs_copy_pages call of that number
-  uint8_t* copy_ok;     // [2][HS_COPY_MAX_PAGES] which of a call's copies are made
-  uint32_t* copy_epoch; // [2] number of the last call that is done, of the running one
 };
 
 enum Counter { C_RESIDENT = 0, C_HITS = 1, C_MISSES = 2, C_H2D = 3, C_D2H = 4, C_N = 8 };

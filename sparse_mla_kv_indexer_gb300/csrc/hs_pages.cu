@@ -9,6 +9,7 @@
 #include <math.h>
 
 #include "hs_chunk.cuh"
+#include "hs_pages.cuh"
 
 namespace hs {
 
@@ -132,8 +133,8 @@ __global__ void __launch_bounds__(CP_THREADS) check_copies_kernel(const Dev D, c
   griddep_wait();
   const bool kv = blockIdx.y == 0;
   const CopyList L = kv ? A.kv : A.idx;
-  const uint32_t epoch = D.copy_epoch[0] + 1;   // of this call; the second launch keeps it
-  if (blockIdx.x == 0 && kv && threadIdx.x == 0) D.copy_epoch[1] = epoch;
+  const uint32_t epoch = copy_epoch(D)[0] + 1;   // of this call; the second launch keeps it
+  if (blockIdx.x == 0 && kv && threadIdx.x == 0) copy_epoch(D)[1] = epoch;
   int32_t *const from = named, *const to = named + L.n;
   #pragma unroll 8
   for (int i = threadIdx.x; i < L.n; i += CP_THREADS) from[i] = L.from[i], to[i] = L.to[i];
@@ -154,9 +155,9 @@ __global__ void __launch_bounds__(CP_THREADS) check_copies_kernel(const Dev D, c
     chained = __reduce_or_sync(0xffffffffu, chained);
     const bool ok = f >= 0 && f < L.pages && d >= 0 && d < L.pages && dests == 1 && !chained && (!A.remap || sources == 1);
     if (lane == 0) {
-      D.copy_ok[(kv ? 0 : HS_COPY_MAX_PAGES) + i] = ok;
+      copy_made_flags(D, kv)[i] = ok;
       if (!ok) set_status(D.status, HS_ERR_BAD_ID);
-      else if (A.remap) D.page_map[(kv ? 0 : D.num_pages) + f] = make_int2((int)epoch, d);
+      else if (A.remap) page_map(D, kv)[f] = make_int2((int)epoch, d);
     }
   }
 }
@@ -187,21 +188,21 @@ __global__ void __launch_bounds__(CP_THREADS, 2) copy_pages_kernel(const Dev D, 
   griddep_wait();
   int cta = blockIdx.x;
   if (cta < A.remap_ctas) {
-    const int epoch = (int)D.copy_epoch[1];
+    const int epoch = (int)copy_epoch(D)[1];
     const long long n = (long long)D.max_requests * D.max_pages;
     if (A.kv.n > 0) {
-      remap_table(D.bt, n, D.page_map, D.num_pages, epoch, cta, A.remap_ctas);
-      remap_table(D.hot_pages, (long long)D.max_requests * D.n_groups * D.hot_pages_max, D.page_map, D.num_pages, epoch, cta, A.remap_ctas);
+      remap_table(D.bt, n, page_map(D, true), D.num_pages, epoch, cta, A.remap_ctas);
+      remap_table(D.hot_pages, (long long)D.max_requests * D.n_groups * D.hot_pages_max, page_map(D, true), D.num_pages, epoch, cta, A.remap_ctas);
     }
-    if (A.idx.n > 0) remap_table(D.idx_bt, n, D.page_map + D.num_pages, D.num_idx_pages, epoch, cta, A.remap_ctas);
-    if (cta == 0 && threadIdx.x == 0) D.copy_epoch[0] = (uint32_t)epoch;
+    if (A.idx.n > 0) remap_table(D.idx_bt, n, page_map(D, false), D.num_idx_pages, epoch, cta, A.remap_ctas);
+    if (cta == 0 && threadIdx.x == 0) copy_epoch(D)[0] = (uint32_t)epoch;
     __threadfence();   // as the forks'
     return;
   }
   cta -= A.remap_ctas;
   const bool kv = cta < A.kv_ctas;
   const CopyList L = kv ? A.kv : A.idx;
-  const uint8_t* const ok = D.copy_ok + (kv ? 0 : HS_COPY_MAX_PAGES);
+  const uint8_t* const ok = copy_made_flags(D, kv);
   const int ctas = kv ? A.kv_ctas : gridDim.x - A.remap_ctas - A.kv_ctas;
   if (!kv) cta -= A.kv_ctas;
   const int lane = threadIdx.x & 31, slices = kv ? CP_KV_SLICES : CP_IDX_SLICES, per_page = (kv ? D.n_layers : D.n_groups) * slices;

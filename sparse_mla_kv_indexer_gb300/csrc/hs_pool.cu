@@ -14,6 +14,7 @@
 
 #include <nvtx3/nvToolsExt.h>
 
+#include "hs_pages.cuh"
 #include "hs_select.cuh"
 
 using namespace hs;
@@ -349,7 +350,7 @@ hs_status hs_pool_init(const hs_pool_config* cfg, void* const* d_kv_layers, void
   chk(dev_alloc(p, &D.tok2slot, R * G * c.max_ctx, 0xFF));
   chk(dev_alloc(p, &D.kv, (size_t)c.n_layers, 0));
   chk(dev_alloc(p, &D.idx, G, 0));
-  chk(dev_alloc(p, &D.status, 1, 0));
+  chk(dev_alloc(p, &D.status, page_state_words(c.num_pages, c.num_idx_pages), 0));
   chk(dev_alloc(p, &D.counters, (size_t)C_N, 0));
   chk(dev_alloc(p, &D.scores, (size_t)c.max_tokens * c.max_ctx, 0));
   chk(dev_alloc(p, &D.o_part, (size_t)c.max_tokens * MAX_SPLITS * 512 * 64, 0));
@@ -363,9 +364,6 @@ hs_status hs_pool_init(const hs_pool_config* cfg, void* const* d_kv_layers, void
     D.bsel_tokens = c.max_tokens < BS_MAX_TOKENS ? c.max_tokens : BS_MAX_TOKENS;
     chk(dev_alloc(p, &D.bsel, (size_t)D.bsel_tokens * sizeof(BselTok), 0));
   }
-  chk(dev_alloc(p, &D.page_map, (size_t)c.num_pages + c.num_idx_pages, 0));
-  chk(dev_alloc(p, &D.copy_ok, 2 * (size_t)HS_COPY_MAX_PAGES, 0));
-  chk(dev_alloc(p, &D.copy_epoch, 2, 0));
   if (s == HS_OK) {
     if (cudaMemcpy(D.kv, d_kv_layers, sizeof(void*) * c.n_layers, cudaMemcpyHostToDevice) != cudaSuccess ||
         cudaMemcpy(D.idx, d_idx_layers, sizeof(void*) * n_groups, cudaMemcpyHostToDevice) != cudaSuccess ||

@@ -28,6 +28,7 @@ constexpr int RO_SOME = 256;
 constexpr int RO_RESIDENT = 2;       // CTAs of as many threads on an SM, by their registers
 constexpr int RO_PARTS = HS_ROTARY_MAX_PARTS;
 constexpr int RO_MAX_PAIRS = HS_ROTARY_MAX_DIMS / 2;
+constexpr int RO_DECODE = 1024;       // most query tokens of a decode
 constexpr int RO_TABLE = 2048;       // (cos, sin) of a CTA's tokens, at most
 constexpr int RO_AHEAD = 3;          // units of a thread in flight
 
@@ -181,6 +182,9 @@ __global__ void __launch_bounds__(RO_THREADS, RO_RESIDENT) rotary_kernel(const _
       store_values(p[i].out + (p[i].halves ? A.pairs : V), y.b);
     }
   }
+  // The sparse attention reads its queries, of at most so many tokens, before it waits for this kernel's end
+  // (after which it starts).
+  if (A.n <= RO_DECODE) __threadfence();
 }
 
 // Whether 16-byte accesses reach every unit of V pairs of this part.
