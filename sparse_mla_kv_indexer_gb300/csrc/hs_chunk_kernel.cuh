@@ -1,5 +1,6 @@
 // Attention of a chunk of new tokens over the paged cache (prefill, the input of a later
-// turn, dense decode): every query token attends to every cached row below its limit.
+// turn, dense decode): every query token attends to every cached row below its limit. SHARED: of
+// requests that share their first positions (hs_prefix.cu), over the blocks that a kernel before has listed.
 //
 // "Serving GLM-5.3 with PCP, DCP and Hybrid HiSparse" (vLLM blog Part 2), footnote 1: QK
 // over 576 dims (512 latent, 64 rope), PV over the 512 latent dims, every row serving all

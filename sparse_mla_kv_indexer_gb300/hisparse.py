@@ -419,25 +419,18 @@ class Pool:
         [dims / 2] from rotary_steps, on the device; parts: (x, out, layout) with x and out [n, heads, dims]
         or [n, dims] of one type, views of the rotated dims with a contiguous last one, out x itself for
         in place; layout "pairs" or "halves". inverse turns backwards (the transpose)."""
-        if not 0 < len(parts) <= ROTARY_MAX_PARTS:
+        k = len(parts)
+        if not 0 < k <= ROTARY_MAX_PARTS:
             raise ValueError(f"1 to {ROTARY_MAX_PARTS} parts are wanted")
         first = parts[0][0]
         code, dtype, n, dev = _dtype(first), first.dtype, pos.shape[0], self._device()
         dims = first.shape[-1]
-        packed = bytearray(_ROTARY_PART.size * len(parts))
+        packed = bytearray(_ROTARY_PART.size * k)
         at = 0
         for x, out, layout in parts:
             shape, xs, os = x.shape, x.stride(), out.stride()
             if out.shape != shape or shape[0] != n or shape[-1] != dims:
                 raise ValueError(f"x and out [{n}, heads, {dims}] or [{n}, {dims}] of one shape are wanted")
-            if len(xs) == 3:
-                heads, xh, oh = shape[1], xs[1], os[1]
-                if heads == 1:
-                    xh = oh = dims
-            elif len(xs) == 2:
-                heads, xh, oh = 1, dims, dims
-            else:
-                raise ValueError(f"x and out [{n}, heads, {dims}] or [{n}, {dims}] are wanted")
             if x.dtype is not dtype or out.dtype is not dtype:
                 raise ValueError("all parts of one element type are wanted")
             if xs[-1] != 1 or os[-1] != 1:
@@ -446,20 +439,29 @@ class Pool:
                 raise ValueError(f"x or out is not on the pool's device, cuda:{dev}")
             if layout not in ROTARY_LAYOUTS:
                 raise ValueError(f"layout {layout!r}: pairs or halves is wanted")
+            if len(xs) == 3:
+                heads, xh, oh = shape[1], xs[1], os[1]
+                if heads == 1:
+                    xh = oh = dims
+            elif len(xs) == 2:
+                heads, xh, oh = 1, dims, dims
+            else:
+                raise ValueError(f"x and out [{n}, heads, {dims}] or [{n}, {dims}] are wanted")
             xt, ot = (xs[0], os[0]) if n > 1 else (dims, dims)
             _ROTARY_PART.pack_into(packed, at, x.data_ptr(), out.data_ptr(), xt, xh, ot, oh, heads, ROTARY_LAYOUTS[layout])
             at += _ROTARY_PART.size
         if steps.shape != (dims // 2,) or steps.dtype not in _Torch.steps or not steps.is_contiguous():
             raise ValueError(f"steps: a contiguous int64 tensor of {dims // 2} elements is wanted")
-        _on("steps", steps, dev)
+        if steps.get_device() != dev:
+            _on("steps", steps, dev)
         _check("hs_rotary", lib.hs_rotary(self.handle, n, _ids("pos", pos, n, dev), dims, steps.data_ptr(), magnitude,
-                                          1 if inverse else 0, code, len(parts), bytes(packed), _stream_of(stream, dev)))
+                                          1 if inverse else 0, code, k, bytes(packed), _stream_of(stream, dev)))
 
     def fork_requests(self, src, dst, length, tail_pages, tail_idx_pages=None, stream=None) -> None:
         """Begin requests dst[i] with the first length[i] positions of src[i]: whole pages shared, the rows of
         a last, partly filled page copied into tail_pages[i] and tail_idx_pages[i]. All [n] int32 on the device."""
-        n, dev = src.shape[0], self._device()
         _Torch.load_once()
+        n, dev = src.shape[0], self._device()
         _check("hs_fork_requests", lib.hs_fork_requests(
             self.handle, n, _ids("src", src, n, dev), _ids("dst", dst, n, dev), _ids("length", length, n, dev),
             _ids("tail_pages", tail_pages, n, dev),
@@ -473,11 +475,16 @@ class Pool:
             raise ValueError("sources and destinations: both or neither are wanted")
         dev = self._device()
         _Torch.load_once()
-        n, m = 0 if src is None else src.shape[0], 0 if idx_src is None else idx_src.shape[0]
-        ids = lambda name, t, k: None if t is None else _ids(name, t, k, dev)  # noqa: E731
-        _check("hs_copy_pages", lib.hs_copy_pages(
-            self.handle, n, ids("src", src, n), ids("dst", dst, n), m, ids("idx_src", idx_src, m), ids("idx_dst", idx_dst, m),
-            1 if remap else 0, _stream_of(stream, dev)))
+        n = m = 0
+        at = to = idx_at = idx_to = None
+        if src is not None:
+            n = src.shape[0]
+            at, to = _ids("src", src, n, dev), _ids("dst", dst, n, dev)
+        if idx_src is not None:
+            m = idx_src.shape[0]
+            idx_at, idx_to = _ids("idx_src", idx_src, m, dev), _ids("idx_dst", idx_dst, m, dev)
+        _check("hs_copy_pages", lib.hs_copy_pages(self.handle, n, at, to, m, idx_at, idx_to, 1 if remap else 0,
+                                                  _stream_of(stream, dev)))
 
     def prefix_workspace_bytes(self, n_tokens: int, n_segments: int, n_groups: int) -> int:
         """Bytes of device workspace that prefix_attention needs for a call of at most these sizes."""
@@ -499,20 +506,25 @@ class Pool:
     def get_pages(self, req, first_page: int, block_table=None, idx_pages=None, host_pages=None, stream=None) -> None:
         """Read table entries [first_page, first_page + n_pages) of requests req [n] into block_table and
         idx_pages (int32) and host_pages (int64), each [n, n_pages] on the device, any of them left out."""
-        outs = [t for t in (block_table, idx_pages, host_pages) if t is not None]
-        if not outs:
+        first = block_table if block_table is not None else idx_pages if idx_pages is not None else host_pages
+        if first is None:
             raise ValueError("none of block_table, idx_pages and host_pages is given")
-        n, dev = req.shape[0], self._device()
         _Torch.load_once()
-        for name, t, dtype in (("block_table", block_table, _Torch.int32), ("idx_pages", idx_pages, _Torch.int32),
-                               ("host_pages", host_pages, _Torch.int64)):
+        n, dev, shape = req.shape[0], self._device(), first.shape
+        if len(shape) != 2 or shape[0] != n:
+            raise ValueError(f"outputs [{n}, pages] are wanted")
+
+        def table(name, t, dtype):
             if t is None:
-                continue
-            if t.dim() != 2 or t.shape[0] != n or t.shape != outs[0].shape or t.dtype is not dtype or not t.is_contiguous():
+                return None
+            if t.shape != shape or t.dtype is not dtype or not t.is_contiguous():
                 raise ValueError(f"{name}: a contiguous {dtype} tensor [{n}, pages] is wanted, of one shape with the others")
-            _on(name, t, dev)
-        _check("hs_get_pages", lib.hs_get_pages(self.handle, n, _ids("req", req, n, dev), first_page, outs[0].shape[1],
-                                                _ptr(block_table), _ptr(idx_pages), _ptr(host_pages), _stream_of(stream, dev)))
+            if t.get_device() != dev:
+                _on(name, t, dev)
+            return t.data_ptr()
+        _check("hs_get_pages", lib.hs_get_pages(
+            self.handle, n, _ids("req", req, n, dev), first_page, shape[1], table("block_table", block_table, _Torch.int32),
+            table("idx_pages", idx_pages, _Torch.int32), table("host_pages", host_pages, _Torch.int64), _stream_of(stream, dev)))
 
     # -- status --------------------------------------------------------------------
     def get_error(self, stream=None) -> int:
