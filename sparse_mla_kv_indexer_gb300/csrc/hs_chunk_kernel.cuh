@@ -50,10 +50,12 @@
 // the measured bf16 rate; per tile of a pair 1.52 us, against 0.73 us of its products alone
 // (1,416 cycles: 36 of 25 for QK, which its shared-memory reads bound, and 8 of 64 for PV).
 // What bounds it is the work around them: 6,500 warp instructions per tile and SM (0.54 a
-// cycle and scheduler), two thirds of them the conversion of K and V, and 2,000 shared-memory
-// and L1 wavefronts besides the 1,246 of the products. With the conversions, the softmax or
-// the products cut short one at a time, a tile takes 7 to 14 % less; more converter warps
-// cost more instructions than they hide. How the roles' instructions interleave moves every long
+// cycle and scheduler), half of them the conversion of K and V, and 1,490 shared-memory wavefronts
+// besides the 1,246 of the products, in 2,990 cycles. With parts of it left out one at a time (8 x 129 tokens over
+// 20,001 rows, 3.40 ms): V's scaling 10 %, three of four loads of scales 7 %, three quarters of V's or K's stores
+// 5 and 4 %, four of five accumulator reads or the exchange of maxima nothing. More converter
+// warps cost more instructions than they hide: K and V on eight warps each 7 to 11 % more time, K one tile
+// ahead of V on the same warps 3 to 5 %. How the roles' instructions interleave moves every long
 // case by 1 to 3 % and the ragged one by up to 12 %, in either direction, for changes that do
 // nothing else (the order of two waits, a constant). One token over 131,072 rows takes 65 us (13 us
 // at the copy rate): 27 tiles a pair of 1.6 us, 12 us before the first and 5 us of merge.
