@@ -285,3 +285,20 @@ def test_tables_read_back_in_part():
             with pytest.raises(c.H.HisparseError):
                 c.pool.get_pages(i32([0]), first, torch.zeros(1, n, dtype=torch.int32, device="cuda"))
         c.pool.get_pages(i32([]), 0, torch.zeros(0, 3, dtype=torch.int32, device="cuda"))
+
+
+def test_a_fork_of_the_longest_context():
+    """Every table entry of a context as long as a pool takes, over several CTAs."""
+    from sparse_mla_kv_indexer_gb300 import hisparse as H
+    with Cache(n_layers=1, lpi=1, pages=(3, 1), max_ctx=H.MAX_CTX, host_pages=5) as c:
+        m = Model(c, 2)
+        rng = np.random.default_rng(3)
+        n = H.MAX_CTX // 64
+        m.set_pages(0, 0, bt=rng.integers(-1, c.n_pages, n).tolist(), ix=rng.integers(-1, c.n_pages, n).tolist(),
+                    hp=rng.integers(-1, 5, n).tolist())
+        tail, idx_tail = (s[0] for s in spare(c))
+        for length in (H.MAX_CTX, 64 * (n - 1), 64 * 1024, 64 * 1023):
+            c.pool.fork_requests(i32([0]), i32([1]), i32([length]), i32([tail]), i32([idx_tail]))
+            m.fork(0, 1, length, tail, idx_tail)
+            assert c.pool.get_error() == 0
+            m.check()

@@ -275,3 +275,54 @@ def test_refusals_and_empty_calls():
         for sizes in ((-1, 1, 1), (16385, 1, 1), (1, 4097, 1), (1, 1, 2049)):
             with pytest.raises(H.HisparseError):
                 c.pool.prefix_workspace_bytes(*sizes)
+
+
+@pytest.mark.parametrize("heads", [16, 32, 64])
+def test_the_smallest_calls(heads):
+    """One token alone, in a group, over one position; two tokens that share a page; empty groups; a workspace that is
+    larger than needed."""
+    with Shared(heads, [2], [64], [65, 70]) as s:
+        q = make_q(s.rng, 2, heads, "bf16")
+        work = torch.empty(c_bytes(s.c, 100), dtype=torch.uint8, device="cuda")
+        for groups, lens in (([0], []), ([0, 1], [64]), ([0, 0, 0], [64, 64]), ([1, 1], [0])):
+            out, lse = run(s.c, groups, lens, [1], [0, 1], [70], q[:1], work=work)
+            check_chunk(s.c, [s.kv[1]], [0], [0, 1], [70], q[:1], SM, out, lse, "bf16")
+            out, lse = run(s.c, groups, lens, [0], [0, 1], [1], q[:1], work=work)
+            check_chunk(s.c, [s.kv[0]], [0], [0, 1], [1], q[:1], SM, out, lse, "bf16")
+        for lens in ([64], [0], [70]):
+            out, lse = run(s.c, [0, 2], lens, [0, 1], [0, 1, 2], [65, 70], q, work=work)
+            assert s.c.pool.get_error() == 0
+            check_chunk(s.c, s.kv, [0, 1], [0, 1, 2], [65, 70], q, SM, out, lse, "bf16")
+
+
+def c_bytes(c, n):
+    return c.pool.prefix_workspace_bytes(n, n, n)
+
+
+def test_the_largest_call():
+    """As many tokens and segments as a call takes, in as many groups: more limits than the plan keeps in shared
+    memory, several rounds of everything."""
+    from sparse_mla_kv_indexer_gb300 import hisparse as H
+    n, segs, groups = H.PREFIX_MAX_TOKENS, H.CHUNK_MAX_SEGMENTS, H.PREFIX_MAX_GROUPS
+    with Cache(heads=16, n_layers=2, lpi=2, pages=(40, 3, 2), max_ctx=2560) as c:
+        rng = np.random.default_rng(0)
+        kv = []
+        for r, m in enumerate((2560, 192, 128)):
+            x = rng.standard_normal((m, 576))
+            rows = CP.pack_rows(x[:, :512], x[:, 512:])
+            c.put_rows(1, r, np.arange(m), rows)
+            kv.append(CP.row_values(rows))
+        # 2,000 single tokens behind 2,432 positions, pairs of short groups, one long segment behind them
+        req = np.r_[np.zeros(2000, int), np.repeat(rng.integers(0, 3, (segs - 2002) // 2), 2), 0, 0]
+        starts = np.r_[0, 2000, 2000 + 2 * np.arange(1, groups - 1)]
+        starts = np.minimum(np.r_[starts, segs], segs)
+        lens = np.r_[2432, rng.integers(0, 129, groups - 1)]
+        news = np.r_[np.ones(segs - 1, int), n - segs + 1]
+        start = np.r_[0, np.cumsum(news)]
+        top = np.array([2560, 192, 128])
+        limit = np.concatenate([rng.integers(0, top[r] + 1, m) for r, m in zip(req, news)])
+        q = make_q(rng, n, 16, "bf16")
+        out, lse = run(c, starts, lens, req, start, limit, q)
+        assert c.pool.get_error() == 0
+        some = set(rng.choice(n, 150, replace=False).tolist()) | {0, 1999, 2000, segs - 2, segs - 1, n - 1}
+        check_chunk(c, kv, req, start, limit, q, SM, out, lse, "bf16", some)
