@@ -8,7 +8,8 @@
 //
 // Measured on a GB300: 64 single tokens behind 32,768 shared rows, 64 heads, 369 us (hs_chunk_attention for the same
 // tokens 676 us), of which the plan 5, the attention 355 (223 tiles a pair of 1.48 us, 11 us before the first), the
-// join 10; 96 behind 131,009 rows, 16 heads, 551 us (3.93 ms). The products' floors are 154 and 229 us: what bounds it is the tile's work around them, as hs_chunk_kernel.cuh has it.
+// join 10; 96 behind 131,009 rows, 16 heads, 551 us (3.93 ms). The products' floors are 154 and 229 us: what bounds
+// it is the tile's work around them, as hs_chunk_kernel.cuh has it.
 #include "hs_chunk_kernel.cuh"
 
 namespace hs {
@@ -20,10 +21,13 @@ namespace {
 // segments they are of; the other pages are a unit per segment. Each unit is cut into blocks of 128 / H
 // tokens.
 // When it pays. Reading a group's shared pages once saves the tiles of (sum of ceil(t_i / tpb) - ceil(sum
-// t_i / tpb)) blocks over them (t_i: tokens of its segments, tpb: tokens of a block), and costs each of the
-// shared blocks its queries and its sums once more: PP_JOIN pages. A group that saves less, like long
-// segments of 64 heads whose blocks are full anyway, is read by each segment alone.
-constexpr int PP_JOIN = 8;
+// t_i / tpb)) blocks over them (t_i: tokens of its segments, tpb: tokens of a block). It costs each of the
+// shared blocks its start and queries, PP_START pages, and every row two partial sums that are written and read again,
+// PP_ROWS pages for 128 rows. A group that saves less, like long segments of 64 heads whose blocks are full anyway, is
+// read by each segment alone. Measured, shared against alone: 200 groups of two single tokens, 16 heads, 4 pages 99
+// and 97 us, 6 pages 110 and 116; 200 of four single tokens, 64 heads, 12 pages 325 and 302, 16 pages 357 and 374;
+// 100 of three times five tokens, 32 heads, 24 pages 400 and 382, 32 pages 466 and 491.
+constexpr int PP_START = 3, PP_ROWS = 11;
 constexpr int PP_LIMITS = 4096;    // limits of so many tokens are kept in shared memory
 constexpr int PP_FEW = 256;        // segments, groups and blocks of as many threads: 256 instead of 1,024
 // shared memory, in ints: segment starts [n_seg + 1], requests [n_seg] and shared pages [n_seg], group starts
@@ -140,8 +144,8 @@ __global__ void __launch_bounds__(THREADS, 1) prefix_plan_kernel(const Dev D, co
     alone = __reduce_add_sync(0xffffffffu, alone);
     first = __reduce_min_sync(0xffffffffu, first);
     valid = __all_sync(0xffffffffu, valid);
-    const int together = blocks_of(start[s1] - start[s0]), pages = fits && valid ? len / PAGE : 0;
-    const bool pays = (long long)(alone - together) * pages > (long long)together * PP_JOIN;
+    const int tokens = start[s1] - start[s0], together = blocks_of(tokens), pages = fits && valid ? len / PAGE : 0;
+    const bool pays = (long long)(alone - together) * pages > together * PP_START + (tokens * D.n_heads * PP_ROWS + CK_ROWS - 1) / CK_ROWS;
     if (lane == 0) reader[g] = first, before[g] = pays ? together : 0;
     if (pays)
       for (int i = s0 + lane; i < s1; i += 32) shared[i] = pages;

@@ -28,7 +28,7 @@ namespace hs {
 namespace {
 
 constexpr int RO_THREADS = 512;      // at most
-constexpr int RO_SOME = 256;
+constexpr int RO_SOME = 256;         // what a CTA of few rows is filled up to
 constexpr int RO_RESIDENT = 2;       // CTAs of as many threads on an SM, by their registers
 constexpr int RO_PARTS = HS_ROTARY_MAX_PARTS;
 constexpr int RO_MAX_PAIRS = HS_ROTARY_MAX_DIMS / 2;

@@ -201,7 +201,7 @@ def test_shared_pages_on_the_host_and_missing():
 def test_values_beyond_the_range():
     """A row that is not finite in the shared part, queries that are not, scores far below: reported, and not seen."""
     lengths = [200 + i for i in range(16)]
-    with Shared(16, [16], [128], lengths) as s:
+    with Shared(16, [16], [192], lengths) as s:
         c = s.c
         start, limit = layout([1] * 16, lengths)
         q = make_q(s.rng, 16, 16, "bf16")
@@ -220,23 +220,23 @@ def test_values_beyond_the_range():
         # every score of the shared part below the range, those behind it within: weights of the latter alone
         big = torch.zeros(16, 16, 576, dtype=torch.bfloat16, device="cuda")
         big[:, :, 575] = 60000.0
-        rows = c.get_rows(1, 0, np.arange(128))
+        rows = c.get_rows(1, 0, np.arange(192))
         rows[:, 654:656] = np.frombuffer(np.array([0xC2C8], "<u2").tobytes(), np.uint8)
-        c.put_rows(1, 0, np.arange(128), rows)                           # rope 63 of the shared rows: -100
+        c.put_rows(1, 0, np.arange(192), rows)                           # rope 63 of the shared rows: -100
         kv = []
         for r, n in enumerate(lengths):
-            mine = c.get_rows(1, r, np.arange(128, n))
+            mine = c.get_rows(1, r, np.arange(192, n))
             mine[:, 654:656] = 0
-            c.put_rows(1, r, np.arange(128, n), mine)
+            c.put_rows(1, r, np.arange(192, n), mine)
             kv.append(CP.row_values(mine))                               # the shared rows weigh nothing
         out, lse = run(c, s.group_start, s.group_len, range(16), start, limit, big, sm=1.0)
         assert c.pool.get_error() == 0
-        check_chunk(c, kv, range(16), start, limit - 128, big, 1.0, out, lse, "bf16")
+        check_chunk(c, kv, range(16), start, limit - 192, big, 1.0, out, lse, "bf16")
         # and of all of a token's parts: sees nothing, and is reported
         for r, n in enumerate(lengths):
-            mine = c.get_rows(1, r, np.arange(128, n))
+            mine = c.get_rows(1, r, np.arange(192, n))
             mine[:, 654:656] = np.frombuffer(np.array([0xC2C8], "<u2").tobytes(), np.uint8)
-            c.put_rows(1, r, np.arange(128, n), mine)
+            c.put_rows(1, r, np.arange(192, n), mine)
         out, lse = run(c, s.group_start, s.group_len, range(16), start, limit, big, sm=1.0)
         assert c.pool.get_error() == RANGE
         assert not out.any() and torch.all(torch.isneginf(lse))
