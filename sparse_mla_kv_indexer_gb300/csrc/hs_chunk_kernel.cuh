@@ -156,12 +156,12 @@ struct ChunkWork {
   float* part;       // [pairs][2][128][512]
 };
 constexpr int64_t CK_SLOT_ROWS = 2 * CK_ROWS;
-// Where four output dims (4 c4 .. + 3) of a row lie among its slot's, in 16 bytes: groups of eight rows, in them every
-// c4's rows of one CTA next to one another. A warp of the attention, which has every other row, then stores 64
-// contiguous bytes for four of its lanes (16 bytes of 32 rows' own lines took 6 us when all SMs wrote their cut blocks
-// at once, now 3), and the joins read four rows at a time.
+// Where four output dims (4 c4 .. + 3) of a row lie among its slot's, in 16 bytes: every c4's of four rows of one CTA
+// next to one another. A warp of the attention, which has every other row, then stores 64 contiguous bytes for four of
+// its lanes (16 bytes of 32 rows' own lines took 6 us when all SMs wrote their cut blocks at once, now 3), and the joins,
+// which take four rows at a time, read 8 KB in one run.
 __device__ __forceinline__ size_t part_unit(size_t row, int c4) {
-  return ((row >> 3) * 128 + c4) * 8 + (row & 1) * 4 + ((row >> 1) & 3);
+  return (((row >> 3) * 2 + (row & 1)) * 128 + c4) * 4 + ((row >> 1) & 3);
 }
 // The j-th row of four that are next to one another.
 __device__ __forceinline__ int quad_row(int four, int j) { return (four >> 1) * 8 + (four & 1) + 2 * j; }
@@ -1518,7 +1518,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
           tmem_wait_ld();
           if (live) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) dst[(c / 4 + j) * 8] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+            for (int j = 0; j < 4; ++j) dst[(c / 4 + j) * 4] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
           }
         }
         if (live && dim == 0) stats[at] = make_float2(m, l);

@@ -229,9 +229,9 @@ __global__ void __launch_bounds__(THREADS, 1) prefix_plan_kernel(const Dev D, co
 // another; WIDE (few rows, of many parts each) a quarter of their dims, the parts dealt to four slices of 128
 // threads. The CTAs go through the tasks in steps of the grid and look up 32 tokens at a time, for most may have
 // nothing to join.
-constexpr int PM_AHEAD = 6;   // parts whose loads are in flight
+constexpr int PM_AHEAD = 4;   // parts whose loads are in flight (51,200 rows of two parts 71 us; six and two CTAs on an SM 84)
 template <typename T, bool WIDE>
-__global__ void __launch_bounds__(CM_THREADS, 2) prefix_merge_kernel(const Dev D, const ChunkArgs A) {
+__global__ void __launch_bounds__(CM_THREADS, 3) prefix_merge_kernel(const Dev D, const ChunkArgs A) {
   __shared__ float4 acc[WIDE ? CM_SLICES : 1][128];
   __shared__ float2 ml[CM_SLICES][4];
   griddep_wait();
@@ -329,7 +329,7 @@ hs_status launch_prefix(hs_pool* p, const ChunkArgs& a, cudaStream_t st) {
   }
   if (s == HS_OK) s = launch_attention_pairs<T, true>(p, a, st);
   if (s != HS_OK) return s;
-  const int rows = a.n_tok * p->cfg.n_heads, most = 2 * num_sms();   // resident at once
+  const int rows = a.n_tok * p->cfg.n_heads, most = 3 * num_sms();   // resident at once
   const auto grid = [&](int tasks) { return dim3(tasks < most ? tasks : most); };
   if (rows <= PM_WIDE_ROWS)
     return launch_pdl(prefix_merge_kernel<T, true>, grid(rows), dim3(CM_THREADS), 0, st, 0, p->d, a);
