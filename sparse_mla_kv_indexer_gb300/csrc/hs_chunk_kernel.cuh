@@ -1016,8 +1016,9 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_attention_kernel(const De
       asm volatile("cp.async.wait_all;" ::: "memory");
       bool bad = false;
       q_first();
+      const int mine = (n_tok << hs) * 36;   // chunks of this CTA's rows that are a token's; the others are 0
 #pragma unroll 1
-      for (int k = 0; k < 18; k += 3) {
+      for (int k = 0; k * 256 < mine; k += 3) {
         uint32_t dst[3];
         uint4 v[3];
 #pragma unroll
