@@ -6,9 +6,9 @@
 // The rows S are converted to the products' operands once for 128 / H tokens of the group, instead of once for each
 // segment: of 96 single tokens with 16 heads an eighth of the tiles. With 64 heads two tokens fill a block.
 //
-// Measured on a GB300: 64 single tokens behind 32,768 shared rows, 64 heads, 369 us (hs_chunk_attention for the same
+// Measured on a GB300: 64 single tokens behind 32,768 shared rows, 64 heads, 370 us (hs_chunk_attention for the same
 // tokens 676 us), of which the plan 5, the attention 355 (223 tiles a pair of 1.48 us, 11 us before the first), the
-// join 10; 96 behind 131,009 rows, 16 heads, 551 us (3.93 ms). The products' floors are 154 and 229 us: what bounds
+// join 10; 96 behind 131,009 rows, 16 heads, 547 us (3.93 ms). The products' floors are 154 and 229 us: what bounds
 // it is the tile's work around them, as hs_chunk_kernel.cuh has it.
 #include "hs_chunk_kernel.cuh"
 
