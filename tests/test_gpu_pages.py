@@ -246,6 +246,31 @@ def test_copies_that_are_not_made():
             assert lib.hs_copy_pages(c.pool.handle, *a, 0, st) == INVALID, a
 
 
+@pytest.mark.parametrize("remap", [False, True])
+@pytest.mark.parametrize("n,n_idx", [(63, 1), (64, 64), (65, 64), (64, 65), (0, 64), (64, 0), (1, 66)])
+def test_copies_around_the_number_that_are_checked_beside_the_copying(n, n_idx, remap):
+    """Of both kinds, with a copy in each list that is not made: the last one has the first one's source as its destination."""
+    with Cache(n_layers=2, lpi=1, pages=(80, 3), spare=80) as c:
+        m = Model(c, 2)
+        m.set_pages(1, 0, bt=list(c.table[0][:2]))
+        for kind, k in (("kv", n), ("idx", n_idx)):
+            free = spare(c)[0 if kind == "kv" else 1]
+            src = np.random.default_rng(k).permutation((c.table if kind == "kv" else c.idx_table)[0])[:k]
+            dst = np.array(free)[:k]
+            made = np.ones(k, bool)
+            if k > 1:
+                dst[-1], made[-1] = src[0], False
+            if kind == "kv":
+                kv = (src, dst, made)
+            else:
+                idx = (src, dst, made)
+        c.pool.copy_pages(i32(kv[0]), i32(kv[1]), i32(idx[0]), i32(idx[1]), remap=remap)
+        for kind, (src, dst, made) in (("kv", kv), ("idx", idx)):
+            moved(m, kind, src[made], dst[made], remap)
+        assert c.pool.get_error() == BAD_ID
+        m.check()
+
+
 def test_a_moved_hot_page_keeps_its_rows():
     """A missed row lies in a hot buffer; after its page has moved, a replay finds it in the new place."""
     with Cache(pages=(8, 1), n_layers=2, lpi=2, spare=6, heads=16) as c:
