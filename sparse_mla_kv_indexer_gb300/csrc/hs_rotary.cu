@@ -16,9 +16,9 @@
 // sines of its tokens, once for all heads, into shared memory. A thread's unit is as many pairs as
 // two 16-byte loads hold: neighbours, or eight of either half of the dims (bf16).
 //
-// Bytes bound the large calls: 16,411 tokens of 130 heads (546 MB) take 91 us, 6.0 TB/s, where a plain contiguous
+// Bytes bound the large calls: 16,411 tokens of 130 heads (546 MB) take 94 us, 5.8 TB/s, where a plain contiguous
 // copy of as many bytes takes 90 us measured alike (80.6 us at the copy rate). With one, two and four units
-// of a thread in flight they take 100 to 121, 107 and 102 us. A decode's token is a launch: 3.3 us on the GPU.
+// of a thread in flight instead of three they took 9 to 30, 16 and 11 us more. A decode's token is a launch: 3.3 us on the GPU.
 #include <math.h>
 
 #include "hs_chunk.cuh"
@@ -32,7 +32,6 @@ constexpr int RO_SOME = 256;         // what a CTA of few rows is filled up to
 constexpr int RO_RESIDENT = 2;       // CTAs of as many threads on an SM, by their registers
 constexpr int RO_PARTS = HS_ROTARY_MAX_PARTS;
 constexpr int RO_MAX_PAIRS = HS_ROTARY_MAX_DIMS / 2;
-constexpr int RO_DECODE = 1024;       // most query tokens of a decode
 constexpr int RO_TABLE = 2048;       // (cos, sin) of a CTA's tokens, at most
 constexpr int RO_AHEAD = 3;          // units of a thread in flight
 
@@ -157,8 +156,7 @@ __global__ void __launch_bounds__(RO_THREADS, RO_RESIDENT) rotary_kernel(const _
     sines[i] = cs.y * A.magnitude * A.sign;
   }
   __syncthreads();
-  if (mine >= step) return;
-  for (int r0 = mine; r0 < all; r0 += RO_AHEAD * step) {
+  for (int r0 = mine < step ? mine : all; r0 < all; r0 += RO_AHEAD * step) {
     if (r0 != mine) {
 #pragma unroll
       for (int i = 0; i < RO_AHEAD; ++i)
@@ -186,9 +184,12 @@ __global__ void __launch_bounds__(RO_THREADS, RO_RESIDENT) rotary_kernel(const _
       store_values(p[i].out + (p[i].halves ? A.pairs : V), y.b);
     }
   }
-  // The sparse attention reads its queries, of at most so many tokens, before it waits for this kernel's end
-  // (after which it starts).
-  if (A.n <= RO_DECODE) __threadfence();
+  // The sparse attention and the indexer read their queries before they wait for this kernel's end (after which they
+  // start), and those may be any tokens of this call: the last of a prefill chunk, or of requests that decode beside
+  // it. So the CTA's stores are done when it ends. (16,411 tokens of 130 heads 90.8 us without this, 93.6 so, 98.0 with
+  // a fence by every thread.)
+  __syncthreads();
+  if (tid == 0) __threadfence();
 }
 
 // Whether 16-byte accesses reach every unit of V pairs of this part.
