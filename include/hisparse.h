@@ -500,9 +500,9 @@ hs_status hs_rotary(hs_pool* pool, int32_t n_tokens, const int32_t* d_pos, int32
  *                the last page's index keys and index page are left alone.
  * A request may be the source of several forks. A fork with a bad id, a length not in
  * [0, max_ctx], a destination that is named twice or is also a source, a tail page that is named
- * twice or is the source's own (for either cache), or a source page to copy from that is in
- * neither place (HS_ERR_HOST_MISSING; an index page: HS_ERR_BAD_ID) is not made at all, and sets
- * HS_ERR_BAD_ID or that. A last page whose source is a placeholder is copied from its host copy.
+ * twice or is the last, partly filled page of any fork's source in this call (for either cache),
+ * or a source page to copy from that is in neither place (HS_ERR_HOST_MISSING; an index page:
+ * HS_ERR_BAD_ID) is not made at all, and sets HS_ERR_BAD_ID or that. A last page whose source is a placeholder is copied from its host copy.
  * The caller empties dst_i's hot buffers first (hs_hot_release), keeps count of who uses a shared
  * page, and appends to positions from len_i on, which no shared page holds. */
 hs_status hs_fork_requests(hs_pool* pool, int32_t n, const int32_t* d_src, const int32_t* d_dst, const int32_t* d_len,

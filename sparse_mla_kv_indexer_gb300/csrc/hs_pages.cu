@@ -38,9 +38,16 @@ __global__ void __launch_bounds__(FK_THREADS) fork_kernel(const Dev D, const For
   const int whole = len >> 6, rows = len & 63;
   bool bad = false;
   for (int j = tid; j < A.n; j += FK_THREADS) {
-    const bool other = j != i, uses = rows && (A.len[j] & 63);
-    bad |= A.src[j] == dst || (other && A.dst[j] == dst);
-    bad |= other && uses && (A.tail[j] == tail || (A.idx_tail && A.idx_tail[j] == idx_tail));
+    const int from = A.src[j], n = A.len[j];
+    const bool other = j != i;
+    bad |= from == dst || (other && A.dst[j] == dst);
+    if (rows == 0 || (n & 63) == 0) continue;
+    bad |= other && (A.tail[j] == tail || (A.idx_tail && A.idx_tail[j] == idx_tail));
+    // a page that this call copies rows from is nobody's to write: its reader may come before or after
+    if (from >= 0 && from < D.max_requests && n > 0 && n <= D.max_ctx) {
+      const size_t at = (size_t)from * D.max_pages + (n >> 6);
+      bad |= D.bt[at] == tail || (A.idx_tail && D.idx_bt[at] == idx_tail);
+    }
   }
   if (src < 0 || src >= D.max_requests || dst < 0 || dst >= D.max_requests || len < 0 || len > D.max_ctx) bad = true;
   const uint8_t* page = nullptr;    // of the CTA's layer
@@ -49,10 +56,10 @@ __global__ void __launch_bounds__(FK_THREADS) fork_kernel(const Dev D, const For
   if (!bad && rows) {
     const size_t at = (size_t)src * D.max_pages + whole;
     page = page_rows(D, piece >= 0 && piece < D.n_layers ? piece : 0, src, whole, &err);
-    bad |= tail < 0 || tail >= D.num_pages || D.bt[at] == tail;
+    bad |= tail < 0 || tail >= D.num_pages;
     if (A.idx_tail) {
       from_idx = D.idx_bt[at];
-      bad |= idx_tail < 0 || idx_tail >= D.num_idx_pages || from_idx < 0 || from_idx >= D.num_idx_pages || from_idx == idx_tail;
+      bad |= idx_tail < 0 || idx_tail >= D.num_idx_pages || from_idx < 0 || from_idx >= D.num_idx_pages;
     }
     if (bad) err = HS_ERR_BAD_ID;
   }
