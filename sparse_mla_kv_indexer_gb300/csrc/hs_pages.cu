@@ -141,18 +141,27 @@ struct CopyArgs {
 // Every copy against all the others of its kind, a warp each, from shared memory: at most 4,096 x 8,192
 // comparisons of whole numbers over the whole GPU are less than building a table of the pages in every CTA was
 // (10 us for 2,500 pages; the search for an entry's page in it 20 us). With remap the copies that are made are
-// marked in the pool's array of pages, with a number of the call's own, so that nothing has to be cleared.
+// marked in the pool's array of pages, with a number of the call's own, so that nothing has to be cleared. The number
+// is taken here, by the last CTA that has read the one before: whether or not the copies are launched, no later call
+// has it again, and finds marks of its own alone.
 __global__ void __launch_bounds__(CP_THREADS) check_copies_kernel(const Dev D, const CopyArgs A) {
   extern __shared__ int32_t named[];
   griddep_wait();
   const bool kv = blockIdx.y == 0;
   const CopyList L = kv ? A.kv : A.idx;
-  const uint32_t epoch = copy_epoch(D)[0] + 1;   // of this call; the second launch keeps it
-  if (blockIdx.x == 0 && kv && threadIdx.x == 0) copy_epoch(D)[1] = epoch;
+  __shared__ uint32_t number;
+  if (A.remap && threadIdx.x == 0) {
+    uint32_t* const e = copy_epoch(D);
+    const uint32_t mine = __ldcg(e) + 1;
+    number = mine;
+    __threadfence();
+    if (atomicAdd(e + 1, 1) == gridDim.x * gridDim.y - 1) e[0] = mine, e[1] = 0;
+  }
   int32_t *const from = named, *const to = named + L.n;
   #pragma unroll 8
   for (int i = threadIdx.x; i < L.n; i += CP_THREADS) from[i] = L.from[i], to[i] = L.to[i];
   __syncthreads();
+  const int epoch = A.remap ? (int)number : 0;
   const int lane = threadIdx.x & 31;
   for (int i = blockIdx.x * CP_WARPS + (threadIdx.x >> 5); i < L.n; i += gridDim.x * CP_WARPS) {
     const int f = from[i], d = to[i];
@@ -171,7 +180,7 @@ __global__ void __launch_bounds__(CP_THREADS) check_copies_kernel(const Dev D, c
     if (lane == 0) {
       copy_made_flags(D, kv)[i] = ok;
       if (!ok) set_status(D.status, HS_ERR_BAD_ID);
-      else if (A.remap) page_map(D, kv)[f] = make_int2((int)epoch, d);
+      else if (A.remap) page_map(D, kv)[f] = make_int2(epoch, d);
     }
   }
 }
@@ -278,10 +287,9 @@ __global__ void __launch_bounds__(CP_THREADS, 2) copy_pages_kernel(const Dev D, 
         remap(kind == 0, FewPages{slots});
       }
     } else {
-      const int epoch = (int)copy_epoch(D)[1];
+      const int epoch = (int)copy_epoch(D)[0];
       if (A.kv.n > 0) remap(true, MarkedPages{page_map(D, true), D.num_pages, epoch});
       if (A.idx.n > 0) remap(false, MarkedPages{page_map(D, false), D.num_idx_pages, epoch});
-      if (cta == 0 && threadIdx.x == 0) copy_epoch(D)[0] = (uint32_t)epoch;
     }
     __threadfence();   // as the forks'
     return;

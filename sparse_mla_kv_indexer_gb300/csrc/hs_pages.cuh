@@ -5,8 +5,9 @@
 
 namespace hs {
 
-// int32 words: the status word; the numbers of the last call that is done and of the running one; which of the
-// call's copies of either kind are made; where each page of either kind went, and in the call of which number.
+// int32 words: the status word; the number of the last call that marked pages, and how many of the running one's CTAs
+// have read it; which of the call's copies of either kind are made; where each page of either kind went, and in the call
+// of which number.
 constexpr size_t PG_EPOCH = 2, PG_OK = 64, PG_MAP = PG_OK + 2 * HS_COPY_MAX_PAGES / 4;
 inline size_t page_state_words(int num_pages, int num_idx_pages) { return PG_MAP + 2 * ((size_t)num_pages + num_idx_pages); }
 
