@@ -452,8 +452,8 @@ typedef struct hs_rotary_config {
 
 /* The steps of hs_rotary for a scaling (h_steps [dims / 2]) and what rotated values are multiplied
  * by (1 but for RAMP); or the steps of n frequencies of the caller's own, in radians per position, at
- * most HS_ROTARY_MAX_FREQUENCY in magnitude. A step is the frequency in 2^-64 turns per position,
- * mod 2^64. Host arrays; no GPU needed. */
+ * most HS_ROTARY_MAX_FREQUENCY in magnitude. A step is the frequency, a double, in 2^-64 turns per
+ * position, to the nearest, mod 2^64. Host arrays; no GPU needed. */
 hs_status hs_rotary_steps(const hs_rotary_config* cfg, uint64_t* h_steps, float* h_magnitude);
 hs_status hs_rotary_steps_of(int32_t n, const double* h_frequencies, uint64_t* h_steps);
 
@@ -481,7 +481,7 @@ typedef struct hs_rotary_part {
  * in fp32, rounded once; inverse != 0 turns by -w (the transpose, and with magnitude 1 the inverse).
  *  d_pos    [n_tokens] int32, any value (negative ones turn backwards).
  *  d_steps  [dims / 2] from hs_rotary_steps, on the device, 8-byte aligned. The angle is exact to
- *           2^-33 turns for positions below 2^21, whatever the frequency.
+ *           2^-34 turns for every position, whatever the frequency (below 2^21 to 2^-44).
  *  dtype    of every part: HS_BF16, HS_FP16 or HS_FP32. Values that are not finite, or leave the
  *           type's range, become what the arithmetic makes of them, and are no error.
  *  parts    host array, taken by value. No part's output overlaps another part.

@@ -6,7 +6,7 @@
 //
 // Angles. In turns, p f / 2 pi mod 1 is p times a step of 2^-64 turns mod 2^64: whole numbers,
 // exact for every 32-bit position, where p f in fp32 is off by 0.08 radian at a million. The step
-// is f / 2 pi in double, off by 2^-54 turns, so the angle of position 2^20 by 2^-34. Of the phase
+// is f / 2 pi rounded to the nearest, so the angle is off by 2^-34 turns at most (position 2^31). Of the phase
 // the nearest quarter turn is taken off (by swapping and negating), and the rest, at most an
 // eighth of a turn, is exact to its own 24 bits before sincospif: cosines and sines are as good
 // near their zeros as at 0, and there is no table of positions to read.
@@ -229,11 +229,15 @@ hs_status launch_rotary(RotaryArgs& a, bool wide, cudaStream_t st) {
 }
 
 bool finite_positive(double x) { return x > 0 && isfinite(x); }
-// A frequency as whole 2^-64 turns per position, mod 2^64.
+// A frequency as whole 2^-64 turns per position, mod 2^64, to the nearest. 1 / (2 pi) is taken in two doubles (106 bits)
+// and the product's own rounding error added back, so that nothing of 163 turns, the largest, is lost: a quotient in
+// double is off by 2^-46 turns there, 2^-25 at position 2^21.
 uint64_t step_of(double radians) {
-  const double turns = radians / 6.283185307179586477, part = turns - floor(turns);   // [0, 1]
-  const double scaled = ldexp(part, 64);
-  return scaled >= 18446744073709551616.0 ? 0 : (uint64_t)scaled;
+  constexpr double inv = 0.15915494309189535, inv_rest = -9.839338337591243e-18;
+  const double x = fabs(radians), turns = x * inv, rest = fma(x, inv_rest, fma(x, inv, -turns));
+  const double scaled = ldexp(turns - floor(turns), 64), whole = floor(scaled);   // below 2^64
+  const uint64_t step = (uint64_t)whole + (uint64_t)llrint(scaled - whole + ldexp(rest, 64));
+  return radians < 0 ? 0 - step : step;
 }
 
 }  // namespace
