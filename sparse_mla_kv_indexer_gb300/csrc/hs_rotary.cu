@@ -8,8 +8,8 @@
 // exact for every 32-bit position, where p f in fp32 is off by 0.08 radian at a million. The step
 // is f / 2 pi rounded to the nearest, so the angle is off by 2^-34 turns at most (position 2^31). Of the phase
 // the nearest quarter turn is taken off (by swapping and negating), and the rest, at most an
-// eighth of a turn, is exact to its own 24 bits before sincospif: cosines and sines are as good
-// near their zeros as at 0, and there is no table of positions to read.
+// eighth of a turn, is rounded to its own 24 bits before sincospif: cosines and sines are as good
+// near their zeros, relative to themselves, as elsewhere, and there is no table of positions to read.
 //
 // Work. A CTA takes a few tokens and all of their heads (part of them when there are fewer tokens
 // than SMs): its threads begin with the loads of their first values, then work out the cosines and
@@ -50,10 +50,11 @@ struct RotaryArgs {
   RotaryPart part[RO_PARTS];
 };
 
-// cos and sin of `phase` 2^-64 turns.
+// cos and sin of `phase` 2^-64 turns. All 62 bits of what lies beside the nearest quarter are converted: of its upper 30
+// alone a phase of 2^-26 turns (a slow pair at an early position) keeps six bits.
 __device__ __forceinline__ float2 cos_sin(uint64_t phase) {
-  const uint32_t top = (uint32_t)(phase >> 32), quarter = (top + 0x20000000u) >> 30;
-  const float x = (float)(int32_t)(top - (quarter << 30)) * 4.656612873077393e-10f;   // 2^-31: in half turns
+  const uint32_t quarter = (uint32_t)((phase + (1ull << 61)) >> 62);
+  const float x = (float)(int64_t)(phase - ((uint64_t)quarter << 62)) * 1.0842021724855044e-19f;   // 2^-63: in half turns
   float s, c;
   sincospif(x, &s, &c);
   const float u = quarter & 1 ? s : c, v = quarter & 1 ? c : s;
