@@ -539,10 +539,11 @@ hs_status hs_prefix_workspace(const hs_pool* pool, int32_t n_tokens, int32_t n_s
 /* hs_chunk_attention for requests that share their first positions: group i is the segments
  * [d_group_start[i], d_group_start[i + 1]), whose requests hold the same rows at positions
  * [0, d_group_len[i]) (by sharing the pages, as after hs_fork_requests, or copies of them). The
- * whole pages of these are read through the table of the group's first segment, once for
- * 128 / H tokens of the group, whatever segments they are of; each segment reads the rest, up to its
- * tokens' limits, through its own request's table. The two parts of a token's sums are joined in
- * fp32. A group of one segment, and segments of no group, share nothing.
+ * whole pages of these are read through the table of the first of the group's segments that has
+ * tokens, once for 128 / H tokens of the group, whatever segments they are of; each segment reads the
+ * rest, up to its tokens' limits, through its own request's table. The two parts of a token's sums are
+ * joined in fp32. A group of one segment, one whose sharing would gain nothing, and segments of no group
+ * share nothing: each segment reads all of its rows through its own request's table.
  *  d_group_start  [n_groups + 1] int32, 0 <= start_0, ascending, the last at most n_segments.
  *  d_group_len    [n_groups] int32, 0 <= len <= max_ctx; tokens may have limits below it.
  *  A group start out of order or range is clamped, a length out of range counts as 0; both set
