@@ -24,9 +24,10 @@ namespace {
 // t_i / tpb)) blocks over them (t_i: tokens of its segments, tpb: tokens of a block). It costs each of the
 // shared blocks its start and queries, PP_START pages, and every row two partial sums that are written and read again,
 // PP_ROWS pages for 128 rows. A group that saves less, like long segments of 64 heads whose blocks are full anyway, is
-// read by each segment alone. Measured, shared against alone: 200 groups of two single tokens, 16 heads, 4 pages 99
-// and 97 us, 6 pages 110 and 116; 200 of four single tokens, 64 heads, 12 pages 325 and 302, 16 pages 357 and 374;
-// 100 of three times five tokens, 32 heads, 24 pages 400 and 382, 32 pages 466 and 491.
+// read by each segment alone. Measured, shared against alone, below the border and on it, where what is saved is
+// what it costs: 200 groups of two single tokens, 16 heads, 5 pages 86 and 84 us, 6 pages 88 and 94; 200 of four single
+// tokens, 64 heads, 13 pages 296 and 288, 14 pages 304 and 315; 100 of three times five tokens, 32 heads, 24 pages 363
+// and 362, 27 pages 390 and 401.
 constexpr int PP_START = 3, PP_ROWS = 11;
 constexpr int PP_LIMITS = 4096;    // limits of so many tokens are kept in shared memory
 constexpr int PP_FEW = 256;        // segments, groups and blocks of as many threads: 256 instead of 1,024
@@ -145,7 +146,7 @@ __global__ void __launch_bounds__(THREADS, 1) prefix_plan_kernel(const Dev D, co
     first = __reduce_min_sync(0xffffffffu, first);
     valid = __all_sync(0xffffffffu, valid);
     const int tokens = start[s1] - start[s0], together = blocks_of(tokens), pages = fits && valid ? len / PAGE : 0;
-    const bool pays = (long long)(alone - together) * pages > together * PP_START + (tokens * D.n_heads * PP_ROWS + CK_ROWS - 1) / CK_ROWS;
+    const bool pays = (long long)(alone - together) * pages >= together * PP_START + (tokens * D.n_heads * PP_ROWS + CK_ROWS - 1) / CK_ROWS;
     if (lane == 0) reader[g] = first, before[g] = pays ? together : 0;
     if (pays)
       for (int i = s0 + lane; i < s1; i += 32) shared[i] = pages;

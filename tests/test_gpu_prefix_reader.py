@@ -49,3 +49,16 @@ def test_ragged_groups_of_32_heads(dtype):
         again, l2 = run(s.c, s.group_start, s.group_len, range(len(lengths)), start, limit, q)
         assert s.c.pool.get_error() == 0 and torch.equal(out, again) and torch.equal(lse, l2)
         check_chunk(s.c, s.kv, range(len(lengths)), start, limit, q, SM, out, lse, dtype)
+
+
+@pytest.mark.parametrize("heads,k,pages", [(16, 2, (5, 6, 7)), (64, 4, (13, 14, 15)), (32, 12, (4, 5))])
+def test_groups_next_to_the_border_of_sharing(heads, k, pages):
+    """What is saved is a little less than what sharing costs, as much, and a little more."""
+    for p in pages:
+        lengths = [64 * p + 1 + (i * 37) % 90 for i in range(3 * k)]
+        with Shared(heads, [k] * 3, [64 * p] * 3, lengths, seed=p) as s:
+            start, limit = layout([1] * (3 * k), lengths)
+            q = make_q(s.rng, 3 * k, heads, "bf16")
+            out, lse = run(s.c, s.group_start, s.group_len, range(3 * k), start, limit, q)
+            assert s.c.pool.get_error() == 0
+            check_chunk(s.c, s.kv, range(3 * k), start, limit, q, SM, out, lse, "bf16")
