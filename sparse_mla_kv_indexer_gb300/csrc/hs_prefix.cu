@@ -30,7 +30,9 @@ namespace {
 // and 362, 27 pages 390 and 401.
 constexpr int PP_START = 3, PP_ROWS = 11;
 constexpr int PP_LIMITS = 4096;    // limits of so many tokens are kept in shared memory
-constexpr int PP_FEW = 256;        // segments, groups and blocks of as many threads: 256 instead of 1,024
+// The plan's threads: 256 for so many segments, groups and blocks, else 1,024. The whole call with either: of 7 blocks at
+// most 20.6 and 21.5 us, of 162 38.5 and 39.5, of 271 44.2 and 44.5, of 645 83.7 and 81.4, of 1,051 112 and 102.
+constexpr int PP_FEW = 256;
 // shared memory, in ints: segment starts [n_seg + 1], requests [n_seg] and shared pages [n_seg], group starts
 // [n_groups + 1], lengths [n_groups] and the segment through whose request each group reads [n_groups], blocks before
 // each unit [n_groups + n_seg + 1], limits
@@ -317,7 +319,11 @@ __global__ void __launch_bounds__(CM_THREADS, 3) prefix_merge_kernel(const Dev D
 
 int prefix_blocks(int n_tok, int n_seg, int n_groups, int tpb) { return n_seg + n_groups + 2 * (n_tok / tpb) + 1; }
 
-constexpr int PM_WIDE_ROWS = 1024;
+// Rows up to which a CTA of the join has a quarter of their dims and deals their parts to four slices. The whole call so
+// and with all dims and no slices: 128 rows behind 131,072 81 and 107 us, 256 rows 116 and 129, 768 rows 283 and 285, 1,024
+// rows 371 and 368; behind 8,192 (64 heads) 768 rows 42.6 and 44.0, 1,024 rows 50.2 and 47.8; behind 640 384 rows 27.7 and
+// 28.3, 768 rows 30.1 and 28.3, 1,024 rows 31.6 and 27.9.
+constexpr int PM_WIDE_ROWS = 768;
 template <typename T>
 hs_status launch_prefix(hs_pool* p, const ChunkArgs& a, cudaStream_t st) {
   const int smem = plan_ints(a.n_seg, a.n_groups, a.n_tok) * 4;

@@ -62,3 +62,16 @@ def test_groups_next_to_the_border_of_sharing(heads, k, pages):
             out, lse = run(s.c, s.group_start, s.group_len, range(3 * k), start, limit, q)
             assert s.c.pool.get_error() == 0
             check_chunk(s.c, s.kv, range(3 * k), start, limit, q, SM, out, lse, "bf16")
+
+
+@pytest.mark.parametrize("heads,tokens", [(64, 12), (64, 13), (16, 48), (16, 49), (16, 64), (16, 65)])
+def test_joins_next_to_the_border_of_rows(heads, tokens):
+    """Rows joined by slices and without, of parts of many pairs."""
+    lengths = [3000 + i for i in range(tokens)]
+    with Shared(heads, [tokens], [2944], lengths, seed=tokens) as s:
+        start, limit = layout([1] * tokens, lengths)
+        q = make_q(s.rng, tokens, heads, "bf16")
+        out, lse = run(s.c, s.group_start, s.group_len, range(tokens), start, limit, q)
+        again, l2 = run(s.c, s.group_start, s.group_len, range(tokens), start, limit, q)
+        assert s.c.pool.get_error() == 0 and torch.equal(out, again) and torch.equal(lse, l2)
+        check_chunk(s.c, s.kv, range(tokens), start, limit, q, SM, out, lse, "bf16", set(range(0, tokens, 5)) | {tokens - 1})
