@@ -54,8 +54,8 @@
  *   hot-buffer state are read before that wait, so they must be final before the
  *   previous kernel started. That holds for values written by the host (copies are
  *   stream-ordered), by this library's own calls (those that write them in a kernel,
- *   hs_rotary, hs_fork_requests and hs_copy_pages, let none start before they end) and
- *   by any ordinary kernel launch, which lets no dependent start before it ends; it
+ *   hs_rotary, hs_fork_requests and hs_copy_pages, let none start before they have
+ *   ended with these stores done, however large the call) and by any ordinary kernel launch, which lets no dependent start before it ends; it
  *   does not hold for a kernel that itself lets its dependents start early
  *   (griddepcontrol.launch_dependents) and writes them afterwards.
  * - A query-token batch is described by per-token device arrays: d_req (the

@@ -57,7 +57,7 @@
 // warps cost more instructions than they hide: K and V on eight warps each 7 to 11 % more time, K one tile
 // ahead of V on the same warps 3 to 5 %. How the roles' instructions interleave moves every long
 // case by 1 to 3 % and the ragged one by up to 12 %, in either direction, for changes that do
-// nothing else (the order of two waits, a constant). One token over 131,072 rows takes 65 us (13 us
+// nothing else (the order of two waits, a constant). One token over 131,072 rows takes 62 us (13 us
 // at the copy rate): 27 tiles a pair of 1.6 us, 12 us before the first and 5 us of merge.
 #pragma once
 
