@@ -301,7 +301,7 @@ def prepare(case, seed):
         return s
     # What a serving program keeps between its calls, and no pass makes again: the pool (0.1 to 0.4 ms) and the tables in
     # it. A request's pages are entered one by one, when the program's allocator hands them out; to enter all of them at
-    # once, as here, takes 0.04 to 28 ms (198,000 entries as Python numbers, 96 requests of 131,000 positions; 7.5 us for
+    # once, as here, takes 0.04 to 4 ms (198,000 entries as Python numbers, 96 requests of 131,000 positions; 6.7 us for
     # one entry). From here on the tables are the pool's: the passes read those, and not the tensors that they were
     # entered from, which forks and moves read them back into. The pages that a pass's own tokens begin are entered in it.
     from sparse_mla_kv_indexer_gb300 import hisparse as H
