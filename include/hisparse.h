@@ -55,8 +55,9 @@
  *   previous kernel started. That holds for values written by the host (copies are
  *   stream-ordered), by this library's own calls (those that write them in a kernel,
  *   hs_rotary, hs_fork_requests and hs_copy_pages, let none start before they have
- *   ended with these stores done, however large the call) and by any ordinary kernel launch, which lets no dependent start before it ends; it
- *   does not hold for a kernel that itself lets its dependents start early
+ *   ended with these stores done, however large the call) and by any ordinary kernel
+ *   launch, which lets no dependent start before it ends; it does not hold for a
+ *   kernel that itself lets its dependents start early
  *   (griddepcontrol.launch_dependents) and writes them afterwards.
  * - A query-token batch is described by per-token device arrays: d_req (the
  *   request slot of each token) and d_limit (causal limit: the token sees
@@ -502,7 +503,8 @@ hs_status hs_rotary(hs_pool* pool, int32_t n_tokens, const int32_t* d_pos, int32
  * [0, max_ctx], a destination that is named twice or is also a source, a tail page that is named
  * twice or is the last, partly filled page of any fork's source in this call (for either cache),
  * or a source page to copy from that is in neither place (HS_ERR_HOST_MISSING; an index page:
- * HS_ERR_BAD_ID) is not made at all, and sets HS_ERR_BAD_ID or that. A last page whose source is a placeholder is copied from its host copy.
+ * HS_ERR_BAD_ID) is not made at all, and sets HS_ERR_BAD_ID or that. A last page whose source is a
+ * placeholder is copied from its host copy.
  * The caller empties dst_i's hot buffers first (hs_hot_release), keeps count of who uses a shared
  * page, and appends to positions from len_i on, which no shared page holds. */
 hs_status hs_fork_requests(hs_pool* pool, int32_t n, const int32_t* d_src, const int32_t* d_dst, const int32_t* d_len,
